@@ -394,6 +394,111 @@ moe_status_t moe_lmhead_get_weights(moe_lmhead_t* head, void* codes_dev, float* 
 /* Free the head (synchronises the device first). NULL is accepted. */
 void moe_lmhead_destroy(moe_lmhead_t* head);
 
+/* ------------------------------------------------------------------------
+ * Routing to experts from given logits, and experts and projections in 8-bit
+ * integers. These calls keep no state: the caller passes every buffer, and the
+ * ones that need scratch say how much. Nothing allocates or synchronises; work is
+ * enqueued on `stream`. (The pages name no such interface; it is this library's own.)
+ * ------------------------------------------------------------------------ */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_S8 = 3 } moe_dtype_t;
+
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_ROUTE_MAX_EXPERTS 512
+#define MOE_ROUTE_MAX_TOP_K 32
+#define MOE_ROUTE_MAX_GROUPS 32
+
+typedef struct {
+  int32_t num_experts;   /* E: 1..MOE_ROUTE_MAX_EXPERTS, a multiple of groups                    */
+  int32_t top_k;         /* k: 1..min(MOE_ROUTE_MAX_TOP_K, top_groups * E / groups)              */
+  int32_t score;         /* MOE_SCORE_*                                                          */
+  int32_t groups;        /* consecutive experts form groups: 1..MOE_ROUTE_MAX_GROUPS             */
+  int32_t top_groups;    /* groups that stay, 1..groups                                          */
+  int32_t group_top;     /* keys added up for a group's score: 1 or 2                            */
+  int32_t renormalise;   /* nonzero: the k weights add up to scale                               */
+  float scale;           /* finite                                                               */
+} moe_route_config_t;
+
+/*
+ * For T rows of logits (logits_dtype F32, BF16 or F16; row t starts at element
+ * t * row_stride, row_stride >= E; any alignment of the element):
+ *   s = softmax(row) or 1 / (1 + exp(-row));  key = s + bias_dev (fp32 [E], NULL = 0)
+ *   the top_groups groups with the largest sums of their group_top largest keys stay
+ *   idx_dev int32 [T, k]    the k largest keys of these groups, descending
+ *   weights_dev fp32 [T, k] scale * s[idx], divided by the sum of the k scores if renormalise
+ * Equal keys, and equal groups, go by the lower index; keys that differ in real
+ * numbers are told apart however close they are, up to the rounding of 64 bits. A
+ * logit of -inf or NaN turns its expert off for the token: it ranks below all
+ * others, in order of index, with weight 0 (all weights are 0 where none is on);
+ * +inf counts as the largest finite fp32 value. T == 0 is a no-op.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (limits above), MOE_ERR_CUDA.
+ */
+moe_status_t moe_route_experts(const moe_route_config_t* cfg, const void* logits_dev, int32_t logits_dtype,
+                               int64_t row_stride, const float* bias_dev, int32_t T, int32_t* idx_dev,
+                               float* weights_dev, void* stream);
+
+/*
+ * The gradient of the logits from that of the weights: d_weights_dev fp32 [T, k]
+ * -> d_logits_dev [T, E] in the logits' type, without gaps, every element written.
+ * idx_dev are the choices of the forward call (distinct in a row; an index outside
+ * [0, E) has no weight and no gradient). The bias chooses only and has no gradient;
+ * experts that are off have gradient 0.
+ */
+moe_status_t moe_route_experts_backward(const moe_route_config_t* cfg, const void* logits_dev, int32_t logits_dtype,
+                                        int64_t row_stride, const int32_t* idx_dev, const float* d_weights_dev,
+                                        int32_t T, void* d_logits_dev, void* stream);
+
+/*
+ * Product in 8-bit integers with a scale for each token and channel:
+ *   out[t, n] = (sum_k q[t, k] * w[n, k]) * x_scale[t] * w_scale[n]
+ * x_dev [T, K]: S8 with x_scale_dev fp32 [T], or BF16 / F16 / F32 with x_scale_dev
+ * NULL. The latter is quantized by the call: x_scale[t] = amax_k |x[t, k]| / 127 in
+ * fp32 (1 for a row of zeros), q = x / x_scale to the nearest whole number, halves to
+ * the even one (of the real quotient). A row that holds an infinity or a NaN gives a
+ * row of NaN. w_dev S8 [N, K], w_scale_dev fp32 [N]; out_dev [T, N] BF16, F16 or F32
+ * without gaps, rounded once. Rows of x and w start x_stride and w_stride elements
+ * apart. K, the strides in bytes and the addresses of x and w are multiples of 16 (K
+ * else MOE_ERR_UNSUPPORTED); K <= MOE_INT8_MAX_K. T or N of 0 is a no-op. Integer sums are exact
+ * up to 2^24 in magnitude and rounded to 24 bits beyond that.
+ * workspace_dev: moe_quant_matmul_workspace() bytes, 256-byte aligned, free for reuse
+ * when the call's work on `stream` has finished (NULL where 0 bytes are needed).
+ */
+#define MOE_INT8_MAX_K 65536
+moe_status_t moe_quant_matmul_workspace(int32_t T, int32_t N, int32_t K, int32_t x_dtype, int64_t* bytes);
+moe_status_t moe_quant_matmul(const void* x_dev, int32_t x_dtype, int64_t x_stride, const float* x_scale_dev,
+                             const int8_t* w_dev, int64_t w_stride, const float* w_scale_dev, void* out_dev,
+                             int32_t out_dtype, int32_t T, int32_t N, int32_t K, void* workspace_dev,
+                             int64_t workspace_bytes, void* stream);
+
+/*
+ * SwiGLU experts in 8-bit integers, applied to the choices of a router:
+ *   q_t = x_t quantized as above;   [g | u] = (q_t . gate_up[e]) * x_scale[t] * gate_up_scale[e]
+ *   h = g / (1 + e^-g) * u, quantized the same way;   y_e = (q_h . down[e]) * h_scale * down_scale[e]
+ *   out[t] = sum_j weights[t, j] * y_{idx[t, j]}(x_t)
+ * x_dev, out_dev [T, H] in x_dtype (BF16 or F16), without gaps; idx_dev int32 [T, k] (a
+ * choice outside [0, E) contributes nothing; a row without a choice is 0), weights_dev
+ * fp32 [T, k]; gate_up_dev S8 [E, 2I, H], the I gate rows before the I up rows, and
+ * gate_up_scale_dev fp32 [E, 2I]; down_dev S8 [E, H, I] and down_scale_dev fp32 [E, H].
+ * A shared expert of the same size is one more expert that every token chooses with
+ * weight 1. H and I are multiples of 16 (else MOE_ERR_UNSUPPORTED), H <= 16384,
+ * I <= 16384, k <= MOE_ROUTE_MAX_TOP_K, E <= MOE_INT8_MAX_EXPERTS; x, out, gate_up and down are 16-byte aligned; out does
+ * not overlap x. workspace as in moe_quant_matmul.
+ */
+#define MOE_INT8_MAX_EXPERTS 1024
+typedef struct {
+  int32_t num_experts, top_k, hidden, intermediate;
+} moe_int8_experts_config_t;
+typedef struct {
+  const int8_t* gate_up_dev;
+  const float* gate_up_scale_dev;
+  const int8_t* down_dev;
+  const float* down_scale_dev;
+} moe_int8_experts_weights_t;
+moe_status_t moe_quant_experts_workspace(const moe_int8_experts_config_t* cfg, int32_t T, int64_t* bytes);
+moe_status_t moe_quant_experts(const moe_int8_experts_config_t* cfg, const moe_int8_experts_weights_t* w,
+                              const void* x_dev, int32_t x_dtype, const int32_t* idx_dev, const float* weights_dev,
+                              void* out_dev, int32_t T, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
 /* Name of a status code (static string). */
 const char* moe_status_string(moe_status_t status);
 

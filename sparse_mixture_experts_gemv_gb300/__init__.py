@@ -9,3 +9,5 @@ from ._native import *  # noqa: F401,F403  (C names: moe_layer_create, moe_layer
 from ._native import load  # noqa: F401
 from .layer import MoeLayer, weights_from_raw  # noqa: F401
 from .lmhead import LmHead  # noqa: F401
+from .routing import route_experts, route_experts_backward  # noqa: F401
+from .int8 import int8_experts, int8_matmul  # noqa: F401

@@ -31,6 +31,18 @@ MOE_FLAG_TEST_FORCE_WAIT_TIMEOUT = 0x100
 MOE_DECODE_MAX_T = 8
 MOE_GROUPED_BLOCK_ROWS = 128
 
+MOE_DTYPE_F32 = 0
+MOE_DTYPE_BF16 = 1
+MOE_DTYPE_F16 = 2
+MOE_DTYPE_S8 = 3
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_ROUTE_MAX_EXPERTS = 512
+MOE_ROUTE_MAX_TOP_K = 32
+MOE_ROUTE_MAX_GROUPS = 32
+MOE_INT8_MAX_K = 65536
+MOE_INT8_MAX_EXPERTS = 1024
+
 MOE_PATH_NONE = 0
 MOE_PATH_DECODE_GEMV = 1
 MOE_PATH_GROUPED = 2
@@ -53,6 +65,19 @@ class moe_stats_t(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int32), ("tokens", ctypes.c_int32), ("distinct_experts", ctypes.c_int32),
                 ("max_expert_rows", ctypes.c_int32), ("weight_bytes", ctypes.c_int64),
                 ("algorithmic_bytes", ctypes.c_int64), ("flops", ctypes.c_double)]
+
+
+class moe_route_config_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_experts", "top_k", "score", "groups", "top_groups", "group_top",
+                                              "renormalise")] + [("scale", ctypes.c_float)]
+
+
+class moe_int8_experts_config_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_experts", "top_k", "hidden", "intermediate")]
+
+
+class moe_int8_experts_weights_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate_up_dev", "gate_up_scale_dev", "down_dev", "down_scale_dev")]
 
 
 class MoeError(RuntimeError):
@@ -99,6 +124,22 @@ _SIGNATURES = {
                                           ctypes.c_void_p]),
     "moe_lmhead_get_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "moe_lmhead_destroy": (None, [ctypes.c_void_p]),
+    "moe_route_experts": (ctypes.c_int, [ctypes.POINTER(moe_route_config_t), ctypes.c_void_p, ctypes.c_int32,
+                                         ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_route_experts_backward": (ctypes.c_int, [ctypes.POINTER(moe_route_config_t), ctypes.c_void_p,
+                                                  ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                                  ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_quant_matmul_workspace": (ctypes.c_int, [ctypes.c_int32] * 4 + [ctypes.POINTER(ctypes.c_int64)]),
+    "moe_quant_matmul": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p] +
+                        [ctypes.c_int32] * 4 + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "moe_quant_experts_workspace": (ctypes.c_int, [ctypes.POINTER(moe_int8_experts_config_t), ctypes.c_int32,
+                                                  ctypes.POINTER(ctypes.c_int64)]),
+    "moe_quant_experts": (ctypes.c_int, [ctypes.POINTER(moe_int8_experts_config_t),
+                                        ctypes.POINTER(moe_int8_experts_weights_t), ctypes.c_void_p, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_cuda_error": (ctypes.c_char_p, []),
 }

@@ -1,0 +1,40 @@
+"""What the calls on torch tensors share: streams, dtype codes, argument errors."""
+from __future__ import annotations
+
+import torch
+
+from . import _native as N
+
+DTYPE_CODES = {torch.float32: N.MOE_DTYPE_F32, torch.bfloat16: N.MOE_DTYPE_BF16, torch.float16: N.MOE_DTYPE_F16,
+               torch.int8: N.MOE_DTYPE_S8}
+
+
+def invalid(what: str, why: str):
+    raise ValueError(f"{what}: {why}")
+
+
+def want(cond: bool, what: str, why: str):
+    if not cond:
+        invalid(what, why)
+
+
+def check(status: int, what: str):
+    if status != N.MOE_OK:
+        raise N.MoeError(status, what)
+
+
+def vector(t, name, n, what, device, dtype=torch.float32):
+    """A 1-D tensor of n values without gaps on the device."""
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or t.device != device:
+        invalid(what, f"{name} must be {dtype} [{n}] on {device}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def raw_stream(stream, device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+
+
+def run_on(stream, fn, *args, **kw):
+    """fn(*args) with `stream` as the current one, so that what it allocates belongs to that stream."""
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)

@@ -1,0 +1,128 @@
+// Device helpers of the 8-bit integer operators: loads by type, the quantization
+// of a row, the stores of results.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_common.cuh"
+#include "moe_layer.h"
+
+namespace moe {
+namespace int8 {
+
+// 16 consecutive elements (16-byte aligned) as fp32.
+template <int DT>
+MOE_DEV void load16(const void* p, int64_t i, float (&v)[16]) {
+  if constexpr (DT == MOE_DTYPE_F32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 f = __ldg(q + c);
+      v[4 * c] = f.x; v[4 * c + 1] = f.y; v[4 * c + 2] = f.z; v[4 * c + 3] = f.w;
+    }
+  } else {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint4 u = __ldg(q + c);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (DT == MOE_DTYPE_BF16) {
+          v[8 * c + 2 * j] = bf16_lo(w[j]);
+          v[8 * c + 2 * j + 1] = bf16_hi(w[j]);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          v[8 * c + 2 * j] = f.x;
+          v[8 * c + 2 * j + 1] = f.y;
+        }
+      }
+    }
+  }
+}
+// The same for fp32 written earlier in this call (by a kernel this one may overlap).
+MOE_DEV void load16_cg(const float* p, float (&v)[16]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint4 u = ldg_cg(p + 4 * c);
+    v[4 * c] = __uint_as_float(u.x); v[4 * c + 1] = __uint_as_float(u.y);
+    v[4 * c + 2] = __uint_as_float(u.z); v[4 * c + 3] = __uint_as_float(u.w);
+  }
+}
+
+// max of the bit patterns of |v|: an infinity or a NaN stays above every finite
+// value, so that a row's largest pattern also says whether the row is finite.
+MOE_DEV uint32_t amax_bits(const float (&v)[16]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return a;
+}
+
+// How a row is quantized, from amax_bits over it: the scale, its reciprocal, and
+// whether the quotients need the division (scale below the normal range's middle,
+// where the reciprocal overflows or loses bits).
+struct RowScale {
+  float scale, inv;
+};
+MOE_DEV RowScale row_scale(uint32_t bits) {
+  RowScale r;
+  const float amax = __uint_as_float(bits);
+  if (bits >= 0x7F800000u) r.scale = __uint_as_float(0x7FC00000u);   // NaN: the whole row
+  else r.scale = bits ? amax / 127.f : 1.f;
+  r.inv = r.scale >= 0x1p-100f ? 1.f / r.scale : 0.f;   // 0: divide (also for NaN)
+  return r;
+}
+
+// x / scale to the nearest whole number, halves to the even one, decided on the real
+// quotient: a row's half of the largest value is a tie but for the scale's rounding.
+// The product with the reciprocal is off by less than 1e-4, so its rounding is at
+// most one off, which the exact remainder x - q * scale tells (one rounding, far
+// below what it is compared with).
+MOE_DEV int quantize(float x, const RowScale r) {
+  float q;
+  if (r.inv != 0.f) {
+    q = rintf(x * r.inv);
+    const float d = fmaf(-q, r.scale, x), half = 0.5f * r.scale;
+    const bool odd = (int)q & 1;
+    if (d > half || (d == half && odd)) q += 1.f;
+    else if (d < -half || (d == -half && odd)) q -= 1.f;
+  } else {
+    q = r.scale > 0.f ? rintf(x / r.scale) : 0.f;   // 0 for a scale that underflowed, and for NaN
+  }
+  return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+MOE_DEV uint32_t pack4(int a, int b, int c, int d) {
+  return (uint32_t)(a & 0xFF) | ((uint32_t)(b & 0xFF) << 8) | ((uint32_t)(c & 0xFF) << 16) | ((uint32_t)d << 24);
+}
+MOE_DEV uint4 quantize16(const float (&v)[16], const RowScale r) {
+  uint4 o;
+  o.x = pack4(quantize(v[0], r), quantize(v[1], r), quantize(v[2], r), quantize(v[3], r));
+  o.y = pack4(quantize(v[4], r), quantize(v[5], r), quantize(v[6], r), quantize(v[7], r));
+  o.z = pack4(quantize(v[8], r), quantize(v[9], r), quantize(v[10], r), quantize(v[11], r));
+  o.w = pack4(quantize(v[12], r), quantize(v[13], r), quantize(v[14], r), quantize(v[15], r));
+  return o;
+}
+
+MOE_DEV int dot16(const uint4 w, const uint4 x, int acc) {
+  acc = __dp4a((int)w.x, (int)x.x, acc);
+  acc = __dp4a((int)w.y, (int)x.y, acc);
+  acc = __dp4a((int)w.z, (int)x.z, acc);
+  return __dp4a((int)w.w, (int)x.w, acc);
+}
+
+// One value, rounded to nearest even (a NaN stays one).
+MOE_DEV uint16_t to_16(int dtype, float f) {
+  if (dtype == MOE_DTYPE_F16) return __half_as_ushort(__float2half_rn(f));
+  return isnan(f) ? (uint16_t)0x7FC0u : f32_to_bf16_rne(f);
+}
+MOE_DEV void store(void* out, int dtype, int64_t i, float f) {
+  if (dtype == MOE_DTYPE_F32) static_cast<float*>(out)[i] = f;
+  else static_cast<uint16_t*>(out)[i] = to_16(dtype, f);
+}
+
+}  // namespace int8
+}  // namespace moe

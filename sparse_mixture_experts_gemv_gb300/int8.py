@@ -1,0 +1,128 @@
+"""Projections and SwiGLU experts in 8-bit integers (moe_quant_* in the C ABI), with a
+scale for each token and channel. Argument checks and marshalling only."""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from . import _native as N
+from ._tensors import DTYPE_CODES, check, invalid, raw_stream, run_on, vector, want
+
+
+@functools.lru_cache(maxsize=256)
+def _matmul_workspace(T, n, K, code):
+    b = ctypes.c_int64()
+    check(N.load().moe_quant_matmul_workspace(T, n, K, code, ctypes.byref(b)), "moe_quant_matmul_workspace")
+    return b.value
+
+
+@functools.lru_cache(maxsize=256)
+def _experts_config(E, k, H, I, T):
+    cfg = N.moe_int8_experts_config_t(E, k, H, I)
+    b = ctypes.c_int64()
+    check(N.load().moe_quant_experts_workspace(ctypes.byref(cfg), T, ctypes.byref(b)), "moe_quant_experts_workspace")
+    return ctypes.byref(cfg), b.value
+
+
+def _rows(t, what, name):
+    """A matrix whose rows the kernels can read: 16-byte addresses and row strides."""
+    size = t.element_size()
+    if t.stride(1) != 1 or t.stride(0) < t.shape[1] or t.stride(0) * size % 16 or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+        want(t.shape[1] * size % 16 == 0, what, f"the rows of {name} must be a multiple of 16 bytes long")
+    return t
+
+
+def int8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale: torch.Tensor = None,
+                out_dtype: torch.dtype = None, stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """out[t, n] = (sum_k q[t, k] w[n, k]) x_scale[t] w_scale[n].
+
+    w: int8 [N, K], w_scale: fp32 [N]. x [T, K]: int8 with x_scale fp32 [T], or bf16, fp16 or
+    fp32 without: each row is then quantized by the call to its largest magnitude / 127, to
+    the nearest whole number (a row with an infinity or a NaN gives NaN). K is a multiple of
+    16. Rows may be apart (any stride(0)); rows off 16-byte boundaries are copied first.
+    out_dtype: bf16, fp16 or fp32; by default x's, and bf16 for int8 x.
+    """
+    if stream is not None:
+        return run_on(stream, int8_matmul, x, w, w_scale, x_scale, out_dtype)
+    what = "int8_matmul"
+    if not x.is_cuda or x.dim() != 2 or x.dtype not in DTYPE_CODES:
+        invalid(what, "x must be a CUDA tensor [T, K] of int8, bf16, fp16 or fp32")
+    T, K = x.shape
+    dev = x.device
+    if w.dim() != 2 or w.dtype is not torch.int8 or w.shape[1] != K or w.device != dev:
+        invalid(what, f"w must be int8 [N, {K}] on {dev}")
+    n = w.shape[0]
+    w_scale = vector(w_scale, "w_scale", n, what, dev)
+    quantized = x.dtype is torch.int8
+    if quantized != (x_scale is not None):
+        invalid(what, "x_scale goes with int8 x, and with no other")
+    if quantized:
+        x_scale = vector(x_scale, "x_scale", T, what, dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if quantized else x.dtype
+    if out_dtype not in DTYPE_CODES or out_dtype is torch.int8:
+        invalid(what, "out_dtype must be bf16, fp16 or fp32")
+    out = torch.empty((T, n), dtype=out_dtype, device=dev)
+    if T == 0 or n == 0:
+        return out
+    x, w = _rows(x, what, "x"), _rows(w, what, "w")
+    code = DTYPE_CODES[x.dtype]
+    need = _matmul_workspace(T, n, K, code)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    check(N.load().moe_quant_matmul(x.data_ptr(), code, x.stride(0), None if x_scale is None else x_scale.data_ptr(),
+                                   w.data_ptr(), w.stride(0), w_scale.data_ptr(), out.data_ptr(),
+                                   DTYPE_CODES[out_dtype], T, n, K, None if ws is None else ws.data_ptr(), need,
+                                   raw_stream(None, dev)), "moe_quant_matmul")
+    return out
+
+
+def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate_up: torch.Tensor,
+                 gate_up_scale: torch.Tensor, down: torch.Tensor, down_scale: torch.Tensor,
+                 stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * expert[idx[t, j]](x[t]) with SwiGLU experts in int8.
+
+    x: bf16 or fp16 [T, H]. idx int32, weights fp32 [T, k], as route_experts gives them; a
+    choice outside [0, E) contributes nothing. gate_up: int8 [E, 2I, H], gate rows before up
+    rows, gate_up_scale fp32 [E, 2I]; down: int8 [E, H, I], down_scale fp32 [E, H]. x and the
+    SwiGLU outputs are quantized for each token as in int8_matmul. Returns [T, H] in x's type.
+    """
+    if stream is not None:
+        return run_on(stream, int8_experts, x, idx, weights, gate_up, gate_up_scale, down, down_scale)
+    what = "int8_experts"
+    if not x.is_cuda or x.dim() != 2 or (x.dtype is not torch.bfloat16 and x.dtype is not torch.float16):
+        invalid(what, "x must be a CUDA tensor [T, H] of bf16 or fp16")
+    T, H = x.shape
+    dev = x.device
+    if idx.dim() != 2 or idx.shape[0] != T or idx.dtype is not torch.int32 or idx.device != dev:
+        invalid(what, f"idx must be int32 [{T}, k] on {dev}")
+    k = idx.shape[1]
+    if weights.shape != idx.shape or weights.dtype is not torch.float32 or weights.device != dev:
+        invalid(what, f"weights must be fp32 [{T}, {k}] on {dev}")
+    if gate_up.dim() != 3 or gate_up.shape[2] != H or gate_up.shape[1] % 2 or gate_up.dtype is not torch.int8:
+        invalid(what, f"gate_up must be int8 [E, 2I, {H}]")
+    E, I = gate_up.shape[0], gate_up.shape[1] // 2
+    if down.shape != (E, H, I) or down.dtype is not torch.int8:
+        invalid(what, f"down must be int8 [{E}, {H}, {I}]")
+    for name, t, shape in (("gate_up_scale", gate_up_scale, (E, 2 * I)), ("down_scale", down_scale, (E, H))):
+        if t.shape != shape or t.dtype is not torch.float32:
+            invalid(what, f"{name} must be fp32 {list(shape)}")
+    for name, t in (("gate_up", gate_up), ("gate_up_scale", gate_up_scale), ("down", down), ("down_scale", down_scale)):
+        if t.device != dev or not t.is_contiguous():
+            invalid(what, f"{name} must be on {dev} and without gaps")
+    x, idx, weights = x.contiguous(), idx.contiguous(), weights.contiguous()
+    if x.data_ptr() % 16:
+        x = x.clone()
+    out = torch.empty((T, H), dtype=x.dtype, device=dev)
+    if T == 0:
+        return out
+    cfg, need = _experts_config(E, k, H, I, T)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    w = N.moe_int8_experts_weights_t(gate_up.data_ptr(), gate_up_scale.data_ptr(), down.data_ptr(),
+                                     down_scale.data_ptr())
+    check(N.load().moe_quant_experts(cfg, ctypes.byref(w), x.data_ptr(), DTYPE_CODES[x.dtype], idx.data_ptr(),
+                                    weights.data_ptr(), out.data_ptr(), T, ws.data_ptr(), need,
+                                    raw_stream(None, dev)), "moe_quant_experts")
+    return out

@@ -1,0 +1,109 @@
+"""Routing to experts from given logits (moe_route_experts in the C ABI): softmax or
+sigmoid scores, a bias that only chooses, groups of experts, top-k, renormalised
+weights, and the gradient of the logits. Argument checks and marshalling only."""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from . import _native as N
+from ._tensors import DTYPE_CODES, check, invalid, raw_stream, run_on, vector, want
+
+SCORES = {"softmax": N.MOE_SCORE_SOFTMAX, "sigmoid": N.MOE_SCORE_SIGMOID}
+
+
+@functools.lru_cache(maxsize=256)
+def _config(E, k, score, groups, top_groups, group_top, renormalise, scale):
+    if score not in SCORES:
+        invalid("route_experts", f"score must be one of {sorted(SCORES)}")
+    return ctypes.byref(N.moe_route_config_t(E, k, SCORES[score], groups, top_groups, group_top,
+                                             1 if renormalise else 0, scale))
+
+
+def _logits(what, logits):
+    if not logits.is_cuda or logits.dim() != 2 or logits.dtype not in DTYPE_CODES or logits.dtype is torch.int8:
+        invalid(what, "logits must be a CUDA tensor [T, E] of fp32, bf16 or fp16")
+    if logits.stride(1) != 1 or logits.stride(0) < logits.shape[1]:
+        logits = logits.contiguous()
+    return logits
+
+
+def _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise, scale):
+    logits = _logits("route_experts", logits)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        bias = vector(bias.detach(), "bias", E, "route_experts", dev)
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    check(N.load().moe_route_experts(_config(E, k, score, groups, top_groups, group_top, renormalise, scale),
+                                     logits.data_ptr(), DTYPE_CODES[logits.dtype], logits.stride(0) if T > 1 else E,
+                                     None if bias is None else bias.data_ptr(), T, idx.data_ptr(), weights.data_ptr(),
+                                     raw_stream(None, dev)), "moe_route_experts")
+    return idx, weights
+
+
+class _RouteExperts(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, score, bias, groups, top_groups, group_top, renormalise, scale):
+        idx, weights = _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise, scale)
+        ctx.save_for_backward(logits, idx)
+        ctx.how = (score, renormalise, scale)
+        ctx.mark_non_differentiable(idx)
+        return idx, weights
+
+    @staticmethod
+    def backward(ctx, _, d_weights):
+        logits, idx = ctx.saved_tensors
+        d_logits = route_experts_backward(d_weights, logits, idx, *ctx.how)
+        return (d_logits,) + (None,) * 8
+
+
+def route_experts(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tensor = None, groups: int = 1,
+                  top_groups: int = None, group_top: int = 2, renormalise: bool = True, scale: float = 1.0,
+                  stream: torch.cuda.Stream = None):
+    """Chooses k experts for each row of logits [T, E] (fp32, bf16 or fp16).
+
+    score: "softmax" or "sigmoid". bias: fp32 [E], added to the scores for the choice alone
+    (a bias for balance). groups > 1: consecutive experts form groups; the top_groups groups
+    whose group_top (1 or 2) largest keys add up to most stay. The weights are the scores
+    without the bias, divided by their sum if renormalise, times scale. Equal keys go by the
+    lower index; a logit of -inf or NaN turns its expert off for the row.
+
+    Returns (idx int32 [T, k], weights fp32 [T, k]), in descending order of the keys. The
+    weights are differentiable with respect to the logits.
+    """
+    if top_groups is None:
+        top_groups = groups
+    args = (logits, k, score, bias, groups, top_groups, group_top, renormalise, scale)
+    if stream is not None:
+        return run_on(stream, route_experts, *args)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _RouteExperts.apply(*args)
+    return _forward(*args)
+
+
+def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, idx: torch.Tensor, score: str = "softmax",
+                           renormalise: bool = True, scale: float = 1.0, stream: torch.cuda.Stream = None):
+    """d_logits [T, E] in the logits' type from d_weights fp32 [T, k], with the idx that
+    route_experts returned for these logits and the same score, renormalise and scale."""
+    if stream is not None:
+        return run_on(stream, route_experts_backward, d_weights, logits, idx, score, renormalise, scale)
+    what = "route_experts_backward"
+    logits = _logits(what, logits)
+    T, E = logits.shape
+    dev = logits.device
+    want(idx.dim() == 2 and idx.shape[0] == T and idx.dtype is torch.int32 and idx.device == dev, what,
+         "idx must be int32 [T, k] on the logits' device")
+    k = idx.shape[1]
+    want(d_weights.shape == idx.shape and d_weights.dtype is torch.float32 and d_weights.device == dev, what,
+         "d_weights must be fp32 [T, k] on the logits' device")
+    idx, d_weights = idx.contiguous(), d_weights.contiguous()
+    d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    check(N.load().moe_route_experts_backward(_config(E, k, score, 1, 1, 1, renormalise, scale), logits.data_ptr(),
+                                              DTYPE_CODES[logits.dtype], logits.stride(0) if T > 1 else E,
+                                              idx.data_ptr(), d_weights.data_ptr(), T, d_logits.data_ptr(),
+                                              raw_stream(None, dev)), "moe_route_experts_backward")
+    return d_logits
