@@ -481,8 +481,8 @@ moe_status_t moe_quant_matmul(const void* x_dev, int32_t x_dtype, int64_t x_stri
  * gate_up_scale_dev fp32 [E, 2I]; down_dev S8 [E, H, I] and down_scale_dev fp32 [E, H].
  * A shared expert of the same size is one more expert that every token chooses with
  * weight 1. H and I are multiples of 16 (else MOE_ERR_UNSUPPORTED), H <= 16384,
- * I <= 16384, k <= MOE_ROUTE_MAX_TOP_K, E <= MOE_INT8_MAX_EXPERTS; x, out, gate_up and down are 16-byte aligned; out does
- * not overlap x. workspace as in moe_quant_matmul.
+ * I <= 16384, k <= MOE_ROUTE_MAX_TOP_K, E <= MOE_INT8_MAX_EXPERTS; x, out, gate_up, down and down_scale are 16-byte aligned; out does
+ * not overlap x. T * k < 2^30. workspace as in moe_quant_matmul.
  */
 #define MOE_INT8_MAX_EXPERTS 1024
 typedef struct {
@@ -498,6 +498,13 @@ moe_status_t moe_quant_experts_workspace(const moe_int8_experts_config_t* cfg, i
 moe_status_t moe_quant_experts(const moe_int8_experts_config_t* cfg, const moe_int8_experts_weights_t* w,
                               const void* x_dev, int32_t x_dtype, const int32_t* idx_dev, const float* weights_dev,
                               void* out_dev, int32_t T, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/*
+ * Synchronise `stream`, then read and clear the error word of the 8-bit products on the
+ * current device: MOE_OK, or MOE_ERR_TIMEOUT if a bounded wait inside one of them ran
+ * out (its outputs are undefined then).
+ */
+moe_status_t moe_quant_sync_status(void* stream);
 
 /* Name of a status code (static string). */
 const char* moe_status_string(moe_status_t status);

@@ -10,4 +10,4 @@ from ._native import load  # noqa: F401
 from .layer import MoeLayer, weights_from_raw  # noqa: F401
 from .lmhead import LmHead  # noqa: F401
 from .routing import route_experts, route_experts_backward  # noqa: F401
-from .int8 import int8_experts, int8_matmul  # noqa: F401
+from .int8 import int8_experts, int8_matmul, int8_sync_status  # noqa: F401

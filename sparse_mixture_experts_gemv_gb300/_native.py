@@ -140,6 +140,7 @@ _SIGNATURES = {
                                         ctypes.POINTER(moe_int8_experts_weights_t), ctypes.c_void_p, ctypes.c_int32,
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "moe_quant_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_cuda_error": (ctypes.c_char_p, []),
 }

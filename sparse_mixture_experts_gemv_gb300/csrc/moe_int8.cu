@@ -1,5 +1,6 @@
-// Products and SwiGLU experts in 8-bit integers, for few tokens: the weights are
-// streamed once and multiplied on the integer dot-product units.
+// Products and SwiGLU experts in 8-bit integers: the entry points, the kernels for few
+// tokens, which stream the weights once through the integer dot-product units, and what
+// goes around the tensor-core products of many tokens (moe_int8_gemm.cu).
 //
 //   out[t, n] = (sum_k q[t, k] w[n, k]) x_scale[t] w_scale[n]
 //
@@ -13,6 +14,7 @@
 #include <stdint.h>
 
 #include "moe_int8.cuh"
+#include "moe_int8.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -290,6 +292,197 @@ __global__ void __launch_bounds__(kDownThreads, 6) int8_experts_down_kernel(cons
   }
 }
 
+// ------------------------------------------------- around the tensor-core products
+struct PrepareParams {
+  const void* x;          // [rows][K], row stride `stride` elements
+  int64_t stride;
+  const float* x_scale;   // S8 alone
+  int rows, K;
+  const int* num_rows;    // rows there really are, or NULL
+  __half* q;              // [rows][K] whole numbers
+  float* scale;           // [rows]
+  // grouping of choices by expert, by block 0 where idx is not NULL
+  const int* idx;
+  int choices, E, block, max_blocks;
+  int* perm;
+  int* pos;
+  int4* blocks;
+  int* counts;            // [0]: blocks, [1]: grouped rows
+};
+
+constexpr int kPrepareThreads = 1024;
+
+MOE_DEV uint32_t int_pair_f16(int a, int b) {
+  const __half2 h = __halves2half2(__int2half_rn(a), __int2half_rn(b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Choices in order of their experts: a histogram, a scan, and a scatter whose order
+// within an expert is the atomics' (every row is computed by itself, so no result
+// depends on it). An expert's rows are cut evenly into blocks of at most p.block.
+MOE_DEV void group_choices(const PrepareParams& p) {
+  __shared__ int count[kPrepareThreads], cursor[kPrepareThreads], sums[2][32];
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  count[i] = 0;
+  __syncthreads();
+  for (int a = i; a < p.choices; a += kPrepareThreads) {
+    const int e = __ldg(p.idx + a);
+    if (e >= 0 && e < p.E) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  const int c = count[i], nb = (c + p.block - 1) / p.block;
+  int rows = c, blocks = nb;   // inclusive scans
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int r = __shfl_up_sync(0xFFFFFFFFu, rows, o), b = __shfl_up_sync(0xFFFFFFFFu, blocks, o);
+    if (lane >= o) { rows += r; blocks += b; }
+  }
+  if (lane == 31) { sums[0][warp] = rows; sums[1][warp] = blocks; }
+  __syncthreads();
+  if (warp == 0) {
+    int r = sums[0][lane], b = sums[1][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, r, o), y = __shfl_up_sync(0xFFFFFFFFu, b, o);
+      if (lane >= o) { r += x; b += y; }
+    }
+    sums[0][lane] = r;
+    sums[1][lane] = b;
+  }
+  __syncthreads();
+  if (warp > 0) { rows += sums[0][warp - 1]; blocks += sums[1][warp - 1]; }
+  const int row0 = rows - c, b0 = blocks - nb;
+  cursor[i] = row0;
+  const int size = nb ? ((c + nb - 1) / nb + 15) & ~15 : 0;
+  for (int b = 0; b < nb; ++b)
+    if (b0 + b < p.max_blocks) p.blocks[b0 + b] = make_int4(i, row0 + b * size, min(size, c - b * size), 0);
+  if (i == kPrepareThreads - 1) { p.counts[0] = blocks; p.counts[1] = rows; }
+  __syncthreads();
+  for (int a = i; a < p.choices; a += kPrepareThreads) {
+    const int e = __ldg(p.idx + a);
+    int at = -1;
+    if (e >= 0 && e < p.E) {
+      at = atomicAdd(&cursor[e], 1);
+      p.perm[at] = a;
+    }
+    p.pos[a] = at;
+  }
+}
+
+// Rows as whole numbers in f16, and their scales: one warp a row.
+template <int DT>
+__global__ void __launch_bounds__(kPrepareThreads) int8_prepare_kernel(const PrepareParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  int first = blockIdx.x, stride = gridDim.x;
+  if (p.idx) {
+    if (blockIdx.x == 0) {
+      group_choices(p);
+      return;
+    }
+    --first;
+    --stride;
+  }
+  const int lane = threadIdx.x & 31, nch = p.K / 16;
+  const int rows = p.num_rows ? min(p.rows, ldg_cg_s32(p.num_rows)) : p.rows;
+  for (int64_t r = (int64_t)first * 32 + (threadIdx.x >> 5); r < rows; r += (int64_t)stride * 32) {
+    uint4* q = reinterpret_cast<uint4*>(p.q + r * p.K);
+    if constexpr (DT == MOE_DTYPE_S8) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.x) + r * p.stride);
+      for (int c = lane; c < nch; c += 32) {
+        const uint4 u = __ldg(src + c);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[2 * i] = int_pair_f16((int8_t)w[i], (int8_t)(w[i] >> 8));
+          o[2 * i + 1] = int_pair_f16((int8_t)(w[i] >> 16), (int8_t)(w[i] >> 24));
+        }
+        q[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
+        q[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      if (lane == 0) p.scale[r] = p.x_scale[r];
+    } else {
+      float v[16];
+      uint32_t m = 0;
+      for (int c = lane; c < nch; c += 32) {
+        if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(p.x) + r * p.stride + 16 * c, v);
+        else load16<DT>(p.x, r * p.stride + 16 * c, v);
+        m = max(m, amax_bits(v));
+      }
+      const RowScale s = row_scale(__reduce_max_sync(0xFFFFFFFFu, m));
+      for (int c = lane; c < nch; c += 32) {
+        if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(p.x) + r * p.stride + 16 * c, v);
+        else load16<DT>(p.x, r * p.stride + 16 * c, v);
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = int_pair_f16(quantize(v[2 * i], s), quantize(v[2 * i + 1], s));
+        q[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
+        q[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      if (lane == 0) p.scale[r] = s.scale;
+    }
+  }
+}
+
+struct CombineParams {
+  const __half* y;           // [rows][H]: integer sums times 1 / factor
+  const float* h_scale;      // [rows]
+  const int* idx;
+  const int* pos;            // grouped row of each choice, -1: none
+  const float* weights;
+  const float* down_scale;   // [E][H]
+  void* out;
+  int T, k, H, out_dtype;
+  float factor;
+};
+
+constexpr int kCombineThreads = 256;
+
+// out[t] = sum_j weights[t, j] h_scale y_j down_scale[e_j], eight channels a thread.
+__global__ void __launch_bounds__(kCombineThreads) int8_combine_kernel(const CombineParams p) {
+  __shared__ float s_f[MOE_ROUTE_MAX_TOP_K];
+  __shared__ int s_e[MOE_ROUTE_MAX_TOP_K], s_pos[MOE_ROUTE_MAX_TOP_K];
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    __syncthreads();
+    if (threadIdx.x < p.k) {
+      const int64_t a = t * p.k + threadIdx.x;
+      const int at = ldg_cg_s32(p.pos + a);
+      s_pos[threadIdx.x] = at;
+      s_e[threadIdx.x] = __ldg(p.idx + a);
+      s_f[threadIdx.x] = at >= 0 ? __ldg(p.weights + a) * (ldg_cg_f32(p.h_scale + at) * p.factor) : 0.f;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x * 8; c < p.H; c += kCombineThreads * 8) {
+      float acc[8] = {};
+#pragma unroll 4
+      for (int j = 0; j < p.k; ++j) {
+        const int at = s_pos[j];
+        if (at < 0) continue;
+        const float f = s_f[j];
+        const uint4 y = ldg_cg(p.y + (int64_t)at * p.H + c);
+        const float4* ws = reinterpret_cast<const float4*>(p.down_scale + (int64_t)s_e[j] * p.H + c);
+        const float4 w0 = __ldg(ws), w1 = __ldg(ws + 1);
+        const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&yw[i]));
+          acc[2 * i] += f * w[2 * i] * v.x;
+          acc[2 * i + 1] += f * w[2 * i + 1] * v.y;
+        }
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = (uint32_t)to_16(p.out_dtype, acc[2 * i]) | ((uint32_t)to_16(p.out_dtype, acc[2 * i + 1]) << 16);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.H + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
 template <class K, class... A>
 cudaError_t launch_pdl(K kernel, dim3 grid, int block, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
@@ -334,6 +527,187 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 int dtype_size(int d) { return d == MOE_DTYPE_S8 ? 1 : d == MOE_DTYPE_F32 ? 4 : 2; }
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
+// Tokens up to which the weights are streamed through the dot-product units.
+constexpr int kStreamTokens = 8;
+
+cudaError_t launch_prepare(const PrepareParams& p, int dtype, int num_sms, cudaStream_t s) {
+  const int64_t blocks = ((int64_t)p.rows + 31) / 32;
+  const dim3 grid((unsigned)((blocks < 2 * num_sms ? blocks : 2 * num_sms) + (p.idx ? 1 : 0)));
+  switch (dtype) {
+    case MOE_DTYPE_F32: return launch_pdl(int8_prepare_kernel<MOE_DTYPE_F32>, grid, kPrepareThreads, 0, s, p);
+    case MOE_DTYPE_BF16: return launch_pdl(int8_prepare_kernel<MOE_DTYPE_BF16>, grid, kPrepareThreads, 0, s, p);
+    case MOE_DTYPE_F16: return launch_pdl(int8_prepare_kernel<MOE_DTYPE_F16>, grid, kPrepareThreads, 0, s, p);
+    default: return launch_pdl(int8_prepare_kernel<MOE_DTYPE_S8>, grid, kPrepareThreads, 0, s, p);
+  }
+}
+
+struct MatmulWorkspace {
+  int64_t q, scale, bytes;
+};
+MatmulWorkspace matmul_workspace(int64_t T, int64_t K) {
+  MatmulWorkspace w = {};
+  if (T <= kStreamTokens) return w;
+  w.scale = pad256(T * K * 2);
+  w.bytes = w.scale + pad256(T * 4);
+  return w;
+}
+
+cudaError_t launch_matmul_tensor(const StreamParams& p, int x_dtype, uint8_t* ws, int num_sms, cudaStream_t s) {
+  const MatmulWorkspace w = matmul_workspace(p.T, p.K);
+  PrepareParams a = {};
+  a.x = p.x;
+  a.stride = p.x_stride;
+  a.x_scale = p.x_scale;
+  a.rows = p.T;
+  a.K = p.K;
+  a.q = (__half*)(ws + w.q);
+  a.scale = (float*)(ws + w.scale);
+  cudaError_t e = launch_prepare(a, x_dtype, num_sms, s);
+  if (e != cudaSuccess) return e;
+  GemmArgs g = {};
+  g.a = p.w;
+  g.a_rows = p.N;
+  g.a_stride = p.w_stride;
+  g.b = a.q;
+  g.b_rows = p.T;
+  g.b_stride = p.K;
+  g.K = p.K;
+  g.channels = p.N;
+  const int tiles = (p.T + kMaxBlock - 1) / kMaxBlock;   // as few token tiles as there can be, of even size
+  g.block = ((p.T + tiles - 1) / tiles + 15) / 16 * 16;
+  g.T = p.T;
+  g.row_scale = a.scale;
+  g.w_scale = p.w_scale;
+  g.out = p.out;
+  g.out_dtype = p.out_dtype;
+  return launch_gemm(kDense, g, num_sms, s);
+}
+
+// Scratch of the experts' call. y takes h's place, which is dead by then.
+struct ExpertsWorkspace {
+  int64_t h, q, x_scale, hq, h_scale, perm, pos, blocks, counts, bytes;
+  int block, max_blocks;
+};
+ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T) {
+  ExpertsWorkspace w = {};
+  const int64_t rows = T * c->top_k, H = c->hidden, I = c->intermediate;
+  if (T <= kStreamTokens) {
+    w.bytes = pad256(rows * I * 4);
+    return w;
+  }
+  // blocks about one and a half times an expert's mean load: most experts are one block
+  const int64_t touched = rows < c->num_experts ? rows : c->num_experts;
+  const int64_t want = (rows * 3 / (2 * touched) + 15) / 16 * 16;
+  w.block = (int)(want < 32 ? 32 : want > kMaxBlock ? kMaxBlock : want);
+  w.max_blocks = (int)(touched + rows / w.block);
+  int64_t at = 0;
+  const auto take = [&at](int64_t bytes) { const int64_t o = at; at += pad256(bytes); return o; };
+  w.h = take(rows * (I * 4 > H * 2 ? I * 4 : H * 2));
+  w.q = take(T * H * 2);
+  w.x_scale = take(T * 4);
+  w.hq = take(rows * I * 2);
+  w.h_scale = take(rows * 4);
+  w.perm = take(rows * 4);
+  w.pos = take(rows * 4);
+  w.blocks = take((int64_t)w.max_blocks * 16);
+  w.counts = take(8);
+  w.bytes = at;
+  return w;
+}
+
+cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts_config_t* cfg, int x_dtype,
+                                  uint8_t* ws, int num_sms, cudaStream_t s) {
+  const ExpertsWorkspace w = experts_workspace(cfg, p.T);
+  const int rows = p.T * p.k;
+  PrepareParams a = {};
+  a.x = p.x;
+  a.stride = p.H;
+  a.rows = p.T;
+  a.K = p.H;
+  a.q = (__half*)(ws + w.q);
+  a.scale = (float*)(ws + w.x_scale);
+  a.idx = p.idx;
+  a.choices = rows;
+  a.E = p.E;
+  a.block = w.block;
+  a.max_blocks = w.max_blocks;
+  a.perm = (int*)(ws + w.perm);
+  a.pos = (int*)(ws + w.pos);
+  a.blocks = (int4*)(ws + w.blocks);
+  a.counts = (int*)(ws + w.counts);
+  cudaError_t e = launch_prepare(a, x_dtype, num_sms, s);
+  if (e != cudaSuccess) return e;
+
+  GemmArgs g = {};
+  g.a = p.gate_up;
+  g.a_rows = (int64_t)p.E * 2 * p.I;
+  g.a_stride = p.H;
+  g.b = a.q;
+  g.b_rows = p.T;
+  g.b_stride = p.H;
+  g.K = p.H;
+  g.channels = p.I;
+  g.rows_per_group = 2 * p.I;
+  g.block = w.block;
+  g.blocks = a.blocks;
+  g.num_blocks = a.counts;
+  g.max_blocks = w.max_blocks;
+  g.T = p.T;
+  g.perm = a.perm;
+  g.k = p.k;
+  g.row_scale = a.scale;
+  g.w_scale = p.gate_up_scale;
+  g.out = ws + w.h;
+  e = launch_gemm(kUp, g, num_sms, s);
+  if (e != cudaSuccess) return e;
+
+  PrepareParams b = {};
+  b.x = ws + w.h;
+  b.stride = p.I;
+  b.rows = rows;
+  b.K = p.I;
+  b.num_rows = a.counts + 1;
+  b.q = (__half*)(ws + w.hq);
+  b.scale = (float*)(ws + w.h_scale);
+  e = launch_prepare(b, MOE_DTYPE_F32, num_sms, s);
+  if (e != cudaSuccess) return e;
+
+  // the down sums (at most 127 * 128 * I) fit f16 once divided by a power of two, and whole numbers
+  // times it are never below f16's normal range: the rounding to 11 bits is relative, and far below
+  // that of the output
+  float factor = 1.f;
+  while (127.f * 128.f * (float)p.I > 65504.f * factor) factor *= 2.f;
+  g.a = p.down;
+  g.a_rows = (int64_t)p.E * p.H;
+  g.a_stride = p.I;
+  g.b = b.q;
+  g.b_rows = rows;
+  g.b_stride = p.I;
+  g.K = p.I;
+  g.channels = p.H;
+  g.rows_per_group = p.H;
+  g.w_scale = nullptr;
+  g.out = ws + w.h;
+  g.factor = 1.f / factor;
+  e = launch_gemm(kDown, g, num_sms, s);
+  if (e != cudaSuccess) return e;
+
+  CombineParams c = {};
+  c.y = (const __half*)(ws + w.h);
+  c.h_scale = b.scale;
+  c.idx = p.idx;
+  c.pos = a.pos;
+  c.weights = p.weights;
+  c.down_scale = p.down_scale;
+  c.out = p.out;
+  c.T = p.T;
+  c.k = p.k;
+  c.H = p.H;
+  c.out_dtype = p.out_dtype;
+  c.factor = factor;
+  return launch_pdl(int8_combine_kernel, dim3((unsigned)(p.T < num_sms * 8 ? p.T : num_sms * 8)), kCombineThreads, 0, s, c);
+}
+
 }  // namespace
 }  // namespace int8
 }  // namespace moe
@@ -342,7 +716,7 @@ extern "C" {
 
 moe_status_t moe_quant_matmul_workspace(int32_t T, int32_t N, int32_t K, int32_t x_dtype, int64_t* bytes) {
   if (!bytes || T < 0 || N < 0 || K < 1 || x_dtype < MOE_DTYPE_F32 || x_dtype > MOE_DTYPE_S8) return MOE_ERR_INVALID_ARG;
-  *bytes = 0;
+  *bytes = moe::int8::matmul_workspace(T, K).bytes;
   return MOE_OK;
 }
 
@@ -351,8 +725,6 @@ moe_status_t moe_quant_matmul(const void* x_dev, int32_t x_dtype, int64_t x_stri
                              int32_t out_dtype, int32_t T, int32_t N, int32_t K, void* workspace_dev,
                              int64_t workspace_bytes, void* stream) {
   using namespace moe::int8;
-  (void)workspace_dev;
-  (void)workspace_bytes;
   if (T < 0 || N < 0 || K < 1) return MOE_ERR_INVALID_ARG;
   if (x_dtype < MOE_DTYPE_F32 || x_dtype > MOE_DTYPE_S8 || out_dtype < MOE_DTYPE_F32 || out_dtype > MOE_DTYPE_F16)
     return MOE_ERR_INVALID_ARG;
@@ -368,10 +740,13 @@ moe_status_t moe_quant_matmul(const void* x_dev, int32_t x_dtype, int64_t x_stri
   if (overlap(x_dev, ((T - 1) * x_stride + K) * xs, out_dev, (int64_t)T * N * os) ||
       overlap(w_dev, (N - 1) * w_stride + K, out_dev, (int64_t)T * N * os))
     return MOE_ERR_INVALID_ARG;
+  const int64_t need = matmul_workspace(T, K).bytes;
+  if (need && (!workspace_dev || workspace_bytes < need || (uintptr_t)workspace_dev & 255)) return MOE_ERR_INVALID_ARG;
   const StreamParams p = {x_dev, x_stride, x_scale_dev, w_dev, w_stride, w_scale_dev, out_dev, out_dtype, T, N, K};
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  switch (x_dtype) {
+  if (need) e = launch_matmul_tensor(p, x_dtype, (uint8_t*)workspace_dev, device_sms(), s);
+  else switch (x_dtype) {
     case MOE_DTYPE_F32: e = launch_stream_dt<MOE_DTYPE_F32>(p, device_sms(), s); break;
     case MOE_DTYPE_BF16: e = launch_stream_dt<MOE_DTYPE_BF16>(p, device_sms(), s); break;
     case MOE_DTYPE_F16: e = launch_stream_dt<MOE_DTYPE_F16>(p, device_sms(), s); break;
@@ -387,7 +762,8 @@ moe_status_t moe_quant_experts_workspace(const moe_int8_experts_config_t* c, int
   if (c->hidden % 16 || c->intermediate % 16 || c->hidden > 16384 || c->intermediate > 16384 ||
       c->top_k > MOE_ROUTE_MAX_TOP_K || c->num_experts > MOE_INT8_MAX_EXPERTS)
     return MOE_ERR_UNSUPPORTED;
-  *bytes = pad256((int64_t)T * c->top_k * c->intermediate * 4);
+  if ((int64_t)T * c->top_k > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  *bytes = experts_workspace(c, T).bytes;
   return MOE_OK;
 }
 
@@ -403,8 +779,9 @@ moe_status_t moe_quant_experts(const moe_int8_experts_config_t* c, const moe_int
   if (!w || !w->gate_up_dev || !w->gate_up_scale_dev || !w->down_dev || !w->down_scale_dev || !x_dev || !idx_dev ||
       !weights_dev || !out_dev || !workspace_dev || workspace_bytes < need)
     return MOE_ERR_INVALID_ARG;
-  if (((uintptr_t)x_dev | (uintptr_t)out_dev | (uintptr_t)w->gate_up_dev | (uintptr_t)w->down_dev) & 15 ||
-      ((uintptr_t)idx_dev | (uintptr_t)weights_dev | (uintptr_t)w->gate_up_scale_dev | (uintptr_t)w->down_scale_dev) & 3 ||
+  if (((uintptr_t)x_dev | (uintptr_t)out_dev | (uintptr_t)w->gate_up_dev | (uintptr_t)w->down_dev |
+       (uintptr_t)w->down_scale_dev) & 15 ||
+      ((uintptr_t)idx_dev | (uintptr_t)weights_dev | (uintptr_t)w->gate_up_scale_dev) & 3 ||
       (uintptr_t)workspace_dev & 255)
     return MOE_ERR_INVALID_ARG;
   const int64_t xb = (int64_t)T * c->hidden * 2;
@@ -425,8 +802,18 @@ moe_status_t moe_quant_experts(const moe_int8_experts_config_t* c, const moe_int
   p.H = c->hidden;
   p.I = c->intermediate;
   p.out_dtype = x_dtype;
-  const cudaError_t e = launch_experts_stream(p, x_dtype, (cudaStream_t)stream);
+  const cudaError_t e = T <= kStreamTokens
+                            ? launch_experts_stream(p, x_dtype, (cudaStream_t)stream)
+                            : launch_experts_tensor(p, c, x_dtype, (uint8_t*)workspace_dev, device_sms(),
+                                                    (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : moe::record_cuda_failure(e, "moe_quant_experts");
+}
+
+moe_status_t moe_quant_sync_status(void* stream) {
+  int code = 0;
+  const cudaError_t e = moe::int8::gemm_status((cudaStream_t)stream, &code);
+  if (e != cudaSuccess) return moe::record_cuda_failure(e, "moe_quant_sync_status");
+  return (moe_status_t)code;
 }
 
 }  // extern "C"

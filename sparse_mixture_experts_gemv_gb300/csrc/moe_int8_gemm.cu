@@ -1,0 +1,505 @@
+// 8-bit integer products on the tensor cores, for many tokens: dense, and grouped by
+// expert.
+//
+//   D[channel, token] = sum_k w[channel, k] q[token, k]
+//
+// The fifth-generation tensor cores have no 8-bit integer kind on this chip, and the
+// older integer instructions run far below the f16 rate. Whole numbers of 8 bits are
+// exact in f16, their products (at most 2^14) and sums (up to 2^24) in the fp32
+// accumulators, so the products run as f16 x f16, and give the integers themselves.
+//
+// The weights stay bytes in memory: each tile of 128 channels x 64 bytes comes in by
+// TMA, eight converter warps turn it into f16 and write it straight into tensor memory,
+// from where the MMA reads its A operand. (Through shared memory the f16 copy would
+// be written and read there once more, and with the token operand that is what bounds
+// the MMA.) The tokens, far fewer than weights or read many times, are f16 in memory
+// already and are the B operand, up to 192 a tile in steps of 16: with few tokens of an
+// expert the MMA does no more than they need, and the weight stream bounds it.
+//
+// One persistent CTA an SM, warp-specialised:
+//   warp 0        weights by TMA              warp 2  tokens by TMA (gathered rows: up)
+//   warp 1        issues the MMAs             warp 3  idle
+//   warps 4-11    converters: two groups of four, alternate steps of 64 along K
+//   warps 12-15   epilogue of the previous tile while the next one accumulates
+// Tensor memory: two accumulators of 192 columns, four operand slots of 32.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <stdint.h>
+
+#include "moe_int8.cuh"
+#include "moe_int8.h"
+#include "moe_layer.h"
+#include "moe_sm100.cuh"
+
+namespace moe {
+namespace int8 {
+namespace {
+
+using namespace sm100;
+
+constexpr int kChannels = 128;            // channels of a tile = lanes of tensor memory
+constexpr int kStep = 64;                 // K of a stage
+constexpr int kRawBytes = kChannels * kStep;
+constexpr int kMaxStages = 16;
+constexpr int kSlots = 4;                 // f16 weight operands in tensor memory
+constexpr int kSlotCols = kStep / 2;
+constexpr int kSlotBase = 2 * kMaxBlock;  // their first column
+constexpr int kGemmThreads = 512;
+constexpr int kStageBudget = 200 * 1024;  // shared memory of all stages
+constexpr int kFixedSmem = 1024 /*align*/ + 4 * kMaxBlock * 4 /*scales*/ + 1024 /*barriers*/;
+
+__device__ int g_gemm_error;              // MOE_ERR_TIMEOUT once a bounded wait ran out
+
+struct Params {
+  const int4* blocks;
+  const int* num_blocks;
+  int max_blocks;
+  int tiles_m;               // channel tiles of a group
+  int tiles_t;               // dense: token tiles
+  int T, block, channels, rows_per_group;
+  int steps, stages, stage_bytes;
+  const int* perm;
+  int k;
+  const float* row_scale;
+  const float* w_scale;
+  void* out;
+  int out_dtype;
+  float factor;
+};
+
+struct Tile {
+  int e, mt, row0, rows, n;   // n: rows rounded up to 16
+};
+
+template <int KIND>
+MOE_DEV Tile decode(const Params& p, int tile) {
+  Tile t;
+  if (KIND == kDense) {   // neighbouring CTAs share the weights of a channel tile
+    t.e = 0;
+    t.mt = tile / p.tiles_t;
+    t.row0 = (tile % p.tiles_t) * p.block;
+    t.rows = min(p.block, p.T - t.row0);
+  } else {                // neighbouring CTAs share the rows of a block; an expert's blocks follow each other
+    const uint4 b = ldg_cg(p.blocks + tile / p.tiles_m);
+    t.e = (int)b.x;
+    t.mt = tile % p.tiles_m;
+    t.row0 = (int)b.y;
+    t.rows = (int)b.z;
+  }
+  t.n = (t.rows + 15) & ~15;
+  return t;
+}
+
+// Four bytes of signed integers -> two f16 pairs. 0x64uu is 1024 + uu; with the sign
+// bit flipped uu = b + 128, so b = that minus 1152, exactly.
+MOE_DEV void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+}
+
+// 32 columns of this warp's 32 lanes of tensor memory.
+MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+         "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+         "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
+MOE_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      :: "r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Four rows (any four of the matrix) of one 128-byte column block.
+MOE_DEV void tma_gather4(void* dst, const CUtensorMap* map, int c0, const int4 rows, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      :: "r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w),
+         "r"(smem_u32(bar)) : "memory");
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  // stage: tokens (block x 128 bytes, whole 1024-byte swizzle atoms) and raw weights behind all of them
+  const int b_bytes = p.stage_bytes - kRawBytes;
+  uint8_t* s_b = smem;
+  uint8_t* s_raw = smem + p.stages * b_bytes;
+  float* s_scale = reinterpret_cast<float*>(s_raw + p.stages * kRawBytes);   // [4][kMaxBlock]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + 4 * kMaxBlock);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* a_full = empty + kMaxStages;
+  uint64_t* a_empty = a_full + kSlots;
+  uint64_t* d_full = a_empty + kSlots;
+  uint64_t* d_empty = d_full + 2;
+  uint64_t* drain = d_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* err = &g_gemm_error;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&a_full[s], 4);
+      mbar_init(&a_empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&d_full[a], 1);
+      mbar_init(&d_empty[a], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&map_a);
+    prefetch_tmap(&map_b);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  pdl_wait();
+  asm volatile("fence.proxy.async.global;" ::: "memory");   // tokens written by the kernel before, read by TMA here
+  pdl_launch_dependents();
+
+  int total;
+  if (KIND == kDense) {
+    total = p.tiles_m * p.tiles_t;
+  } else {
+    const int nb = ldg_cg_s32(p.num_blocks);
+    total = (nb < 0 || nb > p.max_blocks ? 0 : nb) * p.tiles_m;
+  }
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- weights
+    if (lane == 0) {
+      uint32_t it = 0;
+      int s = 0, ph = 1;
+      bool stop = false;
+      for (int tile = blockIdx.x; tile < total && !stop && !*abort_flag; tile += gridDim.x) {
+        const Tile t = decode<KIND>(p, tile);
+        const int r0 = KIND == kUp ? t.e * p.rows_per_group + t.mt * 64 : t.e * p.rows_per_group + t.mt * kChannels;
+        const int r1 = KIND == kUp ? r0 + p.channels : r0 + 64;   // up: 64 gate rows, then their up rows
+        for (int ks = 0; ks < p.steps; ++ks, ++it) {
+          if (!mbar_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
+          mbar_arrive_expect_tx(&full[s], (uint32_t)(kRawBytes + t.n * 128));
+          tma_load_2d(s_raw + s * kRawBytes, &map_a, ks * kStep, r0, &full[s]);
+          tma_load_2d(s_raw + s * kRawBytes + kRawBytes / 2, &map_a, ks * kStep, r1, &full[s]);
+          if (++s == p.stages) { s = 0; ph ^= 1; }
+        }
+      }
+      if (*abort_flag) {   // let copies in flight land before the CTA exits
+        for (uint32_t q = it > (uint32_t)p.stages ? it - p.stages : 0; q < it; ++q)
+          mbar_wait(&full[q % p.stages], (q / p.stages) & 1, err, abort_flag, 20000000LL, false);
+      }
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- tokens
+    int s = 0, ph = 1;
+    bool stop = false;
+    for (int tile = blockIdx.x; tile < total && !stop && !*abort_flag; tile += gridDim.x) {
+      const Tile t = decode<KIND>(p, tile);
+      int4 rows[2] = {};
+      if (KIND == kUp) {   // lane l gathers rows 4l.. and 4(l + 32)..; rows past the block's end repeat its last
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = 4 * (lane + 32 * i), last = t.row0 + t.rows - 1;
+          if (c < t.n) {
+            rows[i].x = ldg_cg_s32(p.perm + min(t.row0 + c, last)) / p.k;
+            rows[i].y = ldg_cg_s32(p.perm + min(t.row0 + c + 1, last)) / p.k;
+            rows[i].z = ldg_cg_s32(p.perm + min(t.row0 + c + 2, last)) / p.k;
+            rows[i].w = ldg_cg_s32(p.perm + min(t.row0 + c + 3, last)) / p.k;
+          }
+        }
+      }
+      for (int ks = 0; ks < p.steps; ++ks) {
+        if (!mbar_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
+        uint8_t* dst = s_b + s * b_bytes;
+        if (KIND == kUp) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = 4 * (lane + 32 * i);
+            if (c < t.n) tma_gather4(dst + c * 128, &map_b, ks * kStep, rows[i], &full[s]);
+          }
+        } else if (lane < t.n / 16) {
+          tma_load_2d(dst + lane * 2048, &map_b, ks * kStep, t.row0 + lane * 16, &full[s]);
+        }
+        if (++s == p.stages) { s = 0; ph ^= 1; }
+      }
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      int s = 0, ph = 0;
+      uint32_t it = 0, tc = 0;
+      for (int tile = blockIdx.x; tile < total && !*abort_flag; tile += gridDim.x, ++tc) {
+        const Tile t = decode<KIND>(p, tile);
+        // f16 x f16 -> fp32, both K-major, 128 x n
+        const uint32_t idesc = (1u << 4) | ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kChannels >> 4) << 24);
+        const int ab = tc & 1;
+        if (!mbar_wait(&d_empty[ab], ((tc >> 1) & 1) ^ 1, err, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + ab * kMaxBlock;
+        bool ok = true;
+        for (int ks = 0; ks < p.steps; ++ks, ++it) {
+          const int slot = it & (kSlots - 1);
+          if (!mbar_wait(&full[s], ph, err, abort_flag) ||
+              !mbar_wait(&a_full[slot], (it / kSlots) & 1, err, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a0 = tmem + kSlotBase + slot * kSlotCols, b0 = smem_u32(s_b + s * b_bytes);
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            mma_f16_ts(d, a0 + kk * 8, smem_desc_sw128(b0 + kk * 32), idesc, (ks | kk) != 0 ? 1u : 0u);
+          mma_commit(&empty[s]);      // the converters have read this stage's weights by now too
+          mma_commit(&a_empty[slot]);
+          if (++s == p.stages) { s = 0; ph ^= 1; }
+        }
+        if (!ok) break;
+        mma_commit(&d_full[ab]);
+      }
+      mma_commit(drain);   // all MMAs complete before tensor memory is released
+      mbar_wait(drain, 0, err, abort_flag, 2000000000LL, false);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ---------------------------------------------------------- converters
+    const int group = (warp - 4) >> 2, quad = warp & 3;
+    // The lane's row of the raw tile. up: a warp's lower 16 lanes are gate rows, its upper
+    // 16 the up rows of the same features, so that the epilogue pairs them by a shuffle.
+    const int row = KIND == kUp ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
+    const int sw = (row >> 1) & 3;   // 64-byte swizzle: 16-byte chunk c of row r lands at c ^ (r / 2 % 4)
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    uint32_t it = 0;
+    int s = 0, ph = 0;
+    bool stop = false;
+    for (int tile = blockIdx.x; tile < total && !stop && !*abort_flag; tile += gridDim.x) {
+      for (int ks = 0; ks < p.steps; ++ks, ++it) {
+        if ((int)(it & 1) == group) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], ph, err, abort_flag))) { stop = true; break; }
+          const uint8_t* src = s_raw + s * kRawBytes + row * kStep;
+          uint32_t r[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
+            s8x4_to_f16(w.x, r[8 * c], r[8 * c + 1]);
+            s8x4_to_f16(w.y, r[8 * c + 2], r[8 * c + 3]);
+            s8x4_to_f16(w.z, r[8 * c + 4], r[8 * c + 5]);
+            s8x4_to_f16(w.w, r[8 * c + 6], r[8 * c + 7]);
+          }
+          const int slot = it & (kSlots - 1);
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&a_empty[slot], ((it / kSlots) & 1) ^ 1, err, abort_flag))) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          tmem_st32(tmem + lanes + kSlotBase + slot * kSlotCols, r);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&a_full[slot]);
+        }
+        if (++s == p.stages) { s = 0; ph ^= 1; }
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;
+    float* cs = s_scale + quad * kMaxBlock;   // the warp's copy of the tile's token scales
+    uint32_t tc = 0;
+    for (int tile = blockIdx.x; tile < total && !*abort_flag; tile += gridDim.x, ++tc) {
+      const Tile t = decode<KIND>(p, tile);
+      const int ab = tc & 1;
+      __syncwarp();
+      if (KIND != kDown) {
+        for (int c = lane; c < t.rows; c += 32) {
+          const int row = KIND == kUp ? ldg_cg_s32(p.perm + t.row0 + c) / p.k : t.row0 + c;
+          cs[c] = ldg_cg_f32(p.row_scale + row);
+        }
+      }
+      const int ch = KIND == kUp ? t.mt * 64 + quad * 16 + (lane & 15) : t.mt * kChannels + quad * 32 + lane;
+      const bool in = ch < p.channels;
+      float w0 = 0.f, w1 = 0.f;
+      if (in && KIND == kDense) w0 = __ldg(p.w_scale + ch);
+      if (in && KIND == kUp) {
+        w0 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + ch);
+        w1 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + p.channels + ch);
+      }
+      __syncwarp();
+      const bool ok = mbar_wait(&d_full[ab], (tc >> 1) & 1, err, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + ab * kMaxBlock + ((uint32_t)(quad * 32) << 16);
+      for (int c0 = 0; c0 < t.rows; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(taddr + c0, v);
+        const int nc = min(32, t.rows - c0);
+        if (KIND == kUp) {
+          // lower lanes take the even columns, upper lanes the odd ones: each sends its partner the
+          // other column's half of the pair
+          float* dst = static_cast<float*>(p.out) + ((int64_t)t.row0 + c0 + (lane >> 4)) * p.channels + ch;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const bool upper = lane >= 16;
+            const float keep = __uint_as_float(upper ? v[2 * i + 1] : v[2 * i]);
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[2 * i] : v[2 * i + 1]), 16);
+            const int c = 2 * i + (lane >> 4);
+            if (in && c < nc) {
+              const float xs = cs[c0 + c];
+              dst[(int64_t)2 * i * p.channels] = swiglu((upper ? got : keep) * xs * w0, (upper ? keep : got) * xs * w1);
+            }
+          }
+        } else if (KIND == kDown) {
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + ((int64_t)t.row0 + c0) * p.channels + ch;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (in && i < nc)
+              dst[(int64_t)i * p.channels] = __half_as_ushort(__float2half_rn(__uint_as_float(v[i]) * p.factor));
+        } else {
+          const int64_t at = ((int64_t)t.row0 + c0) * p.channels + ch;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (in && i < nc) {
+              const float f = __uint_as_float(v[i]) * cs[c0 + i] * w0;
+              if (p.out_dtype == MOE_DTYPE_F32) static_cast<float*>(p.out)[at + (int64_t)i * p.channels] = f;
+              else static_cast<uint16_t*>(p.out)[at + (int64_t)i * p.channels] = to_16(p.out_dtype, f);
+            }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_empty[ab]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 f = nullptr;
+  if (!f) {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      f = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+  }
+  return f;
+}
+
+cudaError_t encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
+                   int64_t stride_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
+  if (!f) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)stride_bytes};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = f(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int KIND>
+cudaError_t launch_kind(const CUtensorMap& ma, const CUtensorMap& mb, const Params& p, int grid, size_t smem,
+                        cudaStream_t s) {
+  static bool allowed[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !allowed[dev]) {
+    e = cudaFuncSetAttribute(int8_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kStageBudget + kFixedSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<KIND>, ma, mb, p);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStream_t s) {
+  CUtensorMap ma, mb;
+  cudaError_t e = encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, a.a_rows, a.K, a.a_stride, kStep, 64,
+                         CU_TENSOR_MAP_SWIZZLE_64B);
+  if (e == cudaSuccess)
+    e = encode(&mb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.b, a.b_rows, a.K, a.b_stride * 2, kStep, kind == kUp ? 1 : 16,
+               CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  Params p = {};
+  p.blocks = a.blocks;
+  p.num_blocks = a.num_blocks;
+  p.max_blocks = a.max_blocks;
+  const int per_tile = kind == kUp ? 64 : kChannels;
+  p.tiles_m = (a.channels + per_tile - 1) / per_tile;
+  p.tiles_t = kind == kDense ? (a.T + a.block - 1) / a.block : 1;
+  p.T = a.T;
+  p.block = a.block;
+  p.channels = a.channels;
+  p.rows_per_group = a.rows_per_group;
+  p.steps = (a.K + kStep - 1) / kStep;
+  p.stage_bytes = a.block * 128 + kRawBytes;
+  p.stages = kStageBudget / p.stage_bytes;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.stages &= ~1;   // even: a converter group meets the same stages again, every phase of them
+  p.perm = a.perm;
+  p.k = a.k;
+  p.row_scale = a.row_scale;
+  p.w_scale = a.w_scale;
+  p.out = a.out;
+  p.out_dtype = a.out_dtype;
+  p.factor = a.factor;
+  const size_t smem = (size_t)p.stages * p.stage_bytes + kFixedSmem;
+  const int64_t tiles = (int64_t)p.tiles_m * (kind == kDense ? p.tiles_t : a.max_blocks);
+  const int grid = (int)(tiles < num_sms ? tiles : num_sms);
+  switch (kind) {
+    case kDense: return launch_kind<kDense>(ma, mb, p, grid, smem, s);
+    case kUp: return launch_kind<kUp>(ma, mb, p, grid, smem, s);
+    default: return launch_kind<kDown>(ma, mb, p, grid, smem, s);
+  }
+}
+
+cudaError_t gemm_status(cudaStream_t s, int* code) {
+  const int zero = 0;
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(code, g_gemm_error, sizeof(int));
+  if (e == cudaSuccess && *code) e = cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof(int));
+  return e;
+}
+
+}  // namespace int8
+}  // namespace moe

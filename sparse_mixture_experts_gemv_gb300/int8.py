@@ -84,9 +84,10 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
                  stream: torch.cuda.Stream = None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] * expert[idx[t, j]](x[t]) with SwiGLU experts in int8.
 
-    x: bf16 or fp16 [T, H]. idx int32, weights fp32 [T, k], as route_experts gives them; a
+    x: bf16 or fp16 [T, H]. idx int32 and weights fp32 [T, k] as route_experts gives them; a
     choice outside [0, E) contributes nothing. gate_up: int8 [E, 2I, H], gate rows before up
-    rows, gate_up_scale fp32 [E, 2I]; down: int8 [E, H, I], down_scale fp32 [E, H]. x and the
+    rows, gate_up_scale fp32 [E, 2I]; down: int8 [E, H, I], down_scale fp32 [E, H];
+    these four without gaps and on 16-byte boundaries. H and I are multiples of 16. x and the
     SwiGLU outputs are quantized for each token as in int8_matmul. Returns [T, H] in x's type.
     """
     if stream is not None:
@@ -112,6 +113,8 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
     for name, t in (("gate_up", gate_up), ("gate_up_scale", gate_up_scale), ("down", down), ("down_scale", down_scale)):
         if t.device != dev or not t.is_contiguous():
             invalid(what, f"{name} must be on {dev} and without gaps")
+        if t.data_ptr() % 16:
+            invalid(what, f"{name} must start on a 16-byte boundary")
     x, idx, weights = x.contiguous(), idx.contiguous(), weights.contiguous()
     if x.data_ptr() % 16:
         x = x.clone()
@@ -126,3 +129,8 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
                                     weights.data_ptr(), out.data_ptr(), T, ws.data_ptr(), need,
                                     raw_stream(None, dev)), "moe_quant_experts")
     return out
+
+
+def int8_sync_status(stream: torch.cuda.Stream = None) -> int:
+    """Waits for the stream; MOE_OK, or MOE_ERR_TIMEOUT if a product's bounded wait ran out since the last call."""
+    return N.load().moe_quant_sync_status(raw_stream(stream, torch.device("cuda", torch.cuda.current_device())))
