@@ -301,36 +301,135 @@ struct PrepareParams {
   const int* num_rows;    // rows there really are, or NULL
   __half* q;              // [rows][K] whole numbers
   float* scale;           // [rows]
-  // grouping of choices by expert, by block 0 where idx is not NULL
-  const int* idx;
-  int choices, E, block, max_blocks;
-  int* perm;
-  int* pos;
-  int4* blocks;
-  int* counts;            // [0]: blocks, [1]: grouped rows
 };
-
-constexpr int kPrepareThreads = 1024;
 
 MOE_DEV uint32_t int_pair_f16(int a, int b) {
   const __half2 h = __halves2half2(__int2half_rn(a), __int2half_rn(b));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Choices in order of their experts: a histogram, a scan, and a scatter whose order
-// within an expert is the atomics' (every row is computed by itself, so no result
-// depends on it). An expert's rows are cut evenly into blocks of at most p.block.
-MOE_DEV void group_choices(const PrepareParams& p) {
-  __shared__ int count[kPrepareThreads], cursor[kPrepareThreads], sums[2][32];
-  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
-  count[i] = 0;
+// 16 elements of a row as whole numbers in f16.
+template <int DT>
+MOE_DEV void quantize16_f16(const void* x, int64_t i, const RowScale s, uint4& lo, uint4& hi) {
+  uint32_t o[8];
+  if constexpr (DT == MOE_DTYPE_S8) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(x) + i));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      o[2 * c] = int_pair_f16((int8_t)w[c], (int8_t)(w[c] >> 8));
+      o[2 * c + 1] = int_pair_f16((int8_t)(w[c] >> 16), (int8_t)(w[c] >> 24));
+    }
+  } else {
+    float v[16];
+    if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(x) + i, v);
+    else load16<DT>(x, i, v);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = int_pair_f16(quantize(v[2 * c], s), quantize(v[2 * c + 1], s));
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The scale of a row, found by one warp.
+template <int DT>
+MOE_DEV RowScale warp_row_scale(const void* x, int64_t row0, int nch, int lane) {
+  float v[16];
+  uint32_t m = 0;
+  for (int c = lane; c < nch; c += 32) {
+    if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(x) + row0 + 16 * c, v);
+    else load16<DT>(x, row0 + 16 * c, v);
+    m = max(m, amax_bits(v));
+  }
+  return row_scale(__reduce_max_sync(0xFFFFFFFFu, m));
+}
+
+constexpr int kPrepareThreads = 256;
+
+// Rows as whole numbers in f16, and their scales: one warp a row.
+template <int DT>
+__global__ void __launch_bounds__(kPrepareThreads) int8_prepare_kernel(const PrepareParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, nch = p.K / 16;
+  const int rows = p.num_rows ? min(p.rows, ldg_cg_s32(p.num_rows)) : p.rows;
+  constexpr int kW = kPrepareThreads / 32;
+  for (int64_t r = (int64_t)blockIdx.x * kW + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * kW) {
+    uint4* q = reinterpret_cast<uint4*>(p.q + r * p.K);
+    RowScale s = {};
+    if constexpr (DT != MOE_DTYPE_S8) s = warp_row_scale<DT>(p.x, r * p.stride, nch, lane);
+    for (int c = lane; c < nch; c += 32) quantize16_f16<DT>(p.x, r * p.stride + 16 * c, s, q[2 * c], q[2 * c + 1]);
+    if (lane == 0) p.scale[r] = DT == MOE_DTYPE_S8 ? p.x_scale[r] : s.scale;
+  }
+}
+
+// Choices in the order of their experts, and each one's token as whole numbers in f16 in
+// that order. Two launches over the same chunks of tokens: the first counts each chunk's
+// choices by expert; in the second every CTA adds the counts up for itself (which
+// rows its chunk's choices take), and copies its tokens to their rows, k each. Gathering the
+// rows inside the product instead took a copy of four rows at a time, whose issue alone
+// made the up product 683 us at T = 4096 (Qwen-shaped).
+struct GroupParams {
+  const void* x;             // [T][H]
+  const int* idx;            // [T][k]
+  int T, k, E, H;
+  int chunk, chunks;         // tokens of a CTA
+  int block, max_blocks;
+  int* chunk_counts;         // [chunks][E]
+  __half* q;                 // [rows][H]
+  float* scale;              // [rows]
+  int* pos;                  // [T][k]: grouped row, -1 where there is none
+  int4* blocks;
+  int* counts;               // [0]: blocks, [1]: grouped rows
+};
+
+constexpr int kGroupThreads = 1024;
+
+__global__ void __launch_bounds__(kGroupThreads) int8_count_kernel(const GroupParams p) {
+  __shared__ int count[MOE_INT8_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < p.E; e += kGroupThreads) count[e] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
   __syncthreads();
-  for (int a = i; a < p.choices; a += kPrepareThreads) {
+  const int64_t a0 = (int64_t)blockIdx.x * p.chunk * p.k;
+  const int64_t a1 = min(a0 + (int64_t)p.chunk * p.k, (int64_t)p.T * p.k);
+  for (int64_t a = a0 + threadIdx.x; a < a1; a += kGroupThreads) {
     const int e = __ldg(p.idx + a);
     if (e >= 0 && e < p.E) atomicAdd(&count[e], 1);
   }
   __syncthreads();
-  const int c = count[i], nb = (c + p.block - 1) / p.block;
+  for (int e = threadIdx.x; e < p.E; e += kGroupThreads) p.chunk_counts[(int64_t)blockIdx.x * p.E + e] = count[e];
+}
+
+// An expert's rows are cut evenly into blocks of at most p.block. Within an expert and a
+// chunk the order is the shared-memory atomics': every row is computed by itself, so no
+// result depends on it.
+template <int DT>
+__global__ void __launch_bounds__(kGroupThreads) int8_group_kernel(const GroupParams p) {
+  static_assert(kGroupThreads >= MOE_INT8_MAX_EXPERTS, "one thread an expert");
+  __shared__ int cursor[MOE_INT8_MAX_EXPERTS], all[MOE_INT8_MAX_EXPERTS], before[MOE_INT8_MAX_EXPERTS], sums[2][32];
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  all[i] = 0;
+  before[i] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  // several threads an expert where there are few experts: part q of n takes chunks q, q + n, ...
+  const int parts = max(1, kGroupThreads / p.E), part = i / p.E;
+  if (part < parts) {
+    const int e = i - part * p.E;
+    int sum = 0, own = 0;
+#pragma unroll 8
+    for (int c = part; c < p.chunks; c += parts) {
+      const int n = ldg_cg_s32(p.chunk_counts + (int64_t)c * p.E + e);
+      sum += n;
+      own += c < (int)blockIdx.x ? n : 0;
+    }
+    atomicAdd(&all[e], sum);
+    atomicAdd(&before[e], own);
+  }
+  __syncthreads();
+  const int c = i < p.E ? all[i] : 0, nb = (c + p.block - 1) / p.block;
   int rows = c, blocks = nb;   // inclusive scans
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -351,76 +450,38 @@ MOE_DEV void group_choices(const PrepareParams& p) {
   }
   __syncthreads();
   if (warp > 0) { rows += sums[0][warp - 1]; blocks += sums[1][warp - 1]; }
-  const int row0 = rows - c, b0 = blocks - nb;
-  cursor[i] = row0;
-  const int size = nb ? ((c + nb - 1) / nb + 15) & ~15 : 0;
-  for (int b = 0; b < nb; ++b)
-    if (b0 + b < p.max_blocks) p.blocks[b0 + b] = make_int4(i, row0 + b * size, min(size, c - b * size), 0);
-  if (i == kPrepareThreads - 1) { p.counts[0] = blocks; p.counts[1] = rows; }
+  const int row0 = rows - c;
+  cursor[i] = row0 + before[i];
+  if (blockIdx.x == 0) {
+    const int b0 = blocks - nb, size = nb ? ((c + nb - 1) / nb + 15) & ~15 : 0;
+    for (int b = 0; b < nb; ++b)
+      if (b0 + b < p.max_blocks) p.blocks[b0 + b] = make_int4(i, row0 + b * size, min(size, c - b * size), 0);
+    if (i == kGroupThreads - 1) { p.counts[0] = blocks; p.counts[1] = rows; }
+  }
   __syncthreads();
-  for (int a = i; a < p.choices; a += kPrepareThreads) {
-    const int e = __ldg(p.idx + a);
+  const int nch = p.H / 16;
+  const int t1 = min(p.T, ((int)blockIdx.x + 1) * p.chunk);
+  for (int t = blockIdx.x * p.chunk + warp; t < t1; t += kGroupThreads / 32) {
     int at = -1;
-    if (e >= 0 && e < p.E) {
-      at = atomicAdd(&cursor[e], 1);
-      p.perm[at] = a;
+    if (lane < p.k) {
+      const int e = __ldg(p.idx + (int64_t)t * p.k + lane);
+      if (e >= 0 && e < p.E) at = atomicAdd(&cursor[e], 1);
+      p.pos[(int64_t)t * p.k + lane] = at;
     }
-    p.pos[a] = at;
-  }
-}
-
-// Rows as whole numbers in f16, and their scales: one warp a row.
-template <int DT>
-__global__ void __launch_bounds__(kPrepareThreads) int8_prepare_kernel(const PrepareParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  int first = blockIdx.x, stride = gridDim.x;
-  if (p.idx) {
-    if (blockIdx.x == 0) {
-      group_choices(p);
-      return;
-    }
-    --first;
-    --stride;
-  }
-  const int lane = threadIdx.x & 31, nch = p.K / 16;
-  const int rows = p.num_rows ? min(p.rows, ldg_cg_s32(p.num_rows)) : p.rows;
-  for (int64_t r = (int64_t)first * 32 + (threadIdx.x >> 5); r < rows; r += (int64_t)stride * 32) {
-    uint4* q = reinterpret_cast<uint4*>(p.q + r * p.K);
-    if constexpr (DT == MOE_DTYPE_S8) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.x) + r * p.stride);
-      for (int c = lane; c < nch; c += 32) {
-        const uint4 u = __ldg(src + c);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[2 * i] = int_pair_f16((int8_t)w[i], (int8_t)(w[i] >> 8));
-          o[2 * i + 1] = int_pair_f16((int8_t)(w[i] >> 16), (int8_t)(w[i] >> 24));
+    const RowScale s = warp_row_scale<DT>(p.x, (int64_t)t * p.H, nch, lane);
+    if (at >= 0) p.scale[at] = s.scale;
+    for (int c0 = 0; c0 < nch; c0 += 32) {
+      const int ch = c0 + lane;
+      uint4 lo, hi;
+      if (ch < nch) quantize16_f16<DT>(p.x, (int64_t)t * p.H + 16 * ch, s, lo, hi);
+      for (int j = 0; j < p.k; ++j) {
+        const int to = __shfl_sync(0xFFFFFFFFu, at, j);
+        if (to >= 0 && ch < nch) {
+          uint4* q = reinterpret_cast<uint4*>(p.q + (int64_t)to * p.H) + 2 * ch;
+          q[0] = lo;
+          q[1] = hi;
         }
-        q[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
-        q[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      if (lane == 0) p.scale[r] = p.x_scale[r];
-    } else {
-      float v[16];
-      uint32_t m = 0;
-      for (int c = lane; c < nch; c += 32) {
-        if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(p.x) + r * p.stride + 16 * c, v);
-        else load16<DT>(p.x, r * p.stride + 16 * c, v);
-        m = max(m, amax_bits(v));
-      }
-      const RowScale s = row_scale(__reduce_max_sync(0xFFFFFFFFu, m));
-      for (int c = lane; c < nch; c += 32) {
-        if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(p.x) + r * p.stride + 16 * c, v);
-        else load16<DT>(p.x, r * p.stride + 16 * c, v);
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = int_pair_f16(quantize(v[2 * i], s), quantize(v[2 * i + 1], s));
-        q[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
-        q[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      if (lane == 0) p.scale[r] = s.scale;
     }
   }
 }
@@ -531,8 +592,8 @@ int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 constexpr int kStreamTokens = 8;
 
 cudaError_t launch_prepare(const PrepareParams& p, int dtype, int num_sms, cudaStream_t s) {
-  const int64_t blocks = ((int64_t)p.rows + 31) / 32;
-  const dim3 grid((unsigned)((blocks < 2 * num_sms ? blocks : 2 * num_sms) + (p.idx ? 1 : 0)));
+  const int64_t blocks = ((int64_t)p.rows + kPrepareThreads / 32 - 1) / (kPrepareThreads / 32);
+  const dim3 grid((unsigned)(blocks < 16 * num_sms ? blocks : 16 * num_sms));
   switch (dtype) {
     case MOE_DTYPE_F32: return launch_pdl(int8_prepare_kernel<MOE_DTYPE_F32>, grid, kPrepareThreads, 0, s, p);
     case MOE_DTYPE_BF16: return launch_pdl(int8_prepare_kernel<MOE_DTYPE_BF16>, grid, kPrepareThreads, 0, s, p);
@@ -585,8 +646,8 @@ cudaError_t launch_matmul_tensor(const StreamParams& p, int x_dtype, uint8_t* ws
 
 // Scratch of the experts' call. y takes h's place, which is dead by then.
 struct ExpertsWorkspace {
-  int64_t h, q, x_scale, hq, h_scale, perm, pos, blocks, counts, bytes;
-  int block, max_blocks;
+  int64_t h, q, x_scale, hq, h_scale, chunk_counts, pos, blocks, counts, bytes;
+  int block, max_blocks, chunk, chunks;
 };
 ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T) {
   ExpertsWorkspace w = {};
@@ -600,14 +661,17 @@ ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T
   const int64_t want = (rows * 3 / (2 * touched) + 15) / 16 * 16;
   w.block = (int)(want < 32 ? 32 : want > kMaxBlock ? kMaxBlock : want);
   w.max_blocks = (int)(touched + rows / w.block);
+  // a warp a token and CTA at a time; no more CTAs than SMs
+  w.chunk = (int)((T + 127) / 128 > 32 ? (T + 127) / 128 : 32);
+  w.chunks = (int)((T + w.chunk - 1) / w.chunk);
   int64_t at = 0;
   const auto take = [&at](int64_t bytes) { const int64_t o = at; at += pad256(bytes); return o; };
   w.h = take(rows * (I * 4 > H * 2 ? I * 4 : H * 2));
-  w.q = take(T * H * 2);
-  w.x_scale = take(T * 4);
+  w.q = take(rows * H * 2);
+  w.x_scale = take(rows * 4);
   w.hq = take(rows * I * 2);
   w.h_scale = take(rows * 4);
-  w.perm = take(rows * 4);
+  w.chunk_counts = take((int64_t)w.chunks * c->num_experts * 4);
   w.pos = take(rows * 4);
   w.blocks = take((int64_t)w.max_blocks * 16);
   w.counts = take(8);
@@ -619,23 +683,27 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
                                   uint8_t* ws, int num_sms, cudaStream_t s) {
   const ExpertsWorkspace w = experts_workspace(cfg, p.T);
   const int rows = p.T * p.k;
-  PrepareParams a = {};
+  GroupParams a = {};
   a.x = p.x;
-  a.stride = p.H;
-  a.rows = p.T;
-  a.K = p.H;
-  a.q = (__half*)(ws + w.q);
-  a.scale = (float*)(ws + w.x_scale);
   a.idx = p.idx;
-  a.choices = rows;
+  a.T = p.T;
+  a.k = p.k;
   a.E = p.E;
+  a.H = p.H;
+  a.chunk = w.chunk;
+  a.chunks = w.chunks;
   a.block = w.block;
   a.max_blocks = w.max_blocks;
-  a.perm = (int*)(ws + w.perm);
+  a.chunk_counts = (int*)(ws + w.chunk_counts);
+  a.q = (__half*)(ws + w.q);
+  a.scale = (float*)(ws + w.x_scale);
   a.pos = (int*)(ws + w.pos);
   a.blocks = (int4*)(ws + w.blocks);
   a.counts = (int*)(ws + w.counts);
-  cudaError_t e = launch_prepare(a, x_dtype, num_sms, s);
+  cudaError_t e = launch_pdl(int8_count_kernel, dim3(w.chunks), kGroupThreads, 0, s, a);
+  if (e != cudaSuccess) return e;
+  e = x_dtype == MOE_DTYPE_BF16 ? launch_pdl(int8_group_kernel<MOE_DTYPE_BF16>, dim3(w.chunks), kGroupThreads, 0, s, a)
+                                : launch_pdl(int8_group_kernel<MOE_DTYPE_F16>, dim3(w.chunks), kGroupThreads, 0, s, a);
   if (e != cudaSuccess) return e;
 
   GemmArgs g = {};
@@ -643,7 +711,7 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   g.a_rows = (int64_t)p.E * 2 * p.I;
   g.a_stride = p.H;
   g.b = a.q;
-  g.b_rows = p.T;
+  g.b_rows = rows;
   g.b_stride = p.H;
   g.K = p.H;
   g.channels = p.I;
@@ -652,9 +720,6 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   g.blocks = a.blocks;
   g.num_blocks = a.counts;
   g.max_blocks = w.max_blocks;
-  g.T = p.T;
-  g.perm = a.perm;
-  g.k = p.k;
   g.row_scale = a.scale;
   g.w_scale = p.gate_up_scale;
   g.out = ws + w.h;

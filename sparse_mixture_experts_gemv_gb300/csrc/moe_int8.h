@@ -27,10 +27,8 @@ struct GemmArgs {
   const int4* blocks;
   const int* num_blocks;
   int max_blocks;
-  int T;                      // dense: tokens; up: tokens of x
-  const int* perm;            // up: choice t * k + j at each grouped row
-  int k;
-  const float* row_scale;     // dense, up: scale of each token
+  int T;                      // dense: tokens
+  const float* row_scale;     // dense, up: scale of each row of b
   const float* w_scale;       // dense: [N]; up: [E][2I]
   void* out;                  // dense: [T][N] out_dtype; up: fp32 h [rows][I]; down: f16 y [rows][H]
   int out_dtype;

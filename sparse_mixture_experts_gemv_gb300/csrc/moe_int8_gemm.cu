@@ -17,7 +17,7 @@
 // expert the MMA does no more than they need, and the weight stream bounds it.
 //
 // One persistent CTA an SM, warp-specialised:
-//   warp 0        weights by TMA              warp 2  tokens by TMA (gathered rows: up)
+//   warp 0        weights by TMA              warp 2  tokens by TMA
 //   warp 1        issues the MMAs             warp 3  idle
 //   warps 4-11    converters: two groups of four, alternate steps of 64 along K
 //   warps 12-15   epilogue of the previous tile while the next one accumulates
@@ -60,8 +60,6 @@ struct Params {
   int tiles_t;               // dense: token tiles
   int T, block, channels, rows_per_group;
   int steps, stages, stage_bytes;
-  const int* perm;
-  int k;
   const float* row_scale;
   const float* w_scale;
   void* out;
@@ -115,6 +113,21 @@ MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp, the same one each time. Roles run as whole warps and elect a
+// lane around what it issues: the compiler then keeps addresses and descriptors in uniform
+// registers (four MMAs and a commit of one thread in a divergent branch issue in 300
+// cycles, elected in 165).
+MOE_DEV bool elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+// mbar_wait by a whole warp, which goes on or gives up as one.
+MOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err, abort));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
 MOE_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -123,18 +136,10 @@ MOE_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, 
       :: "r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// Four rows (any four of the matrix) of one 128-byte column block.
-MOE_DEV void tma_gather4(void* dst, const CUtensorMap* map, int c0, const int4 rows, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-      :: "r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w),
-         "r"(smem_u32(bar)) : "memory");
-}
-
 template <int KIND>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Params p) {
+int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ CUtensorMap map_b64, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   // stage: tokens (block x 128 bytes, whole 1024-byte swizzle atoms) and raw weights behind all of them
@@ -145,8 +150,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + 4 * kMaxBlock);
   uint64_t* empty = full + kMaxStages;
   uint64_t* a_full = empty + kMaxStages;
-  uint64_t* a_empty = a_full + kSlots;
-  uint64_t* d_full = a_empty + kSlots;
+  uint64_t* d_full = a_full + kSlots;
   uint64_t* d_empty = d_full + 2;
   uint64_t* drain = d_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -159,10 +163,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&a_full[s], 4);
-      mbar_init(&a_empty[s], 1);
-    }
+    for (int s = 0; s < kSlots; ++s) mbar_init(&a_full[s], 4);
     for (int a = 0; a < 2; ++a) {
       mbar_init(&d_full[a], 1);
       mbar_init(&d_empty[a], 4);
@@ -172,6 +173,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     fence_barrier_init();
     prefetch_tmap(&map_a);
     prefetch_tmap(&map_b);
+    prefetch_tmap(&map_b64);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -193,94 +195,82 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 
   if (warp == 0) {
     // ------------------------------------------------------------- weights
-    if (lane == 0) {
-      uint32_t it = 0;
-      int s = 0, ph = 1;
-      bool stop = false;
-      for (int tile = blockIdx.x; tile < total && !stop && !*abort_flag; tile += gridDim.x) {
-        const Tile t = decode<KIND>(p, tile);
-        const int r0 = KIND == kUp ? t.e * p.rows_per_group + t.mt * 64 : t.e * p.rows_per_group + t.mt * kChannels;
-        const int r1 = KIND == kUp ? r0 + p.channels : r0 + 64;   // up: 64 gate rows, then their up rows
-        for (int ks = 0; ks < p.steps; ++ks, ++it) {
-          if (!mbar_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
+    uint32_t it = 0;
+    int s = 0, ph = 1;
+    bool stop = false;
+    for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
+      const Tile t = decode<KIND>(p, tile);
+      const int r0 = KIND == kUp ? t.e * p.rows_per_group + t.mt * 64 : t.e * p.rows_per_group + t.mt * kChannels;
+      const int r1 = KIND == kUp ? r0 + p.channels : r0 + 64;   // up: 64 gate rows, then their up rows
+      for (int ks = 0; ks < p.steps; ++ks, ++it) {
+        if (!warp_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
+        if (elect()) {
           mbar_arrive_expect_tx(&full[s], (uint32_t)(kRawBytes + t.n * 128));
           tma_load_2d(s_raw + s * kRawBytes, &map_a, ks * kStep, r0, &full[s]);
           tma_load_2d(s_raw + s * kRawBytes + kRawBytes / 2, &map_a, ks * kStep, r1, &full[s]);
-          if (++s == p.stages) { s = 0; ph ^= 1; }
         }
+        __syncwarp();
+        if (++s == p.stages) { s = 0; ph ^= 1; }
       }
-      if (*abort_flag) {   // let copies in flight land before the CTA exits
-        for (uint32_t q = it > (uint32_t)p.stages ? it - p.stages : 0; q < it; ++q)
-          mbar_wait(&full[q % p.stages], (q / p.stages) & 1, err, abort_flag, 20000000LL, false);
-      }
+    }
+    if (lane == 0 && *abort_flag) {   // let copies in flight land before the CTA exits
+      for (uint32_t q = it > (uint32_t)p.stages ? it - p.stages : 0; q < it; ++q)
+        mbar_wait(&full[q % p.stages], (q / p.stages) & 1, err, abort_flag, 20000000LL, false);
     }
   } else if (warp == 2) {
     // -------------------------------------------------------------- tokens
+    // in boxes of 64 rows and, for the rest, 16: a copy costs its issue as much as its bytes
     int s = 0, ph = 1;
     bool stop = false;
-    for (int tile = blockIdx.x; tile < total && !stop && !*abort_flag; tile += gridDim.x) {
+    for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = decode<KIND>(p, tile);
-      int4 rows[2] = {};
-      if (KIND == kUp) {   // lane l gathers rows 4l.. and 4(l + 32)..; rows past the block's end repeat its last
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = 4 * (lane + 32 * i), last = t.row0 + t.rows - 1;
-          if (c < t.n) {
-            rows[i].x = ldg_cg_s32(p.perm + min(t.row0 + c, last)) / p.k;
-            rows[i].y = ldg_cg_s32(p.perm + min(t.row0 + c + 1, last)) / p.k;
-            rows[i].z = ldg_cg_s32(p.perm + min(t.row0 + c + 2, last)) / p.k;
-            rows[i].w = ldg_cg_s32(p.perm + min(t.row0 + c + 3, last)) / p.k;
-          }
-        }
-      }
       for (int ks = 0; ks < p.steps; ++ks) {
-        if (!mbar_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
-        uint8_t* dst = s_b + s * b_bytes;
-        if (KIND == kUp) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c = 4 * (lane + 32 * i);
-            if (c < t.n) tma_gather4(dst + c * 128, &map_b, ks * kStep, rows[i], &full[s]);
-          }
-        } else if (lane < t.n / 16) {
-          tma_load_2d(dst + lane * 2048, &map_b, ks * kStep, t.row0 + lane * 16, &full[s]);
+        if (!warp_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
+        if (elect()) {
+          uint8_t* dst = s_b + s * b_bytes;
+          int r = 0;
+          for (; r + 64 <= t.n; r += 64) tma_load_2d(dst + r * 128, &map_b64, ks * kStep, t.row0 + r, &full[s]);
+          for (; r < t.n; r += 16) tma_load_2d(dst + r * 128, &map_b, ks * kStep, t.row0 + r, &full[s]);
         }
+        __syncwarp();
         if (++s == p.stages) { s = 0; ph ^= 1; }
       }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
-      int s = 0, ph = 0;
-      uint32_t it = 0, tc = 0;
-      for (int tile = blockIdx.x; tile < total && !*abort_flag; tile += gridDim.x, ++tc) {
-        const Tile t = decode<KIND>(p, tile);
-        // f16 x f16 -> fp32, both K-major, 128 x n
-        const uint32_t idesc = (1u << 4) | ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kChannels >> 4) << 24);
-        const int ab = tc & 1;
-        if (!mbar_wait(&d_empty[ab], ((tc >> 1) & 1) ^ 1, err, abort_flag)) break;
+    int s = 0, ph = 0;
+    uint32_t it = 0, tc = 0;
+    bool stop = false;
+    const uint32_t b_base = smem_u32(s_b);
+    for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x, ++tc) {
+      const Tile t = decode<KIND>(p, tile);
+      // f16 x f16 -> fp32, both K-major, 128 x n
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kChannels >> 4) << 24);
+      const int ab = tc & 1;
+      if (!warp_wait(&d_empty[ab], ((tc >> 1) & 1) ^ 1, err, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + ab * kMaxBlock;
+      for (int ks = 0; ks < p.steps; ++ks, ++it) {
+        const int slot = it & (kSlots - 1);
+        if (!warp_wait(&full[s], ph, err, abort_flag) ||
+            !warp_wait(&a_full[slot], (it / kSlots) & 1, err, abort_flag)) { stop = true; break; }
         tc_fence_after();
-        const uint32_t d = tmem + ab * kMaxBlock;
-        bool ok = true;
-        for (int ks = 0; ks < p.steps; ++ks, ++it) {
-          const int slot = it & (kSlots - 1);
-          if (!mbar_wait(&full[s], ph, err, abort_flag) ||
-              !mbar_wait(&a_full[slot], (it / kSlots) & 1, err, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t a0 = tmem + kSlotBase + slot * kSlotCols, b0 = smem_u32(s_b + s * b_bytes);
+        const uint32_t a0 = tmem + kSlotBase + slot * kSlotCols;
+        const uint64_t bdesc = smem_desc_sw128(b_base + s * b_bytes);
+        if (elect()) {
 #pragma unroll
-          for (int kk = 0; kk < kStep / 16; ++kk)
-            mma_f16_ts(d, a0 + kk * 8, smem_desc_sw128(b0 + kk * 32), idesc, (ks | kk) != 0 ? 1u : 0u);
-          mma_commit(&empty[s]);      // the converters have read this stage's weights by now too
-          mma_commit(&a_empty[slot]);
-          if (++s == p.stages) { s = 0; ph ^= 1; }
+          for (int kk = 0; kk < kStep / 16; ++kk)   // 16 of K: 8 columns, and 32 bytes (2 in the descriptor)
+            mma_f16_ts(d, a0 + kk * 8, bdesc + kk * 2, idesc, (ks | kk) != 0 ? 1u : 0u);
+          mma_commit(&empty[s]);   // frees the stage and, since the converters wait on it too, the slot
+          if (ks == p.steps - 1) mma_commit(&d_full[ab]);
         }
-        if (!ok) break;
-        mma_commit(&d_full[ab]);
+        __syncwarp();
+        if (++s == p.stages) { s = 0; ph ^= 1; }
       }
-      mma_commit(drain);   // all MMAs complete before tensor memory is released
-      mbar_wait(drain, 0, err, abort_flag, 2000000000LL, false);
     }
+    if (elect()) mma_commit(drain);   // all MMAs complete before tensor memory is released
+    __syncwarp();
+    mbar_wait(drain, 0, err, abort_flag, 2000000000LL, false);
   } else if (warp >= 4 && warp < 12) {
     // ---------------------------------------------------------- converters
     const int group = (warp - 4) >> 2, quad = warp & 3;
@@ -291,11 +281,12 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     uint32_t it = 0;
     int s = 0, ph = 0;
+    int es = p.stages - kSlots, eph = 1;   // stage and phase of the step kSlots before, whose MMAs read this slot
     bool stop = false;
-    for (int tile = blockIdx.x; tile < total && !stop && !*abort_flag; tile += gridDim.x) {
+    for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       for (int ks = 0; ks < p.steps; ++ks, ++it) {
         if ((int)(it & 1) == group) {
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], ph, err, abort_flag))) { stop = true; break; }
+          if (!warp_wait(&full[s], ph, err, abort_flag)) { stop = true; break; }
           const uint8_t* src = s_raw + s * kRawBytes + row * kStep;
           uint32_t r[32];
 #pragma unroll
@@ -307,10 +298,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             s8x4_to_f16(w.w, r[8 * c + 6], r[8 * c + 7]);
           }
           const int slot = it & (kSlots - 1);
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&a_empty[slot], ((it / kSlots) & 1) ^ 1, err, abort_flag))) {
-            stop = true;
-            break;
-          }
+          if (it >= kSlots && !warp_wait(&empty[es], eph, err, abort_flag)) { stop = true; break; }
           tc_fence_after();
           tmem_st32(tmem + lanes + kSlotBase + slot * kSlotCols, r);
           tc_fence_before();
@@ -318,6 +306,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           if (lane == 0) mbar_arrive(&a_full[slot]);
         }
         if (++s == p.stages) { s = 0; ph ^= 1; }
+        if (++es == p.stages) { es = 0; eph ^= 1; }
       }
     }
   } else if (warp >= 12) {
@@ -325,15 +314,12 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     const int quad = warp & 3;
     float* cs = s_scale + quad * kMaxBlock;   // the warp's copy of the tile's token scales
     uint32_t tc = 0;
-    for (int tile = blockIdx.x; tile < total && !*abort_flag; tile += gridDim.x, ++tc) {
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++tc) {
       const Tile t = decode<KIND>(p, tile);
       const int ab = tc & 1;
       __syncwarp();
       if (KIND != kDown) {
-        for (int c = lane; c < t.rows; c += 32) {
-          const int row = KIND == kUp ? ldg_cg_s32(p.perm + t.row0 + c) / p.k : t.row0 + c;
-          cs[c] = ldg_cg_f32(p.row_scale + row);
-        }
+        for (int c = lane; c < t.rows; c += 32) cs[c] = ldg_cg_f32(p.row_scale + t.row0 + c);
       }
       const int ch = KIND == kUp ? t.mt * 64 + quad * 16 + (lane & 15) : t.mt * kChannels + quad * 32 + lane;
       const bool in = ch < p.channels;
@@ -344,8 +330,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         w1 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + p.channels + ch);
       }
       __syncwarp();
-      const bool ok = mbar_wait(&d_full[ab], (tc >> 1) & 1, err, abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (!warp_wait(&d_full[ab], (tc >> 1) & 1, err, abort_flag)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ab * kMaxBlock + ((uint32_t)(quad * 32) << 16);
       for (int c0 = 0; c0 < t.rows; c0 += 32) {
@@ -425,8 +410,8 @@ cudaError_t encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, i
 }
 
 template <int KIND>
-cudaError_t launch_kind(const CUtensorMap& ma, const CUtensorMap& mb, const Params& p, int grid, size_t smem,
-                        cudaStream_t s) {
+cudaError_t launch_kind(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mb64, const Params& p, int grid,
+                        size_t smem, cudaStream_t s) {
   static bool allowed[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -447,17 +432,20 @@ cudaError_t launch_kind(const CUtensorMap& ma, const CUtensorMap& mb, const Para
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<KIND>, ma, mb, p);
+  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<KIND>, ma, mb, mb64, p);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStream_t s) {
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mb64;
   cudaError_t e = encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, a.a_rows, a.K, a.a_stride, kStep, 64,
                          CU_TENSOR_MAP_SWIZZLE_64B);
   if (e == cudaSuccess)
-    e = encode(&mb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.b, a.b_rows, a.K, a.b_stride * 2, kStep, kind == kUp ? 1 : 16,
+    e = encode(&mb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.b, a.b_rows, a.K, a.b_stride * 2, kStep, 16,
+               CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e == cudaSuccess)
+    e = encode(&mb64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.b, a.b_rows, a.K, a.b_stride * 2, kStep, 64,
                CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   Params p = {};
@@ -476,8 +464,6 @@ cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStrea
   p.stages = kStageBudget / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.stages &= ~1;   // even: a converter group meets the same stages again, every phase of them
-  p.perm = a.perm;
-  p.k = a.k;
   p.row_scale = a.row_scale;
   p.w_scale = a.w_scale;
   p.out = a.out;
@@ -487,9 +473,9 @@ cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStrea
   const int64_t tiles = (int64_t)p.tiles_m * (kind == kDense ? p.tiles_t : a.max_blocks);
   const int grid = (int)(tiles < num_sms ? tiles : num_sms);
   switch (kind) {
-    case kDense: return launch_kind<kDense>(ma, mb, p, grid, smem, s);
-    case kUp: return launch_kind<kUp>(ma, mb, p, grid, smem, s);
-    default: return launch_kind<kDown>(ma, mb, p, grid, smem, s);
+    case kDense: return launch_kind<kDense>(ma, mb, mb64, p, grid, smem, s);
+    case kUp: return launch_kind<kUp>(ma, mb, mb64, p, grid, smem, s);
+    default: return launch_kind<kDown>(ma, mb, mb64, p, grid, smem, s);
   }
 }
 
