@@ -48,7 +48,7 @@ constexpr int kSlotCols = kStep / 2;
 constexpr int kSlotBase = 2 * kMaxBlock;  // their first column
 constexpr int kGemmThreads = 512;
 constexpr int kStageBudget = 200 * 1024;  // shared memory of all stages
-constexpr int kFixedSmem = 1024 /*align*/ + 4 * kMaxBlock * 4 /*scales*/ + 1024 /*barriers*/;
+constexpr int kFixedSmem = 1024 /*align*/ + 4 * kMaxBlock * 4 /*scales*/ + 4 * 2048 /*turned results*/ + 1024 /*barriers*/;
 
 __device__ int g_gemm_error;              // MOE_ERR_TIMEOUT once a bounded wait ran out
 
@@ -64,7 +64,15 @@ struct Params {
   const float* w_scale;
   void* out;
   int out_dtype;
+  int wide;                  // dense: 16-bit results whose rows are 16-byte aligned
   float factor;
+};
+
+// A copy's issue costs about as much as 8 KB, so that every step is one copy of weights (up: two) and one
+// of tokens: a map for each number of rows a tile can have.
+struct Maps {
+  CUtensorMap a;
+  CUtensorMap b[kMaxBlock / 16];   // boxes of 16, 32, ... rows; those a launch can use are filled in
 };
 
 struct Tile {
@@ -138,8 +146,7 @@ MOE_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, 
 
 template <int KIND>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                 const __grid_constant__ CUtensorMap map_b64, const Params p) {
+int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   // stage: tokens (block x 128 bytes, whole 1024-byte swizzle atoms) and raw weights behind all of them
@@ -147,7 +154,8 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   uint8_t* s_b = smem;
   uint8_t* s_raw = smem + p.stages * b_bytes;
   float* s_scale = reinterpret_cast<float*>(s_raw + p.stages * kRawBytes);   // [4][kMaxBlock]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + 4 * kMaxBlock);
+  uint16_t* s_turn = reinterpret_cast<uint16_t*>(s_scale + 4 * kMaxBlock);   // [4][1024]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_turn + 4 * 1024);
   uint64_t* empty = full + kMaxStages;
   uint64_t* a_full = empty + kMaxStages;
   uint64_t* d_full = a_full + kSlots;
@@ -171,9 +179,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    prefetch_tmap(&map_a);
-    prefetch_tmap(&map_b);
-    prefetch_tmap(&map_b64);
+    prefetch_tmap(&maps.a);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -201,13 +207,13 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = decode<KIND>(p, tile);
       const int r0 = KIND == kUp ? t.e * p.rows_per_group + t.mt * 64 : t.e * p.rows_per_group + t.mt * kChannels;
-      const int r1 = KIND == kUp ? r0 + p.channels : r0 + 64;   // up: 64 gate rows, then their up rows
       for (int ks = 0; ks < p.steps; ++ks, ++it) {
         if (!warp_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
         if (elect()) {
           mbar_arrive_expect_tx(&full[s], (uint32_t)(kRawBytes + t.n * 128));
-          tma_load_2d(s_raw + s * kRawBytes, &map_a, ks * kStep, r0, &full[s]);
-          tma_load_2d(s_raw + s * kRawBytes + kRawBytes / 2, &map_a, ks * kStep, r1, &full[s]);
+          tma_load_2d(s_raw + s * kRawBytes, &maps.a, ks * kStep, r0, &full[s]);
+          if (KIND == kUp)   // 64 gate rows, then their up rows
+            tma_load_2d(s_raw + s * kRawBytes + kRawBytes / 2, &maps.a, ks * kStep, r0 + p.channels, &full[s]);
         }
         __syncwarp();
         if (++s == p.stages) { s = 0; ph ^= 1; }
@@ -219,19 +225,14 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     }
   } else if (warp == 2) {
     // -------------------------------------------------------------- tokens
-    // in boxes of 64 rows and, for the rest, 16: a copy costs its issue as much as its bytes
     int s = 0, ph = 1;
     bool stop = false;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = decode<KIND>(p, tile);
+      const CUtensorMap* map = &maps.b[t.n / 16 - 1];
       for (int ks = 0; ks < p.steps; ++ks) {
         if (!warp_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
-        if (elect()) {
-          uint8_t* dst = s_b + s * b_bytes;
-          int r = 0;
-          for (; r + 64 <= t.n; r += 64) tma_load_2d(dst + r * 128, &map_b64, ks * kStep, t.row0 + r, &full[s]);
-          for (; r < t.n; r += 16) tma_load_2d(dst + r * 128, &map_b, ks * kStep, t.row0 + r, &full[s]);
-        }
+        if (elect()) tma_load_2d(s_b + s * b_bytes, map, ks * kStep, t.row0, &full[s]);
         __syncwarp();
         if (++s == p.stages) { s = 0; ph ^= 1; }
       }
@@ -313,6 +314,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3;
     float* cs = s_scale + quad * kMaxBlock;   // the warp's copy of the tile's token scales
+    uint16_t* turn = s_turn + quad * 1024;    // 32 tokens x 32 channels
     uint32_t tc = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++tc) {
       const Tile t = decode<KIND>(p, tile);
@@ -352,12 +354,24 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
               dst[(int64_t)2 * i * p.channels] = swiglu((upper ? got : keep) * xs * w0, (upper ? keep : got) * xs * w1);
             }
           }
-        } else if (KIND == kDown) {
-          uint16_t* dst = static_cast<uint16_t*>(p.out) + ((int64_t)t.row0 + c0) * p.channels + ch;
+        } else if (KIND == kDown || p.wide) {
+          // 16-bit results: turned in shared memory, so that a token's 32 channels leave in 16-byte pieces
+          // (stored as they are, 2 bytes a lane, a tile of 192 tokens took 26,000 cycles)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (in && i < nc)
-              dst[(int64_t)i * p.channels] = __half_as_ushort(__float2half_rn(__uint_as_float(v[i]) * p.factor));
+          for (int i = 0; i < 32; ++i) {
+            const float f = KIND == kDown ? __uint_as_float(v[i]) * p.factor
+                                          : __uint_as_float(v[i]) * cs[min(c0 + i, kMaxBlock - 1)] * w0;
+            turn[i * 32 + lane] = KIND == kDown ? __half_as_ushort(__float2half_rn(f)) : to_16(p.out_dtype, f);
+          }
+          __syncwarp();
+          const int ch8 = t.mt * kChannels + quad * 32 + (lane & 3) * 8;
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + ((int64_t)t.row0 + c0 + (lane >> 2)) * p.channels + ch8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (ch8 < p.channels && 8 * i + (lane >> 2) < nc)
+              *reinterpret_cast<uint4*>(dst + (int64_t)8 * i * p.channels) =
+                  *reinterpret_cast<const uint4*>(turn + (8 * i + (lane >> 2)) * 32 + (lane & 3) * 8);
+          __syncwarp();
         } else {
           const int64_t at = ((int64_t)t.row0 + c0) * p.channels + ch;
 #pragma unroll
@@ -410,8 +424,7 @@ cudaError_t encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, i
 }
 
 template <int KIND>
-cudaError_t launch_kind(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mb64, const Params& p, int grid,
-                        size_t smem, cudaStream_t s) {
+cudaError_t launch_kind(const Maps& maps, const Params& p, int grid, size_t smem, cudaStream_t s) {
   static bool allowed[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -432,21 +445,20 @@ cudaError_t launch_kind(const CUtensorMap& ma, const CUtensorMap& mb, const CUte
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<KIND>, ma, mb, mb64, p);
+  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<KIND>, maps, p);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStream_t s) {
-  CUtensorMap ma, mb, mb64;
-  cudaError_t e = encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, a.a_rows, a.K, a.a_stride, kStep, 64,
-                         CU_TENSOR_MAP_SWIZZLE_64B);
-  if (e == cudaSuccess)
-    e = encode(&mb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.b, a.b_rows, a.K, a.b_stride * 2, kStep, 16,
-               CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e == cudaSuccess)
-    e = encode(&mb64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.b, a.b_rows, a.K, a.b_stride * 2, kStep, 64,
-               CU_TENSOR_MAP_SWIZZLE_128B);
+  Maps maps = {};
+  cudaError_t e = encode(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, a.a_rows, a.K, a.a_stride, kStep,
+                         kind == kUp ? 64 : kChannels, CU_TENSOR_MAP_SWIZZLE_64B);
+  const int tail = kind == kDense ? ((a.T - 1) % a.block + 16) / 16 * 16 : 0;   // rows of the last tile
+  for (int n = 16; n <= a.block && e == cudaSuccess; n += 16)
+    if (kind != kDense || n == a.block || n == tail)
+      e = encode(&maps.b[n / 16 - 1], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.b, a.b_rows, a.K, a.b_stride * 2, kStep, n,
+                 CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   Params p = {};
   p.blocks = a.blocks;
@@ -468,14 +480,15 @@ cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStrea
   p.w_scale = a.w_scale;
   p.out = a.out;
   p.out_dtype = a.out_dtype;
+  p.wide = a.out_dtype != MOE_DTYPE_F32 && a.channels % 8 == 0 && !((uintptr_t)a.out & 15);
   p.factor = a.factor;
   const size_t smem = (size_t)p.stages * p.stage_bytes + kFixedSmem;
   const int64_t tiles = (int64_t)p.tiles_m * (kind == kDense ? p.tiles_t : a.max_blocks);
   const int grid = (int)(tiles < num_sms ? tiles : num_sms);
   switch (kind) {
-    case kDense: return launch_kind<kDense>(ma, mb, mb64, p, grid, smem, s);
-    case kUp: return launch_kind<kUp>(ma, mb, mb64, p, grid, smem, s);
-    default: return launch_kind<kDown>(ma, mb, mb64, p, grid, smem, s);
+    case kDense: return launch_kind<kDense>(maps, p, grid, smem, s);
+    case kUp: return launch_kind<kUp>(maps, p, grid, smem, s);
+    default: return launch_kind<kDown>(maps, p, grid, smem, s);
   }
 }
 
