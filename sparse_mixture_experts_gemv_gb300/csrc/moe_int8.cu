@@ -299,7 +299,8 @@ struct PrepareParams {
   const float* x_scale;   // S8 alone
   int rows, K;
   const int* num_rows;    // rows there really are, or NULL
-  __half* q;              // [rows][K] whole numbers
+  int K64;                // K rounded up to 64
+  __half* q;              // [rows][K64] whole numbers, zeros behind K
   float* scale;           // [rows]
 };
 
@@ -355,10 +356,15 @@ __global__ void __launch_bounds__(kPrepareThreads) int8_prepare_kernel(const Pre
   const int rows = p.num_rows ? min(p.rows, ldg_cg_s32(p.num_rows)) : p.rows;
   constexpr int kW = kPrepareThreads / 32;
   for (int64_t r = (int64_t)blockIdx.x * kW + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * kW) {
-    uint4* q = reinterpret_cast<uint4*>(p.q + r * p.K);
+    uint4* q = reinterpret_cast<uint4*>(p.q + r * p.K64);
     RowScale s = {};
     if constexpr (DT != MOE_DTYPE_S8) s = warp_row_scale<DT>(p.x, r * p.stride, nch, lane);
-    for (int c = lane; c < nch; c += 32) quantize16_f16<DT>(p.x, r * p.stride + 16 * c, s, q[2 * c], q[2 * c + 1]);
+    for (int c = lane; c < p.K64 / 16; c += 32) {
+      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+      if (c < nch) quantize16_f16<DT>(p.x, r * p.stride + 16 * c, s, lo, hi);
+      q[2 * c] = lo;
+      q[2 * c + 1] = hi;
+    }
     if (lane == 0) p.scale[r] = DT == MOE_DTYPE_S8 ? p.x_scale[r] : s.scale;
   }
 }
@@ -372,11 +378,11 @@ __global__ void __launch_bounds__(kPrepareThreads) int8_prepare_kernel(const Pre
 struct GroupParams {
   const void* x;             // [T][H]
   const int* idx;            // [T][k]
-  int T, k, E, H;
+  int T, k, E, H, H64;       // H64: H rounded up to 64
   int chunk, chunks;         // tokens of a CTA
   int block, max_blocks;
   int* chunk_counts;         // [chunks][E]
-  __half* q;                 // [rows][H]
+  __half* q;                 // [rows][H64], zeros behind H
   float* scale;              // [rows]
   int* pos;                  // [T][k]: grouped row, -1 where there is none
   int4* blocks;
@@ -470,14 +476,14 @@ __global__ void __launch_bounds__(kGroupThreads) int8_group_kernel(const GroupPa
     }
     const RowScale s = warp_row_scale<DT>(p.x, (int64_t)t * p.H, nch, lane);
     if (at >= 0) p.scale[at] = s.scale;
-    for (int c0 = 0; c0 < nch; c0 += 32) {
+    for (int c0 = 0; c0 < p.H64 / 16; c0 += 32) {
       const int ch = c0 + lane;
-      uint4 lo, hi;
+      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
       if (ch < nch) quantize16_f16<DT>(p.x, (int64_t)t * p.H + 16 * ch, s, lo, hi);
       for (int j = 0; j < p.k; ++j) {
         const int to = __shfl_sync(0xFFFFFFFFu, at, j);
-        if (to >= 0 && ch < nch) {
-          uint4* q = reinterpret_cast<uint4*>(p.q + (int64_t)to * p.H) + 2 * ch;
+        if (to >= 0 && ch < p.H64 / 16) {
+          uint4* q = reinterpret_cast<uint4*>(p.q + (int64_t)to * p.H64) + 2 * ch;
           q[0] = lo;
           q[1] = hi;
         }
@@ -587,6 +593,7 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 int dtype_size(int d) { return d == MOE_DTYPE_S8 ? 1 : d == MOE_DTYPE_F32 ? 4 : 2; }
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
+int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
 // Tokens up to which the weights are streamed through the dot-product units.
 constexpr int kStreamTokens = 8;
@@ -608,7 +615,7 @@ struct MatmulWorkspace {
 MatmulWorkspace matmul_workspace(int64_t T, int64_t K) {
   MatmulWorkspace w = {};
   if (T <= kStreamTokens) return w;
-  w.scale = pad256(T * K * 2);
+  w.scale = pad256(T * pad64(K) * 2);
   w.bytes = w.scale + pad256(T * 4);
   return w;
 }
@@ -621,6 +628,7 @@ cudaError_t launch_matmul_tensor(const StreamParams& p, int x_dtype, uint8_t* ws
   a.x_scale = p.x_scale;
   a.rows = p.T;
   a.K = p.K;
+  a.K64 = (int)pad64(p.K);
   a.q = (__half*)(ws + w.q);
   a.scale = (float*)(ws + w.scale);
   cudaError_t e = launch_prepare(a, x_dtype, num_sms, s);
@@ -631,7 +639,7 @@ cudaError_t launch_matmul_tensor(const StreamParams& p, int x_dtype, uint8_t* ws
   g.a_stride = p.w_stride;
   g.b = a.q;
   g.b_rows = p.T;
-  g.b_stride = p.K;
+  g.b_stride = a.K64;
   g.K = p.K;
   g.channels = p.N;
   const int tiles = (p.T + kMaxBlock - 1) / kMaxBlock;   // as few token tiles as there can be, of even size
@@ -667,9 +675,9 @@ ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T
   int64_t at = 0;
   const auto take = [&at](int64_t bytes) { const int64_t o = at; at += pad256(bytes); return o; };
   w.h = take(rows * (I * 4 > H * 2 ? I * 4 : H * 2));
-  w.q = take(rows * H * 2);
+  w.q = take(rows * pad64(H) * 2);
   w.x_scale = take(rows * 4);
-  w.hq = take(rows * I * 2);
+  w.hq = take(rows * pad64(I) * 2);
   w.h_scale = take(rows * 4);
   w.chunk_counts = take((int64_t)w.chunks * c->num_experts * 4);
   w.pos = take(rows * 4);
@@ -690,6 +698,7 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   a.k = p.k;
   a.E = p.E;
   a.H = p.H;
+  a.H64 = (int)pad64(p.H);
   a.chunk = w.chunk;
   a.chunks = w.chunks;
   a.block = w.block;
@@ -712,7 +721,7 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   g.a_stride = p.H;
   g.b = a.q;
   g.b_rows = rows;
-  g.b_stride = p.H;
+  g.b_stride = a.H64;
   g.K = p.H;
   g.channels = p.I;
   g.rows_per_group = 2 * p.I;
@@ -731,6 +740,7 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   b.stride = p.I;
   b.rows = rows;
   b.K = p.I;
+  b.K64 = (int)pad64(p.I);
   b.num_rows = a.counts + 1;
   b.q = (__half*)(ws + w.hq);
   b.scale = (float*)(ws + w.h_scale);
@@ -747,7 +757,7 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   g.a_stride = p.I;
   g.b = b.q;
   g.b_rows = rows;
-  g.b_stride = p.I;
+  g.b_stride = b.K64;
   g.K = p.I;
   g.channels = p.H;
   g.rows_per_group = p.H;

@@ -2,6 +2,7 @@
 // of a row, the stores of results.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -117,7 +118,7 @@ MOE_DEV int dot16(const uint4 w, const uint4 x, int acc) {
 // One value, rounded to nearest even (a NaN stays one).
 MOE_DEV uint16_t to_16(int dtype, float f) {
   if (dtype == MOE_DTYPE_F16) return __half_as_ushort(__float2half_rn(f));
-  return isnan(f) ? (uint16_t)0x7FC0u : f32_to_bf16_rne(f);
+  return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 MOE_DEV void store(void* out, int dtype, int64_t i, float f) {
   if (dtype == MOE_DTYPE_F32) static_cast<float*>(out)[i] = f;

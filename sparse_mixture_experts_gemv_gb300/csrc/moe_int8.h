@@ -13,7 +13,8 @@ constexpr int kMaxBlock = 192;   // tokens of a tensor-core tile: two accumulato
 enum GemmKind { kDense = 0, kUp = 1, kDown = 2 };
 
 // One launch of the tensor-core product. Weights [a_rows][K] bytes (row stride
-// a_stride), tokens f16 [b_rows][K] whole numbers (row stride b_stride elements).
+// a_stride), tokens f16 [b_rows][K] whole numbers, each row padded with zeros to b_stride
+// elements, a multiple of 64.
 struct GemmArgs {
   const void* a;
   int64_t a_rows, a_stride;

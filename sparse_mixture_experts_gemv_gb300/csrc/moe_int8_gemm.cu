@@ -8,7 +8,7 @@
 // exact in f16, their products (at most 2^14) and sums (up to 2^24) in the fp32
 // accumulators, so the products run as f16 x f16, and give the integers themselves.
 //
-// The weights stay bytes in memory: each tile of 128 channels x 64 bytes comes in by
+// The weights stay bytes in memory: each tile of 128 channels x 128 bytes comes in by
 // TMA, eight converter warps turn it into f16 and write it straight into tensor memory,
 // from where the MMA reads its A operand. (Through shared memory the f16 copy would
 // be written and read there once more, and with the token operand that is what bounds
@@ -19,10 +19,14 @@
 // One persistent CTA an SM, warp-specialised:
 //   warp 0        weights by TMA              warp 2  tokens by TMA
 //   warp 1        issues the MMAs             warp 3  idle
-//   warps 4-11    converters: two groups of four, alternate steps of 64 along K
+//   warps 4-11    converters: two groups of four, each half of a step's K
 //   warps 12-15   epilogue of the previous tile while the next one accumulates
-// Tensor memory: two accumulators of 192 columns, four operand slots of 32.
+// A step is 128 of K: eight MMAs. What the issuing warp does between two steps (a wait,
+// addresses, a commit) takes some 300 cycles, about what the MMAs in the queue cover: with
+// 64 of K and two waits a step it bounded the kernel (dense 4,096 x 2,048 x 4,096 76 us).
+// Tensor memory: two accumulators of 192 columns, two operand slots of 64.
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -40,10 +44,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kChannels = 128;            // channels of a tile = lanes of tensor memory
-constexpr int kStep = 64;                 // K of a stage
+constexpr int kStep = 128;                // K of a stage
 constexpr int kRawBytes = kChannels * kStep;
-constexpr int kMaxStages = 16;
-constexpr int kSlots = 4;                 // f16 weight operands in tensor memory
+constexpr int kMaxStages = 12;
+constexpr int kSlots = 2;                 // f16 weight operands in tensor memory
 constexpr int kSlotCols = kStep / 2;
 constexpr int kSlotBase = 2 * kMaxBlock;  // their first column
 constexpr int kGemmThreads = 512;
@@ -123,17 +127,58 @@ MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
 
 // One lane of a converged warp, the same one each time. Roles run as whole warps and elect a
 // lane around what it issues: the compiler then keeps addresses and descriptors in uniform
-// registers (four MMAs and a commit of one thread in a divergent branch issue in 300
+// registers (four MMAs and a commit of one thread in a divergent branch issue in 275
 // cycles, elected in 165).
 MOE_DEV bool elect() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
   return r != 0;
 }
-// mbar_wait by a whole warp, which goes on or gives up as one.
-MOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err, abort));
+// Barriers by their 32-bit shared-memory addresses: the roles' loops are bound by their own
+// instructions, and generic pointers cost several of them each time.
+MOE_DEV bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// Bounded: about two seconds, after which every role winds down and the error word is set.
+__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const long long t0 = clock64();
+  while (!__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) {
+    if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
+    if (__any_sync(0xFFFFFFFFu, clock64() - t0 > 4000000000LL)) {
+      set_error(&g_gemm_error, kDevTimeout);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// A wait by a whole warp, which goes on or gives up as one.
+MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
+  return slow_wait(bar, parity, abort);
+}
+MOE_DEV void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+MOE_DEV void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
+}
+MOE_DEV void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+MOE_DEV void load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+MOE_DEV void load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
@@ -149,7 +194,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  // stage: tokens (block x 128 bytes, whole 1024-byte swizzle atoms) and raw weights behind all of them
+  // stages: tokens (2 x block x 128 bytes, whole 1024-byte swizzle atoms); raw weights behind all of them
   const int b_bytes = p.stage_bytes - kRawBytes;
   uint8_t* s_b = smem;
   uint8_t* s_raw = smem + p.stages * b_bytes;
@@ -163,7 +208,6 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
   uint64_t* drain = d_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* err = &g_gemm_error;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -171,7 +215,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < kSlots; ++s) mbar_init(&a_full[s], 4);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&a_full[s], 8);
     for (int a = 0; a < 2; ++a) {
       mbar_init(&d_full[a], 1);
       mbar_init(&d_empty[a], 4);
@@ -199,6 +243,10 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     total = (nb < 0 || nb > p.max_blocks ? 0 : nb) * p.tiles_m;
   }
 
+  // Stages follow each other in a ring; a role keeps its place in it as a stage number and a parity.
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), a_full0 = smem_u32(a_full);
+  const uint32_t b0 = smem_u32(s_b), raw0 = smem_u32(s_raw);
+
   if (warp == 0) {
     // ------------------------------------------------------------- weights
     uint32_t it = 0;
@@ -206,14 +254,16 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     bool stop = false;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = decode<KIND>(p, tile);
-      const int r0 = KIND == kUp ? t.e * p.rows_per_group + t.mt * 64 : t.e * p.rows_per_group + t.mt * kChannels;
+      const int r0 = t.e * p.rows_per_group + t.mt * (KIND == kUp ? 64 : kChannels);
+      const uint32_t bytes = (uint32_t)(kRawBytes + t.n * kStep * 2);
       for (int ks = 0; ks < p.steps; ++ks, ++it) {
-        if (!warp_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
+        if (!warp_wait(empty0 + 8 * s, ph, abort_flag)) { stop = true; break; }
         if (elect()) {
-          mbar_arrive_expect_tx(&full[s], (uint32_t)(kRawBytes + t.n * 128));
-          tma_load_2d(s_raw + s * kRawBytes, &maps.a, ks * kStep, r0, &full[s]);
+          const uint32_t bar = full0 + 8 * s, dst = raw0 + s * kRawBytes;
+          expect_tx(bar, bytes);
+          load_2d(dst, &maps.a, ks * kStep, r0, bar);
           if (KIND == kUp)   // 64 gate rows, then their up rows
-            tma_load_2d(s_raw + s * kRawBytes + kRawBytes / 2, &maps.a, ks * kStep, r0 + p.channels, &full[s]);
+            load_2d(dst + kRawBytes / 2, &maps.a, ks * kStep, r0 + p.channels, bar);
         }
         __syncwarp();
         if (++s == p.stages) { s = 0; ph ^= 1; }
@@ -221,7 +271,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
     if (lane == 0 && *abort_flag) {   // let copies in flight land before the CTA exits
       for (uint32_t q = it > (uint32_t)p.stages ? it - p.stages : 0; q < it; ++q)
-        mbar_wait(&full[q % p.stages], (q / p.stages) & 1, err, abort_flag, 20000000LL, false);
+        mbar_wait(&full[q % p.stages], (q / p.stages) & 1, &g_gemm_error, abort_flag, 20000000LL, false);
     }
   } else if (warp == 2) {
     // -------------------------------------------------------------- tokens
@@ -231,81 +281,82 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       const Tile t = decode<KIND>(p, tile);
       const CUtensorMap* map = &maps.b[t.n / 16 - 1];
       for (int ks = 0; ks < p.steps; ++ks) {
-        if (!warp_wait(&empty[s], ph, err, abort_flag)) { stop = true; break; }
-        if (elect()) tma_load_2d(s_b + s * b_bytes, map, ks * kStep, t.row0, &full[s]);
+        if (!warp_wait(empty0 + 8 * s, ph, abort_flag)) { stop = true; break; }
+        if (elect()) load_3d(b0 + s * b_bytes, map, 0, t.row0, ks * (kStep / 64), full0 + 8 * s);
         __syncwarp();
         if (++s == p.stages) { s = 0; ph ^= 1; }
       }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
-    int s = 0, ph = 0;
-    uint32_t it = 0, tc = 0;
+    int s = 0;
+    uint32_t slot = 0, slot_ph = 0, tc = 0;
     bool stop = false;
-    const uint32_t b_base = smem_u32(s_b);
+    const uint32_t d_full0 = smem_u32(d_full), d_empty0 = smem_u32(d_empty);
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x, ++tc) {
       const Tile t = decode<KIND>(p, tile);
       // f16 x f16 -> fp32, both K-major, 128 x n
       const uint32_t idesc = (1u << 4) | ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kChannels >> 4) << 24);
-      const int ab = tc & 1;
-      if (!warp_wait(&d_empty[ab], ((tc >> 1) & 1) ^ 1, err, abort_flag)) break;
+      const uint32_t ab = tc & 1, d = tmem + ab * kMaxBlock;
+      const uint32_t half = (uint32_t)t.n * 8;   // the second 64 of K lie n x 128 bytes behind the first
+      if (!warp_wait(d_empty0 + 8 * ab, ((tc >> 1) & 1) ^ 1, abort_flag)) break;
       tc_fence_after();
-      const uint32_t d = tmem + ab * kMaxBlock;
-      for (int ks = 0; ks < p.steps; ++ks, ++it) {
-        const int slot = it & (kSlots - 1);
-        if (!warp_wait(&full[s], ph, err, abort_flag) ||
-            !warp_wait(&a_full[slot], (it / kSlots) & 1, err, abort_flag)) { stop = true; break; }
+      for (int ks = 0; ks < p.steps; ++ks) {
+        // the converters have waited for the stage, tokens and all
+        if (!warp_wait(a_full0 + 8 * slot, slot_ph, abort_flag)) { stop = true; break; }
         tc_fence_after();
         const uint32_t a0 = tmem + kSlotBase + slot * kSlotCols;
-        const uint64_t bdesc = smem_desc_sw128(b_base + s * b_bytes);
+        const uint64_t bdesc = smem_desc_sw128(b0 + s * b_bytes);
         if (elect()) {
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk)   // 16 of K: 8 columns, and 32 bytes (2 in the descriptor)
-            mma_f16_ts(d, a0 + kk * 8, bdesc + kk * 2, idesc, (ks | kk) != 0 ? 1u : 0u);
-          mma_commit(&empty[s]);   // frees the stage and, since the converters wait on it too, the slot
-          if (ks == p.steps - 1) mma_commit(&d_full[ab]);
+            mma_f16_ts(d, a0 + kk * 8, bdesc + (kk & 3) * 2 + (kk >> 2) * half, idesc, (ks | kk) != 0 ? 1u : 0u);
+          commit(empty0 + 8 * s);   // frees the stage and, since the converters wait on it too, the slot
+          if (ks == p.steps - 1) commit(d_full0 + 8 * ab);
         }
         __syncwarp();
-        if (++s == p.stages) { s = 0; ph ^= 1; }
+        if (++s == p.stages) s = 0;
+        slot ^= 1;
+        slot_ph ^= slot ^ 1;   // flips when the slots come round
       }
     }
     if (elect()) mma_commit(drain);   // all MMAs complete before tensor memory is released
     __syncwarp();
-    mbar_wait(drain, 0, err, abort_flag, 2000000000LL, false);
+    mbar_wait(drain, 0, &g_gemm_error, abort_flag, 2000000000LL, false);
   } else if (warp >= 4 && warp < 12) {
     // ---------------------------------------------------------- converters
     const int group = (warp - 4) >> 2, quad = warp & 3;
     // The lane's row of the raw tile. up: a warp's lower 16 lanes are gate rows, its upper
     // 16 the up rows of the same features, so that the epilogue pairs them by a shuffle.
     const int row = KIND == kUp ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
-    const int sw = (row >> 1) & 3;   // 64-byte swizzle: 16-byte chunk c of row r lands at c ^ (r / 2 % 4)
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    uint32_t it = 0;
+    const uint8_t* src0 = s_raw + row * kStep;
+    const int sw = row & 7;   // 128-byte swizzle: 16-byte chunk c of row r lands at c ^ (r % 8)
+    const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + kSlotBase + group * (kSlotCols / 2);
     int s = 0, ph = 0;
-    int es = p.stages - kSlots, eph = 1;   // stage and phase of the step kSlots before, whose MMAs read this slot
-    bool stop = false;
+    int es = p.stages - kSlots, eph = 1;   // stage and parity of the step kSlots before, whose MMAs read this slot
+    uint32_t slot = 0;
+    bool stop = false, first = true;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
-      for (int ks = 0; ks < p.steps; ++ks, ++it) {
-        if ((int)(it & 1) == group) {
-          if (!warp_wait(&full[s], ph, err, abort_flag)) { stop = true; break; }
-          const uint8_t* src = s_raw + s * kRawBytes + row * kStep;
-          uint32_t r[32];
+      for (int ks = 0; ks < p.steps; ++ks) {
+        if (!warp_wait(full0 + 8 * s, ph, abort_flag)) { stop = true; break; }
+        const uint8_t* src = src0 + s * kRawBytes;
+        uint32_t r[32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
-            s8x4_to_f16(w.x, r[8 * c], r[8 * c + 1]);
-            s8x4_to_f16(w.y, r[8 * c + 2], r[8 * c + 3]);
-            s8x4_to_f16(w.z, r[8 * c + 4], r[8 * c + 5]);
-            s8x4_to_f16(w.w, r[8 * c + 6], r[8 * c + 7]);
-          }
-          const int slot = it & (kSlots - 1);
-          if (it >= kSlots && !warp_wait(&empty[es], eph, err, abort_flag)) { stop = true; break; }
-          tc_fence_after();
-          tmem_st32(tmem + lanes + kSlotBase + slot * kSlotCols, r);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&a_full[slot]);
+        for (int c = 0; c < 4; ++c) {
+          const uint4 w = *reinterpret_cast<const uint4*>(src + (((4 * group + c) ^ sw) << 4));
+          s8x4_to_f16(w.x, r[8 * c], r[8 * c + 1]);
+          s8x4_to_f16(w.y, r[8 * c + 2], r[8 * c + 3]);
+          s8x4_to_f16(w.z, r[8 * c + 4], r[8 * c + 5]);
+          s8x4_to_f16(w.w, r[8 * c + 6], r[8 * c + 7]);
         }
+        if (es == 0) first = false;
+        if (!first && !warp_wait(empty0 + 8 * es, eph, abort_flag)) { stop = true; break; }
+        tc_fence_after();
+        tmem_st32(to + slot * kSlotCols, r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(a_full0 + 8 * slot);
+        slot ^= 1;
         if (++s == p.stages) { s = 0; ph ^= 1; }
         if (++es == p.stages) { es = 0; eph ^= 1; }
       }
@@ -315,10 +366,11 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     const int quad = warp & 3;
     float* cs = s_scale + quad * kMaxBlock;   // the warp's copy of the tile's token scales
     uint16_t* turn = s_turn + quad * 1024;    // 32 tokens x 32 channels
+    const bool f16_out = p.out_dtype == MOE_DTYPE_F16;
     uint32_t tc = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++tc) {
       const Tile t = decode<KIND>(p, tile);
-      const int ab = tc & 1;
+      const uint32_t ab = tc & 1;
       __syncwarp();
       if (KIND != kDown) {
         for (int c = lane; c < t.rows; c += 32) cs[c] = ldg_cg_f32(p.row_scale + t.row0 + c);
@@ -332,7 +384,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
         w1 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + p.channels + ch);
       }
       __syncwarp();
-      if (!warp_wait(&d_full[ab], (tc >> 1) & 1, err, abort_flag)) break;
+      if (!warp_wait(smem_u32(&d_full[ab]), (tc >> 1) & 1, abort_flag)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ab * kMaxBlock + ((uint32_t)(quad * 32) << 16);
       for (int c0 = 0; c0 < t.rows; c0 += 32) {
@@ -358,10 +410,22 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
           // 16-bit results: turned in shared memory, so that a token's 32 channels leave in 16-byte pieces
           // (stored as they are, 2 bytes a lane, a tile of 192 tokens took 26,000 cycles)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float f = KIND == kDown ? __uint_as_float(v[i]) * p.factor
-                                          : __uint_as_float(v[i]) * cs[min(c0 + i, kMaxBlock - 1)] * w0;
-            turn[i * 32 + lane] = KIND == kDown ? __half_as_ushort(__float2half_rn(f)) : to_16(p.out_dtype, f);
+          for (int i = 0; i < 32; i += 4) {
+            float f[4];
+            if (KIND == kDown) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(v[i + j]) * p.factor;
+            } else {
+              const float4 xs = *reinterpret_cast<const float4*>(cs + c0 + i);
+              f[0] = __uint_as_float(v[i]) * xs.x * w0;
+              f[1] = __uint_as_float(v[i + 1]) * xs.y * w0;
+              f[2] = __uint_as_float(v[i + 2]) * xs.z * w0;
+              f[3] = __uint_as_float(v[i + 3]) * xs.w * w0;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              turn[(i + j) * 32 + lane] = KIND == kDown || f16_out ? __half_as_ushort(__float2half_rn(f[j]))
+                                                                   : __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));
           }
           __syncwarp();
           const int ch8 = t.mt * kChannels + quad * 32 + (lane & 3) * 8;
@@ -410,17 +474,29 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return f;
 }
 
-cudaError_t encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
-                   int64_t stride_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+cudaError_t encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                   const cuuint64_t* strides, const cuuint32_t* box) {
   PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
   if (!f) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)stride_bytes};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = f(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = f(m, type, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// `box_rows` rows of a step's 128 bytes; zeros past the rows' ends.
+cudaError_t encode_weights(CUtensorMap* m, const GemmArgs& a, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.a_rows}, strides[1] = {(cuuint64_t)a.a_stride};
+  const cuuint32_t box[2] = {kStep, box_rows};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.a, dims, strides, box);
+}
+// A step's tokens in one copy: two columns of n rows x 64 values, one behind the other.
+// Rows are padded to 64 values, so that a column never reaches into the next row.
+cudaError_t encode_tokens(CUtensorMap* m, const GemmArgs& a, uint32_t n) {
+  const cuuint64_t dims[3] = {64, (cuuint64_t)a.b_rows, (cuuint64_t)(a.b_stride / 64)};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.b_stride * 2, 128};
+  const cuuint32_t box[3] = {64, n, kStep / 64};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, a.b, dims, strides, box);
 }
 
 template <int KIND>
@@ -452,13 +528,11 @@ cudaError_t launch_kind(const Maps& maps, const Params& p, int grid, size_t smem
 
 cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStream_t s) {
   Maps maps = {};
-  cudaError_t e = encode(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, a.a_rows, a.K, a.a_stride, kStep,
-                         kind == kUp ? 64 : kChannels, CU_TENSOR_MAP_SWIZZLE_64B);
+  cudaError_t e = encode_weights(&maps.a, a, kind == kUp ? 64 : kChannels);
   const int tail = kind == kDense ? ((a.T - 1) % a.block + 16) / 16 * 16 : 0;   // rows of the last tile
   for (int n = 16; n <= a.block && e == cudaSuccess; n += 16)
     if (kind != kDense || n == a.block || n == tail)
-      e = encode(&maps.b[n / 16 - 1], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.b, a.b_rows, a.K, a.b_stride * 2, kStep, n,
-                 CU_TENSOR_MAP_SWIZZLE_128B);
+      e = encode_tokens(&maps.b[n / 16 - 1], a, n);
   if (e != cudaSuccess) return e;
   Params p = {};
   p.blocks = a.blocks;
@@ -472,10 +546,9 @@ cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStrea
   p.channels = a.channels;
   p.rows_per_group = a.rows_per_group;
   p.steps = (a.K + kStep - 1) / kStep;
-  p.stage_bytes = a.block * 128 + kRawBytes;
+  p.stage_bytes = a.block * kStep * 2 + kRawBytes;
   p.stages = kStageBudget / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.stages &= ~1;   // even: a converter group meets the same stages again, every phase of them
   p.row_scale = a.row_scale;
   p.w_scale = a.w_scale;
   p.out = a.out;
