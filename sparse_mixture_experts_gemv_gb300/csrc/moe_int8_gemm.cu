@@ -46,12 +46,12 @@ using namespace sm100;
 constexpr int kChannels = 128;            // channels of a tile = lanes of tensor memory
 constexpr int kStep = 128;                // K of a stage
 constexpr int kRawBytes = kChannels * kStep;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 8;             // of either ring
 constexpr int kSlots = 2;                 // f16 weight operands in tensor memory
 constexpr int kSlotCols = kStep / 2;
 constexpr int kSlotBase = 2 * kMaxBlock;  // their first column
 constexpr int kGemmThreads = 512;
-constexpr int kStageBudget = 200 * 1024;  // shared memory of all stages
+constexpr int kStageBudget = 208 * 1024;  // shared memory of both rings
 constexpr int kFixedSmem = 1024 /*align*/ + 4 * kMaxBlock * 4 /*scales*/ + 4 * 2048 /*turned results*/ + 1024 /*barriers*/;
 
 __device__ int g_gemm_error;              // MOE_ERR_TIMEOUT once a bounded wait ran out
@@ -63,7 +63,8 @@ struct Params {
   int tiles_m;               // channel tiles of a group
   int tiles_t;               // dense: token tiles
   int T, block, channels, rows_per_group;
-  int steps, stages, stage_bytes;
+  int steps;
+  int raw_stages, b_stages, b_bytes;
   const float* row_scale;
   const float* w_scale;
   void* out;
@@ -107,9 +108,13 @@ MOE_DEV Tile decode(const Params& p, int tile) {
 MOE_DEV void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = w ^ 0x80808080u;
   const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+  asm volatile("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+  asm volatile("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
+
+// silu(g) * u to some 2^-20 of itself, by the approximate exponential and quotient: it is cut to
+// 8 bits next.
+MOE_DEV float fast_swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
 // 32 columns of this warp's 32 lanes of tensor memory.
 MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -181,6 +186,13 @@ MOE_DEV void load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c
       :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
 
+// After an abort: the copies of a ring's last stages land before the CTA exits.
+MOE_DEV void land(uint64_t* full, int stages, uint32_t issued, volatile int* abort) {
+  if ((threadIdx.x & 31) || !*abort) return;
+  for (uint32_t q = issued > (uint32_t)stages ? issued - stages : 0; q < issued; ++q)
+    mbar_wait(&full[q % stages], (q / stages) & 1, &g_gemm_error, abort, 20000000LL, false);
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
 MOE_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -194,15 +206,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  // stages: tokens (2 x block x 128 bytes, whole 1024-byte swizzle atoms); raw weights behind all of them
-  const int b_bytes = p.stage_bytes - kRawBytes;
+  // two rings: tokens (stages of 2 x block x 128 bytes, whole 1024-byte swizzle atoms), which the MMAs free,
+  // and raw weights, which come from further away and are free as soon as they are converted
   uint8_t* s_b = smem;
-  uint8_t* s_raw = smem + p.stages * b_bytes;
-  float* s_scale = reinterpret_cast<float*>(s_raw + p.stages * kRawBytes);   // [4][kMaxBlock]
+  uint8_t* s_raw = smem + p.b_stages * p.b_bytes;
+  float* s_scale = reinterpret_cast<float*>(s_raw + p.raw_stages * kRawBytes);   // [4][kMaxBlock]
   uint16_t* s_turn = reinterpret_cast<uint16_t*>(s_scale + 4 * kMaxBlock);   // [4][1024]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_turn + 4 * 1024);
-  uint64_t* empty = full + kMaxStages;
-  uint64_t* a_full = empty + kMaxStages;
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(s_turn + 4 * 1024);
+  uint64_t* raw_empty = raw_full + kMaxStages;
+  uint64_t* b_full = raw_empty + kMaxStages;
+  uint64_t* b_empty = b_full + kMaxStages;
+  uint64_t* a_full = b_empty + kMaxStages;
   uint64_t* d_full = a_full + kSlots;
   uint64_t* d_empty = d_full + 2;
   uint64_t* drain = d_empty + 2;
@@ -211,9 +225,13 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < p.raw_stages; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 8);
+    }
+    for (int s = 0; s < p.b_stages; ++s) {
+      mbar_init(&b_full[s], 1);
+      mbar_init(&b_empty[s], 1);
     }
     for (int s = 0; s < kSlots; ++s) mbar_init(&a_full[s], 8);
     for (int a = 0; a < 2; ++a) {
@@ -243,8 +261,9 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     total = (nb < 0 || nb > p.max_blocks ? 0 : nb) * p.tiles_m;
   }
 
-  // Stages follow each other in a ring; a role keeps its place in it as a stage number and a parity.
-  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), a_full0 = smem_u32(a_full);
+  // A role keeps its place in a ring as a stage number and a parity.
+  const uint32_t raw_full0 = smem_u32(raw_full), raw_empty0 = smem_u32(raw_empty), b_full0 = smem_u32(b_full),
+                 b_empty0 = smem_u32(b_empty), a_full0 = smem_u32(a_full);
   const uint32_t b0 = smem_u32(s_b), raw0 = smem_u32(s_raw);
 
   if (warp == 0) {
@@ -255,41 +274,42 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = decode<KIND>(p, tile);
       const int r0 = t.e * p.rows_per_group + t.mt * (KIND == kUp ? 64 : kChannels);
-      const uint32_t bytes = (uint32_t)(kRawBytes + t.n * kStep * 2);
       for (int ks = 0; ks < p.steps; ++ks, ++it) {
-        if (!warp_wait(empty0 + 8 * s, ph, abort_flag)) { stop = true; break; }
+        if (!warp_wait(raw_empty0 + 8 * s, ph, abort_flag)) { stop = true; break; }
         if (elect()) {
-          const uint32_t bar = full0 + 8 * s, dst = raw0 + s * kRawBytes;
-          expect_tx(bar, bytes);
+          const uint32_t bar = raw_full0 + 8 * s, dst = raw0 + s * kRawBytes;
+          expect_tx(bar, kRawBytes);
           load_2d(dst, &maps.a, ks * kStep, r0, bar);
           if (KIND == kUp)   // 64 gate rows, then their up rows
             load_2d(dst + kRawBytes / 2, &maps.a, ks * kStep, r0 + p.channels, bar);
         }
         __syncwarp();
-        if (++s == p.stages) { s = 0; ph ^= 1; }
+        if (++s == p.raw_stages) { s = 0; ph ^= 1; }
       }
     }
-    if (lane == 0 && *abort_flag) {   // let copies in flight land before the CTA exits
-      for (uint32_t q = it > (uint32_t)p.stages ? it - p.stages : 0; q < it; ++q)
-        mbar_wait(&full[q % p.stages], (q / p.stages) & 1, &g_gemm_error, abort_flag, 20000000LL, false);
-    }
+    land(raw_full, p.raw_stages, it, abort_flag);
   } else if (warp == 2) {
     // -------------------------------------------------------------- tokens
+    uint32_t it = 0;
     int s = 0, ph = 1;
     bool stop = false;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = decode<KIND>(p, tile);
       const CUtensorMap* map = &maps.b[t.n / 16 - 1];
-      for (int ks = 0; ks < p.steps; ++ks) {
-        if (!warp_wait(empty0 + 8 * s, ph, abort_flag)) { stop = true; break; }
-        if (elect()) load_3d(b0 + s * b_bytes, map, 0, t.row0, ks * (kStep / 64), full0 + 8 * s);
+      for (int ks = 0; ks < p.steps; ++ks, ++it) {
+        if (!warp_wait(b_empty0 + 8 * s, ph, abort_flag)) { stop = true; break; }
+        if (elect()) {
+          expect_tx(b_full0 + 8 * s, (uint32_t)(t.n * kStep * 2));
+          load_3d(b0 + s * p.b_bytes, map, 0, t.row0, ks * (kStep / 64), b_full0 + 8 * s);
+        }
         __syncwarp();
-        if (++s == p.stages) { s = 0; ph ^= 1; }
+        if (++s == p.b_stages) { s = 0; ph ^= 1; }
       }
     }
+    land(b_full, p.b_stages, it, abort_flag);
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
-    int s = 0;
+    int s = 0, ph = 0;
     uint32_t slot = 0, slot_ph = 0, tc = 0;
     bool stop = false;
     const uint32_t d_full0 = smem_u32(d_full), d_empty0 = smem_u32(d_empty);
@@ -302,20 +322,22 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       if (!warp_wait(d_empty0 + 8 * ab, ((tc >> 1) & 1) ^ 1, abort_flag)) break;
       tc_fence_after();
       for (int ks = 0; ks < p.steps; ++ks) {
-        // the converters have waited for the stage, tokens and all
-        if (!warp_wait(a_full0 + 8 * slot, slot_ph, abort_flag)) { stop = true; break; }
+        if (!warp_wait(b_full0 + 8 * s, ph, abort_flag) || !warp_wait(a_full0 + 8 * slot, slot_ph, abort_flag)) {
+          stop = true;
+          break;
+        }
         tc_fence_after();
         const uint32_t a0 = tmem + kSlotBase + slot * kSlotCols;
-        const uint64_t bdesc = smem_desc_sw128(b0 + s * b_bytes);
+        const uint64_t bdesc = smem_desc_sw128(b0 + s * p.b_bytes);
         if (elect()) {
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk)   // 16 of K: 8 columns, and 32 bytes (2 in the descriptor)
             mma_f16_ts(d, a0 + kk * 8, bdesc + (kk & 3) * 2 + (kk >> 2) * half, idesc, (ks | kk) != 0 ? 1u : 0u);
-          commit(empty0 + 8 * s);   // frees the stage and, since the converters wait on it too, the slot
+          commit(b_empty0 + 8 * s);   // frees the stage and, since the converters wait on it too, the slot
           if (ks == p.steps - 1) commit(d_full0 + 8 * ab);
         }
         __syncwarp();
-        if (++s == p.stages) s = 0;
+        if (++s == p.b_stages) { s = 0; ph ^= 1; }
         slot ^= 1;
         slot_ph ^= slot ^ 1;   // flips when the slots come round
       }
@@ -333,12 +355,12 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     const int sw = row & 7;   // 128-byte swizzle: 16-byte chunk c of row r lands at c ^ (r % 8)
     const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + kSlotBase + group * (kSlotCols / 2);
     int s = 0, ph = 0;
-    int es = p.stages - kSlots, eph = 1;   // stage and parity of the step kSlots before, whose MMAs read this slot
+    int es = p.b_stages - kSlots, eph = 1;   // tokens' stage of the step kSlots before, whose MMAs read this slot
     uint32_t slot = 0;
     bool stop = false, first = true;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       for (int ks = 0; ks < p.steps; ++ks) {
-        if (!warp_wait(full0 + 8 * s, ph, abort_flag)) { stop = true; break; }
+        if (!warp_wait(raw_full0 + 8 * s, ph, abort_flag)) { stop = true; break; }
         const uint8_t* src = src0 + s * kRawBytes;
         uint32_t r[32];
 #pragma unroll
@@ -349,16 +371,20 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
           s8x4_to_f16(w.z, r[8 * c + 4], r[8 * c + 5]);
           s8x4_to_f16(w.w, r[8 * c + 6], r[8 * c + 7]);
         }
+        // Free once its values have been used (the conversions are volatile and stay ahead of this): an arrival
+        // right behind the loads could be seen before they have read.
+        __syncwarp();
+        if (lane == 0) arrive(raw_empty0 + 8 * s);
         if (es == 0) first = false;
-        if (!first && !warp_wait(empty0 + 8 * es, eph, abort_flag)) { stop = true; break; }
+        if (!first && !warp_wait(b_empty0 + 8 * es, eph, abort_flag)) { stop = true; break; }
         tc_fence_after();
         tmem_st32(to + slot * kSlotCols, r);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive(a_full0 + 8 * slot);
         slot ^= 1;
-        if (++s == p.stages) { s = 0; ph ^= 1; }
-        if (++es == p.stages) { es = 0; eph ^= 1; }
+        if (++s == p.raw_stages) { s = 0; ph ^= 1; }
+        if (++es == p.b_stages) { es = 0; eph ^= 1; }
       }
     }
   } else if (warp >= 12) {
@@ -403,7 +429,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
             const int c = 2 * i + (lane >> 4);
             if (in && c < nc) {
               const float xs = cs[c0 + c];
-              dst[(int64_t)2 * i * p.channels] = swiglu((upper ? got : keep) * xs * w0, (upper ? keep : got) * xs * w1);
+              dst[(int64_t)2 * i * p.channels] = fast_swiglu((upper ? got : keep) * xs * w0, (upper ? keep : got) * xs * w1);
             }
           }
         } else if (KIND == kDown || p.wide) {
@@ -546,16 +572,20 @@ cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStrea
   p.channels = a.channels;
   p.rows_per_group = a.rows_per_group;
   p.steps = (a.K + kStep - 1) / kStep;
-  p.stage_bytes = a.block * kStep * 2 + kRawBytes;
-  p.stages = kStageBudget / p.stage_bytes;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  // Tokens come from L2 and wait for the MMAs, three stages of the largest; the rest is for the weights,
+  // which come from memory. (One ring of three stages for both bounded the dense product at 50 us.)
+  p.b_bytes = a.block * kStep * 2;
+  p.b_stages = 3 * kMaxBlock * kStep * 2 / p.b_bytes;
+  if (p.b_stages > 6) p.b_stages = 6;
+  p.raw_stages = (kStageBudget - p.b_stages * p.b_bytes) / kRawBytes;
+  if (p.raw_stages > kMaxStages) p.raw_stages = kMaxStages;
   p.row_scale = a.row_scale;
   p.w_scale = a.w_scale;
   p.out = a.out;
   p.out_dtype = a.out_dtype;
   p.wide = a.out_dtype != MOE_DTYPE_F32 && a.channels % 8 == 0 && !((uintptr_t)a.out & 15);
   p.factor = a.factor;
-  const size_t smem = (size_t)p.stages * p.stage_bytes + kFixedSmem;
+  const size_t smem = (size_t)p.b_stages * p.b_bytes + (size_t)p.raw_stages * kRawBytes + kFixedSmem;
   const int64_t tiles = (int64_t)p.tiles_m * (kind == kDense ? p.tiles_t : a.max_blocks);
   const int grid = (int)(tiles < num_sms ? tiles : num_sms);
   switch (kind) {
