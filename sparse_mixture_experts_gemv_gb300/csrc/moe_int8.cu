@@ -578,14 +578,6 @@ cudaError_t launch_experts_stream(const ExpertsParams& p, int x_dtype, cudaStrea
   return launch_pdl(int8_experts_down_kernel, down, kDownThreads, (size_t)held * p.I, s, p, held);
 }
 
-int device_sms() {
-  static int sms[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
-  return sms[dev];
-}
-
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
@@ -784,6 +776,15 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
 }
 
 }  // namespace
+
+int device_sms() {
+  static int sms[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  return sms[dev];
+}
+
 }  // namespace int8
 }  // namespace moe
 

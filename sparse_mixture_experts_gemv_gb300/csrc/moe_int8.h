@@ -35,6 +35,7 @@ struct GemmArgs {
   int out_dtype;
   float factor;               // down: what the integer sums are multiplied by
 };
+int device_sms();   // of the current device
 cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStream_t s);
 cudaError_t gemm_status(cudaStream_t s, int* code);   // synchronises; reads and clears the device's error word
 

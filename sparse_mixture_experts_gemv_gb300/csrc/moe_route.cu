@@ -17,8 +17,7 @@
 // bias and groups the keys are the logits themselves (both scores increase with
 // the logit), so the choice is exact. Otherwise scores are computed in 32 bits,
 // and a choice is kept only if the keys it separates are further apart than the
-// 32-bit errors can reach; a token with a closer pair is decided again with all
-// its scores in 64 bits.
+// 32-bit errors can reach; where a pair is closer, the keys are taken in 64 bits.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -26,6 +25,7 @@
 #include <stdint.h>
 
 #include "moe_common.cuh"
+#include "moe_int8.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -51,10 +51,10 @@ MOE_DEV float load_one(const void* p, int64_t i) {
   return __half2float(__ushort_as_half(v));
 }
 
-// The lane's NPL logits of a row; experts past E are off. VEC: rows start on
+// The lane's NPL logits of a row; -inf for experts past E. VEC: rows start on
 // 16-byte boundaries and E is a multiple of what one 16-byte load holds.
 template <int DT, int NPL, bool VEC>
-MOE_DEV void load_logits(const void* logits, int64_t row0, int E, int lane, float (&x)[NPL]) {
+MOE_DEV void load_raw(const void* logits, int64_t row0, int E, int lane, float (&x)[NPL]) {
   constexpr int per16 = DT == MOE_DTYPE_F32 ? 4 : 8;
   if constexpr (VEC && NPL % per16 == 0) {
     const char* p = static_cast<const char*>(logits) + (row0 + lane * NPL) * (16 / per16);
@@ -86,12 +86,29 @@ MOE_DEV void load_logits(const void* logits, int64_t row0, int E, int lane, floa
       x[q] = e < E ? load_one<DT>(logits, row0 + e) : -INFINITY;
     }
   }
+}
+
+// The same with NaN as -inf and +inf as the largest finite value.
+template <int DT, int NPL, bool VEC>
+MOE_DEV void load_logits(const void* logits, int64_t row0, int E, int lane, float (&x)[NPL]) {
+  load_raw<DT, NPL, VEC>(logits, row0, E, lane, x);
 #pragma unroll
   for (int q = 0; q < NPL; ++q) {
     if (isnan(x[q])) x[q] = -INFINITY;
     x[q] = fminf(x[q], FLT_MAX) + 0.0f;   // -0 becomes +0: equal logits have equal keys
   }
 }
+
+// The same for rows of finite logits, as they are; false where the lane has one that is not.
+template <int DT, int NPL, bool VEC>
+MOE_DEV bool load_finite(const void* logits, int64_t row0, int E, int lane, float (&x)[NPL]) {
+  load_raw<DT, NPL, VEC>(logits, row0, E, lane, x);
+  float zero = 0.f;
+#pragma unroll
+  for (int q = 0; q < NPL; ++q) zero = fmaf(lane * NPL + q < E ? x[q] : 0.f, 0.f, zero);   // NaN from inf and NaN
+  return zero == 0.f;
+}
+
 
 MOE_DEV float warp_max(float v) {
   return f32_from_order_key(__reduce_max_sync(0xFFFFFFFFu, f32_order_key(v)));
@@ -190,142 +207,312 @@ MOE_DEV void route_exact(const RouteParams& p, const float (&x)[NPL], double* ke
 }
 
 // ---------------------------------------------------------------------- forward
-template <int DT, int NPL, bool VEC>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_experts_kernel(const RouteParams p) {
-  __shared__ double s_keys[kRouteWarps][32 * NPL];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* s_f = reinterpret_cast<float*>(s_keys[warp]);
-  const bool keyed = p.bias != nullptr || p.groups > 1;
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < p.T; t += (int64_t)gridDim.x * kRouteWarps) {
-    float x[NPL];
-    load_logits<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, x);
-    float m = x[0];
+// 1 / (1 + e^-x) by the approximate exponential and reciprocal. The exponential's argument is
+// rounded to |x| 2^-23 or so, which s (1 - s) |x| <= 0.23 bounds in the result: within 2^-21
+// of the sigmoid, absolutely, for every x.
+MOE_DEV float key_sigmoid(float x) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
+
+// A pair of keys closer than this may be in either order. A sigmoid is within 2^-21 of what it
+// stands for, a softmax, which has its row's sum besides (16 + 5 additions: 2^-19.6), within 2^-19
+// of the row's largest, 1 / z. A group's score adds two keys, and a difference has two sides: four
+// times that, and the roundings of sums that reach 1 + the largest bias.
+MOE_DEV float near_of(const RouteParams& p, float z, float largest_bias) {
+  return (p.sigmoid ? 0x1p-19f : 0x1p-17f / z) + (1.f + largest_bias) * 0x1p-21f;
+}
+
+// The top_groups largest of the lanes' scores below `lanes` that are a group's, as a mask of lanes; close:
+// the last of them and the first that goes lie within `near`. score: -inf where no expert is on.
+MOE_DEV uint32_t choose_groups(const RouteParams& p, float score, bool is_group, float near, int lane, bool& close) {
+  uint32_t left = is_group ? f32_order_key(score + 0.f) : 0u, kept = 0u;
+  float before = INFINITY;
+  for (int r = 0; r <= p.top_groups; ++r) {
+    const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, left);
+    const uint32_t first = __ballot_sync(0xFFFFFFFFu, left == g);
+    const float v = f32_from_order_key(g);
+    if (r == p.top_groups) {
+      close = g != 0u && v != -INFINITY && before - v <= near;
+      break;
+    }
+    before = v;
+    kept |= first & (0u - first);
+    if (lane == __ffs(first) - 1) left = 0u;
+  }
+  return kept;
+}
+
+// Rows that the short list does not serve: logits that are not finite, too many equal keys, too few
+// lanes with an expert on, groups or (softmax) experts too close to tell apart in 32 bits. All keys
+// one at a time, and in 64 bits where it takes that. Lane r returns the r-th choice.
+template <int DT, int NPL, bool VEC, bool KEYED>
+__device__ __noinline__ int route_slowly(const RouteParams& p, int64_t t, double* keys, int lane) {
+  float x[NPL], c[NPL];
+  load_logits<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, x);
+  int my_e = 0;
+  uint32_t key[NPL];   // 0: not to be chosen (any more)
+  bool close = KEYED;
+  if (!KEYED) {
 #pragma unroll
-    for (int q = 1; q < NPL; ++q) m = fmaxf(m, x[q]);
-    float z = 1.f;
-    if (!p.sigmoid && (keyed || !p.renormalise)) {
+    for (int q = 0; q < NPL; ++q) key[q] = lane * NPL + q < p.E ? f32_order_key(x[q]) : 0u;
+  } else if (p.groups == 1) {
+    float m = x[0], z = 1.f, top = 0.f;
+    if (!p.sigmoid) {
+#pragma unroll
+      for (int q = 1; q < NPL; ++q) m = fmaxf(m, x[q]);
       m = warp_max(m);
       z = 0.f;
 #pragma unroll
       for (int q = 0; q < NPL; ++q) z += x[q] == -INFINITY ? 0.f : expf(x[q] - m);
-      z = warp_sum(z);
+      z = fmaxf(warp_sum(z), 1.f);   // at least the largest's 1, where one is on
     }
-
-    int my_e = 0;        // lane r: the r-th choice
-    bool close = false;
-    uint32_t key[NPL];   // 0: not to be chosen (any more)
-    if (!keyed) {
 #pragma unroll
-      for (int q = 0; q < NPL; ++q) key[q] = lane * NPL + q < p.E ? f32_order_key(x[q]) : 0u;
-    } else {
-      float smax = 0.f, cmax = 0.f;
+    for (int q = 0; q < NPL; ++q) {
+      const int e = lane * NPL + q;
+      const float b = e < p.E && p.bias ? __ldg(p.bias + e) : 0.f;
+      top = fmaxf(top, fabsf(b));
+      c[q] = x[q] == -INFINITY ? -INFINITY : (p.sigmoid ? key_sigmoid(x[q]) : expf(x[q] - m) / z) + b;
+      key[q] = e < p.E ? f32_order_key(c[q] + 0.f) : 0u;
+    }
+    const float near = near_of(p, z, warp_max(top));
+    // as below, but without taking anything off: only to see whether the choice is firm
+    uint32_t left[NPL];
+#pragma unroll
+    for (int q = 0; q < NPL; ++q) left[q] = key[q];
+    float before = INFINITY;
+    close = false;
+#pragma unroll 1
+    for (int r = 0; r <= p.k; ++r) {
+      uint32_t bk = 0u;
+#pragma unroll
+      for (int q = 0; q < NPL; ++q) bk = max(bk, left[q]);
+      const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, bk);
+      const float v = f32_from_order_key(g);
+      if (g == 0u || v == -INFINITY) break;   // experts that are off go by index: nothing to tell apart
+      close |= before - v <= near;
+      before = v;
+      const int src = __ffs(__ballot_sync(0xFFFFFFFFu, bk == g)) - 1;
+      bool got = false;
+#pragma unroll
+      for (int q = 0; q < NPL; ++q)
+        if (lane == src && !got && left[q] == g) { left[q] = 0u; got = true; }
+    }
+  }
+  if (close) {
+    __syncwarp();
+    route_exact<NPL>(p, x, keys, lane, &my_e);
+    return my_e;
+  }
+#pragma unroll 1
+  for (int r = 0; r < p.k; ++r) {
+    uint32_t bk = 0u;
+#pragma unroll
+    for (int q = 0; q < NPL; ++q) bk = max(bk, key[q]);
+    const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, bk);
+    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, bk == g)) - 1;
+    int wq = 0;
+    bool got = false;
+#pragma unroll
+    for (int q = 0; q < NPL; ++q)
+      if (!got && key[q] == g) { wq = q; got = true; if (lane == src) key[q] = 0u; }
+    const int e = src * NPL + __shfl_sync(0xFFFFFFFFu, wq, src);
+    if (lane == r) my_e = e;
+  }
+  return my_e;
+}
+
+// Nearly all rows: the k-th largest of the lanes' largest keys is at most the k-th largest key, and few
+// keys lie above it (about 10 for k = 8). These, each in a lane of its own and in the order of their
+// indexes, are ranked by counting; with a bias or groups, keys closer than `near` are ranked again in
+// 64 bits, one evaluation a lane.
+// Bound by its instructions, some 500 a row of 512 (65,536 rows of 512 bf16 logits: see the launch).
+template <int DT, int NPL, bool VEC, bool KEYED>
+__global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_experts_kernel(const RouteParams p) {
+  __shared__ double s_keys[kRouteWarps][32 * NPL];
+  __shared__ int s_list[kRouteWarps][32];
+  __shared__ float s_sorted[kRouteWarps][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* s_f = reinterpret_cast<float*>(s_keys[warp]);
+  pdl_wait();
+  pdl_launch_dependents();
+  float bias[NPL], largest_bias = 0.f;
+  if (KEYED) {
+#pragma unroll
+    for (int q = 0; q < NPL; ++q) {
+      const int e = lane * NPL + q;
+      bias[q] = e >= p.E ? -INFINITY : p.bias ? __ldg(p.bias + e) : 0.f;   // -inf: never among the chosen
+      if (e < p.E) largest_bias = fmaxf(largest_bias, fabsf(bias[q]));
+    }
+    largest_bias = warp_max(largest_bias);
+  }
+  // lanes a group has, where it is a run of 1, 2, 4, ... whole lanes
+  const int run = p.per % NPL == 0 && ((p.per / NPL) & (p.per / NPL - 1)) == 0 ? p.per / NPL : 0;
+  const uint32_t kOff = 0x007FFFFFu;   // the order key of -inf
+
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < p.T; t += (int64_t)gridDim.x * kRouteWarps) {
+    float c[NPL];
+    const bool finite = load_finite<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, c);
+    bool slow = __any_sync(0xFFFFFFFFu, !finite);
+    float m = 0.f, z = 1.f, near = 0.f;
+    if (!p.sigmoid && (KEYED || !p.renormalise)) {   // c becomes the numerators; experts past E give 0
+      m = c[0];
+#pragma unroll
+      for (int q = 1; q < NPL; ++q) m = fmaxf(m, c[q]);
+      m = warp_max(slow ? 0.f : m);
+      z = 0.f;
 #pragma unroll
       for (int q = 0; q < NPL; ++q) {
-        const int e = lane * NPL + q;
-        float c = -INFINITY;
-        if (x[q] != -INFINITY) {
-          const float s = p.sigmoid ? 1.f / (1.f + expf(-x[q])) : expf(x[q] - m) / z;
-          c = p.bias ? s + __ldg(p.bias + e) : s;
-          smax = fmaxf(smax, s);
-          cmax = fmaxf(cmax, fabsf(c));
-        }
-        key[q] = e < p.E ? f32_order_key(c + 0.f) : 0u;
+        const float e = expf(c[q] - m);
+        z += e;
+        if (KEYED) c[q] = e;
       }
-      // A sigmoid is within 2^-21 of itself (exp to two units in the last place, the sum's and the
-      // quotient's roundings); a softmax has its row's sum besides (16 + 5 additions: 2^-19.6). A
-      // group's score adds two keys, and a difference has two sides: four times that, and the
-      // roundings of the keys' own sums.
-      const float near = warp_max(smax) * (p.sigmoid ? 0x1p-19f : 0x1p-17f) + warp_max(cmax) * 0x1p-21f;
-      if (p.groups > 1) {
+      z = warp_sum(z);
+    }
+    if (KEYED) {
+      near = near_of(p, z, largest_bias);
+      if (p.sigmoid) {
+#pragma unroll
+        for (int q = 0; q < NPL; ++q) c[q] = key_sigmoid(c[q]) + bias[q];
+      } else {
+        const float scale = 1.f / z;
+#pragma unroll
+        for (int q = 0; q < NPL; ++q) c[q] = fmaf(c[q], scale, bias[q]);
+      }
+    }
+
+    float top = c[0];   // the lane's largest key among those that may be chosen
+    if (KEYED && p.groups > 1) {
+      float a = c[0], b = -INFINITY;   // the two largest keys
+      bool close;
+      if (run) {
+#pragma unroll
+        for (int q = 1; q < NPL; ++q) {
+          b = fmaxf(b, fminf(a, c[q]));
+          a = fmaxf(a, c[q]);
+        }
+        top = a;
+        for (int o = 1; o < run; o <<= 1) {
+          const float oa = __shfl_xor_sync(0xFFFFFFFFu, a, o), ob = __shfl_xor_sync(0xFFFFFFFFu, b, o);
+          b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+          a = fmaxf(a, oa);
+        }
+        const float score = p.group_top == 2 && p.per > 1 ? a + b : a;
+        const uint32_t kept = choose_groups(p, score, lane % run == 0 && lane / run < p.groups, near, lane, close);
+        if (!(kept >> (lane - lane % run) & 1u)) top = -INFINITY;
+      } else {
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < NPL; ++q)
-          if (lane * NPL + q < p.E) s_f[lane * NPL + q] = f32_from_order_key(key[q]);
+          if (lane * NPL + q < p.E) s_f[lane * NPL + q] = c[q];
         __syncwarp();
-        float g = 0.f;
-        uint32_t gk = 0u;
-        if (lane < p.groups) {
-          float a = -INFINITY, b = a;
+        a = -INFINITY;
+        if (lane < p.groups)
           for (int i = 0; i < p.per; ++i) {
             const float v = s_f[lane * p.per + i];
-            if (v > a) { b = a; a = v; } else if (v > b) { b = v; }
+            b = fmaxf(b, fminf(a, v));
+            a = fmaxf(a, v);
           }
-          g = p.group_top == 2 && b != -INFINITY ? a + b : a;
-          gk = f32_order_key(g + 0.f);
-        }
-        int rank = 0;
-        for (int o = 0; o < p.groups; ++o) {
-          const uint32_t v = __shfl_sync(0xFFFFFFFFu, gk, o);
-          rank += (v > gk || (v == gk && o < lane)) ? 1 : 0;
-        }
-        const bool stays = lane < p.groups && rank < p.top_groups;
-        const uint32_t kept = __ballot_sync(0xFFFFFFFFu, stays);
-        if (p.top_groups < p.groups) {   // the last group that stays against the first that goes
-          const float last = __shfl_sync(0xFFFFFFFFu, g, __ffs(__ballot_sync(0xFFFFFFFFu, lane < p.groups && rank == p.top_groups - 1)) - 1);
-          const float next = __shfl_sync(0xFFFFFFFFu, g, __ffs(__ballot_sync(0xFFFFFFFFu, lane < p.groups && rank == p.top_groups)) - 1);
-          close = next != -INFINITY && last - next <= near;
-        }
+        const float score = p.group_top == 2 && p.per > 1 ? a + b : a;
+        const uint32_t kept = choose_groups(p, score, lane < p.groups, near, lane, close);
+        top = -INFINITY;
 #pragma unroll
         for (int q = 0; q < NPL; ++q) {
           const int e = lane * NPL + q;
-          if (e < p.E && !(kept >> (e / p.per) & 1u)) key[q] = 0u;
+          if (e >= p.E || !(kept >> (e / p.per) & 1u)) c[q] = -INFINITY;
+          top = fmaxf(top, c[q]);
         }
       }
-      // one round more than k, to see how far the first that is left out lies
-      float before = INFINITY;
-      uint32_t work[NPL];
+      slow |= close;
+    } else {
 #pragma unroll
-      for (int q = 0; q < NPL; ++q) work[q] = key[q];
-#pragma unroll 1
-      for (int r = 0; r <= p.k; ++r) {
-        uint32_t bk = 0u;
-#pragma unroll
-        for (int q = 0; q < NPL; ++q) bk = max(bk, work[q]);
-        const uint32_t gmax = __reduce_max_sync(0xFFFFFFFFu, bk);
-        if (gmax == 0u) break;
-        const float v = f32_from_order_key(gmax);
-        if (v == -INFINITY) {
-          if (r == p.k) break;
-        } else {
-          close |= before - v <= near;
-        }
-        before = v;
-        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, bk == gmax)) - 1;
-        int wq = 0;
-        bool got = false;
-#pragma unroll
-        for (int q = 0; q < NPL; ++q)
-          if (!got && work[q] == gmax) { wq = q; got = true; if (lane == src) work[q] = 0u; }
-        const int e = src * NPL + __shfl_sync(0xFFFFFFFFu, wq, src);
-        if (lane == r && r < p.k) my_e = e;
-      }
-    }
-    if (!keyed) {
-#pragma unroll 1
-      for (int r = 0; r < p.k; ++r) {
-        uint32_t bk = 0u;
-#pragma unroll
-        for (int q = 0; q < NPL; ++q) bk = max(bk, key[q]);
-        const uint32_t gmax = __reduce_max_sync(0xFFFFFFFFu, bk);
-        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, bk == gmax)) - 1;
-        int wq = 0;
-        bool got = false;
-#pragma unroll
-        for (int q = 0; q < NPL; ++q)
-          if (!got && key[q] == gmax) { wq = q; got = true; if (lane == src) key[q] = 0u; }
-        const int e = src * NPL + __shfl_sync(0xFFFFFFFFu, wq, src);
-        if (lane == r) my_e = e;
-      }
-    } else if (close) {
-      __syncwarp();
-      route_exact<NPL>(p, x, s_keys[warp], lane, &my_e);
+      for (int q = 1; q < NPL; ++q) top = fmaxf(top, c[q]);
     }
 
-    // the chosen logits, from the row itself (it is in L1)
-    const bool mine = lane < p.k;
-    float v = mine ? load_one<DT>(p.logits, t * p.stride + my_e) : -INFINITY;
+    // the short list
+    uint32_t left = f32_order_key(top + 0.f), bound = 0u;
+    for (int r = 0; r < p.k; ++r) {
+      bound = __reduce_max_sync(0xFFFFFFFFu, left);
+      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, left == bound)) - 1) left = 0u;
+    }
+    const float least = f32_from_order_key(max(bound, kOff)) - near;
+    uint32_t listed = 0u;
+#pragma unroll
+    for (int q = 0; q < NPL; ++q) listed |= c[q] >= least ? 1u << q : 0u;
+    if (!(top >= least)) listed = 0u;
+    const int count = __popc(listed);
+    int at = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+      if (lane >= o) at += v;
+    }
+    const int n = __shfl_sync(0xFFFFFFFFu, at, 31);
+    slow |= bound <= kOff || n > 32;
+
+    int e = 0, rank = lane;   // the lane's expert, and its place among the chosen
+    if (!slow) {
+      at -= count;
+      __syncwarp();
+      while (listed) {
+        s_list[warp][at++] = lane * NPL + __ffs(listed) - 1;
+        listed &= listed - 1;
+      }
+      __syncwarp();
+      float key = -INFINITY, b = 0.f, v = 0.f;
+      if (lane < n) {
+        e = s_list[warp][lane];
+        v = load_one<DT>(p.logits, t * p.stride + e) + 0.f;   // the row is in L1
+        if (KEYED && p.bias) b = __ldg(p.bias + e);
+        key = !KEYED ? v : p.sigmoid ? key_sigmoid(v) + b : fmaf(expf(v - m), 1.f / z, b);
+      }
+      rank = lane < n ? 0 : 32;
+#pragma unroll 4
+      for (int o = 0; o < n; ++o) {
+        const float w = __shfl_sync(0xFFFFFFFFu, key, o);
+        if (lane < n) rank += (w > key || (w == key && o < lane)) ? 1 : 0;
+      }
+      if (KEYED) {
+        __syncwarp();
+        if (lane < n) s_sorted[warp][rank] = key;
+        __syncwarp();
+        const bool close = lane < p.k && lane + 1 < n && s_sorted[warp][lane] - s_sorted[warp][lane + 1] <= near;
+        if (__any_sync(0xFFFFFFFFu, close)) {
+          if (p.sigmoid) {
+            const unsigned long long exact =
+                lane < n ? f64_order_key(1.0 / (1.0 + exp(-(double)v)) + (double)b) : 0ull;
+            rank = lane < n ? 0 : 32;
+            for (int o = 0; o < n; ++o) {
+              const unsigned long long w = __shfl_sync(0xFFFFFFFFu, exact, o);
+              if (lane < n) rank += (w > exact || (w == exact && o < lane)) ? 1 : 0;
+            }
+          } else {   // the row's sum has to be exact too
+            slow = true;
+          }
+        }
+      }
+    }
+    if (slow) {
+      e = route_slowly<DT, NPL, VEC, KEYED>(p, t, s_keys[warp], lane);
+      rank = lane;
+      if (!p.renormalise && !p.sigmoid) {   // the sums, of the experts that are on
+        float x[NPL];
+        load_logits<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, x);
+        m = x[0];
+#pragma unroll
+        for (int q = 1; q < NPL; ++q) m = fmaxf(m, x[q]);
+        m = warp_max(m);
+        z = 0.f;
+#pragma unroll
+        for (int q = 0; q < NPL; ++q) z += x[q] == -INFINITY ? 0.f : expf(x[q] - m);
+        z = warp_sum(z);
+      }
+    }
+
+    const bool mine = rank < p.k;
+    float v = mine ? load_one<DT>(p.logits, t * p.stride + e) : -INFINITY;
     if (isnan(v)) v = -INFINITY;
     v = fminf(v, FLT_MAX);
     const bool on = v != -INFINITY;
@@ -333,8 +520,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_experts_kernel(const R
     if (p.renormalise) {
       // the scores' ratios alone count: e^(a - max a) / c with s = e^a / c, which no logit over- or underflows
       const float a = p.sigmoid ? fminf(v, 0.f) : v;
-      const float top = warp_max(a);
-      float s = on ? expf(a - top) : 0.f;
+      const float most = warp_max(a);
+      float s = on ? expf(a - most) : 0.f;
       if (p.sigmoid) s /= 1.f + expf(-fabsf(v));
       const float sum = warp_sum(s);
       w = sum > 0.f ? p.scale * (s / sum) : 0.f;
@@ -342,8 +529,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_experts_kernel(const R
       w = p.scale * (on ? (p.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - m) / z) : 0.f);
     }
     if (mine) {
-      p.idx[t * p.k + lane] = my_e;
-      p.weights[t * p.k + lane] = w;
+      p.idx[t * p.k + rank] = e;
+      p.weights[t * p.k + rank] = w;
     }
   }
 }
@@ -374,7 +561,7 @@ MOE_DEV void store_one(void* p, int64_t i, float v) {
 }
 
 template <int DT, int NPL, bool VEC>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const RouteBackParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_backward_kernel(const RouteBackParams p) {
   __shared__ float s_row[kRouteWarps][32 * NPL];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = s_row[warp];
@@ -461,7 +648,9 @@ template <class P>
 using RouteKernel = void (*)(const P);
 
 template <int DT, int NPL, bool VEC>
-RouteKernel<RouteParams> pick_kernel(const RouteParams&) { return route_experts_kernel<DT, NPL, VEC>; }
+RouteKernel<RouteParams> pick_kernel(const RouteParams& p) {
+  return p.bias || p.groups > 1 ? route_experts_kernel<DT, NPL, VEC, true> : route_experts_kernel<DT, NPL, VEC, false>;
+}
 template <int DT, int NPL, bool VEC>
 RouteKernel<RouteBackParams> pick_kernel(const RouteBackParams&) { return route_backward_kernel<DT, NPL, VEC>; }
 
@@ -475,13 +664,17 @@ RouteKernel<P> by_experts(const P& p) {
 
 template <class P>
 cudaError_t launch_route(const P& p, int dtype, bool vec, cudaStream_t s) {
+  const int num_sms = int8::device_sms();
   RouteKernel<P> f;
   if (dtype == MOE_DTYPE_F32) f = vec ? by_experts<MOE_DTYPE_F32, true>(p) : by_experts<MOE_DTYPE_F32, false>(p);
   else if (dtype == MOE_DTYPE_BF16) f = vec ? by_experts<MOE_DTYPE_BF16, true>(p) : by_experts<MOE_DTYPE_BF16, false>(p);
   else f = vec ? by_experts<MOE_DTYPE_F16, true>(p) : by_experts<MOE_DTYPE_F16, false>(p);
+  // no more CTAs than are resident at once: each warp keeps its experts' biases, and a second wave of a
+  // few CTAs would run alone
   const int64_t blocks = ((int64_t)p.T + kRouteWarps - 1) / kRouteWarps;
+  const int per_sm = p.E > 256 ? 6 : 8;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks < 152 * 16 ? blocks : 152 * 16));
+  cfg.gridDim = dim3((unsigned)(blocks < num_sms * per_sm ? blocks : num_sms * per_sm));
   cfg.blockDim = dim3(32 * kRouteWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
