@@ -126,84 +126,84 @@ MOE_DEV unsigned long long f64_order_key(double d) {
 }
 
 // ---------------------------------------------------------------- 64-bit decision
-// The k choices of one token with every score in 64 bits. keys: E doubles of this
-// warp in shared memory. Rare (see the file's head), so written for size.
-template <int NPL>
-MOE_DEV void route_exact(const RouteParams& p, const float (&x)[NPL], double* keys, int lane, int* out_e) {
+// The k choices of one token, lane r's being the r-th, with every key in 64 bits (the logits
+// themselves where nothing else is asked for). keys: E doubles of this warp in shared memory. It
+// serves the rows that the short list does not: too few lanes with an expert on, too many equal
+// keys, groups or (softmax) experts too close to tell apart in 32 bits. Rare, and so fetched cold:
+// rolled loops, as little code as can be (unrolled, its fetch alone took some 50 us of a call).
+template <int DT>
+__device__ __noinline__ int route_exact(const RouteParams& p, int64_t t, bool keyed, double* keys, int lane) {
+  const double kNone = -(double)INFINITY, kOut = __longlong_as_double(0x7FF8000000000000ll);   // off; NaN: out
   double sum = 1.0, top = 0.0;
-  if (!p.sigmoid) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int q = 0; q < NPL; ++q) m = fmaxf(m, x[q]);
-    top = (double)warp_max(m);
-    double z = 0.0;
+  const bool softmax = keyed && !p.sigmoid;
+  __syncwarp();
+  float m = -INFINITY;
 #pragma unroll 1
-    for (int q = 0; q < NPL; ++q) {
-      float v = x[0];
-#pragma unroll
-      for (int i = 1; i < NPL; ++i) if (i == q) v = x[i];
-      if (v != -INFINITY) z += exp((double)v - top);
-    }
-    sum = warp_sum64(z);
+  for (int e = lane; e < p.E; e += 32) {
+    float v = load_one<DT>(p.logits, t * p.stride + e);
+    v = isnan(v) ? -INFINITY : fminf(v, FLT_MAX) + 0.f;
+    m = fmaxf(m, v);
+    keys[e] = (double)v;
+  }
+  if (softmax) {
+    top = (double)warp_max(m);
+    sum = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32) sum += keys[e] == kNone ? 0.0 : exp(keys[e] - top);
+    sum = warp_sum64(sum);
   }
 #pragma unroll 1
-  for (int q = 0; q < NPL; ++q) {
-    float v = x[0];
-#pragma unroll
-    for (int i = 1; i < NPL; ++i) if (i == q) v = x[i];
-    const int e = lane * NPL + q;
-    if (e < p.E) {
-      double key = -(double)INFINITY;
-      if (v != -INFINITY) {
-        key = p.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - top) / sum;
-        if (p.bias) key += (double)__ldg(p.bias + e);
-      }
-      keys[e] = key;
-    }
+  for (int e = lane; keyed && e < p.E; e += 32) {
+    const double v = keys[e];
+    if (v == kNone) continue;
+    const double u = exp(softmax ? v - top : -v);
+    keys[e] = (softmax ? u / sum : 1.0 / (1.0 + u)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
   }
   __syncwarp();
   if (p.groups > 1) {
-    // lane g scores group g
-    unsigned long long gk = 0;
+    unsigned long long gk = 0;   // lane g scores group g
     if (lane < p.groups) {
-      double a = -(double)INFINITY, b = a;
+      double a = kNone, b = kNone;
+#pragma unroll 1
       for (int i = 0; i < p.per; ++i) {
         const double v = keys[lane * p.per + i];
         if (v > a) { b = a; a = v; } else if (v > b) { b = v; }
       }
       // an expert that is off adds nothing; a group with none on stays at -inf
-      gk = f64_order_key(p.group_top == 2 && b != -(double)INFINITY ? a + b : a);
+      gk = f64_order_key(p.group_top == 2 && b != kNone ? a + b : a);
     }
     int rank = 0;
+#pragma unroll 1
     for (int g = 0; g < p.groups; ++g) {
       const unsigned long long o = __shfl_sync(0xFFFFFFFFu, gk, g);
       rank += (o > gk || (o == gk && g < lane)) ? 1 : 0;
     }
     const uint32_t kept = __ballot_sync(0xFFFFFFFFu, lane < p.groups && rank < p.top_groups);
+#pragma unroll 1
     for (int e = lane; e < p.E; e += 32)
-      if (!(kept >> (e / p.per) & 1u)) keys[e] = __longlong_as_double(0x7FF8000000000000ll);   // NaN: out
+      if (!(kept >> (e / p.per) & 1u)) keys[e] = kOut;
     __syncwarp();
   }
+  int mine = 0;
 #pragma unroll 1
   for (int r = 0; r < p.k; ++r) {
     unsigned long long best = 0;
-    int be = 0;
-    for (int q = 0; q < NPL; ++q) {
-      const int e = lane * NPL + q;
-      if (e >= p.E) break;
+    uint32_t be = 0;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32) {
       const double v = keys[e];
       const unsigned long long kk = isnan(v) ? 0ull : f64_order_key(v);
       if (kk > best) { best = kk; be = e; }
     }
     const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(best >> 32));
-    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, (uint32_t)(best >> 32) == hi && (uint32_t)best == lo);
-    const int src = __ffs(who) - 1;
-    const int e = __shfl_sync(0xFFFFFFFFu, be, src);
-    if (lane == r) *out_e = e;
-    if (lane == src) keys[e] = __longlong_as_double(0x7FF8000000000000ll);
+    const bool high = (uint32_t)(best >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, high ? (uint32_t)best : 0u);
+    const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, high && (uint32_t)best == lo ? be : 0xFFFFFFFFu);
+    if (lane == r) mine = (int)e;
+    if (lane == (int)(e & 31u)) keys[e] = kOut;
     __syncwarp();
   }
+  return mine;
 }
 
 // ---------------------------------------------------------------------- forward
@@ -225,127 +225,113 @@ MOE_DEV float near_of(const RouteParams& p, float z, float largest_bias) {
   return (p.sigmoid ? 0x1p-19f : 0x1p-17f / z) + (1.f + largest_bias) * 0x1p-21f;
 }
 
-// The top_groups largest of the lanes' scores below `lanes` that are a group's, as a mask of lanes; close:
-// the last of them and the first that goes lie within `near`. score: -inf where no expert is on.
-MOE_DEV uint32_t choose_groups(const RouteParams& p, float score, bool is_group, float near, int lane, bool& close) {
-  uint32_t left = is_group ? f32_order_key(score + 0.f) : 0u, kept = 0u;
-  float before = INFINITY;
+// A key with its last 5 bits replaced by the lane: distinct, so that a warp's largest also says whose
+// it is. Off by less than 2^-18 of itself.
+MOE_DEV uint32_t lane_key(float v, int lane) { return (f32_order_key(v) & ~31u) | (uint32_t)lane; }
+
+// The top_groups largest of the scores that the lanes below p.groups hold, as a mask; close: the last
+// of them and the first that goes lie within `near`. score: -inf where no expert is on.
+MOE_DEV uint32_t choose_groups(const RouteParams& p, float score, float near, int lane, bool& close) {
+  uint32_t left = lane < p.groups ? f32_order_key(score + 0.f) : 0u, kept = 0u, g = 0u, last = 0u;
   for (int r = 0; r <= p.top_groups; ++r) {
-    const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, left);
+    last = g;
+    g = __reduce_max_sync(0xFFFFFFFFu, left);
     const uint32_t first = __ballot_sync(0xFFFFFFFFu, left == g);
-    const float v = f32_from_order_key(g);
-    if (r == p.top_groups) {
-      close = g != 0u && v != -INFINITY && before - v <= near;
-      break;
-    }
-    before = v;
-    kept |= first & (0u - first);
+    if (r < p.top_groups) kept |= first & (0u - first);
     if (lane == __ffs(first) - 1) left = 0u;
   }
+  const float a = f32_from_order_key(last), b = f32_from_order_key(g);
+  close = b != -INFINITY && a - b <= near;
   return kept;
 }
 
-// Rows that the short list does not serve: logits that are not finite, too many equal keys, too few
-// lanes with an expert on, groups or (softmax) experts too close to tell apart in 32 bits. All keys
-// one at a time, and in 64 bits where it takes that. Lane r returns the r-th choice.
-template <int DT, int NPL, bool VEC, bool KEYED>
-__device__ __noinline__ int route_slowly(const RouteParams& p, int64_t t, double* keys, int lane) {
-  float x[NPL], c[NPL];
-  load_logits<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, x);
-  int my_e = 0;
-  uint32_t key[NPL];   // 0: not to be chosen (any more)
-  bool close = KEYED;
-  if (!KEYED) {
-#pragma unroll
-    for (int q = 0; q < NPL; ++q) key[q] = lane * NPL + q < p.E ? f32_order_key(x[q]) : 0u;
-  } else if (p.groups == 1) {
-    float m = x[0], z = 1.f, top = 0.f;
-    if (!p.sigmoid) {
-#pragma unroll
-      for (int q = 1; q < NPL; ++q) m = fmaxf(m, x[q]);
-      m = warp_max(m);
-      z = 0.f;
-#pragma unroll
-      for (int q = 0; q < NPL; ++q) z += x[q] == -INFINITY ? 0.f : expf(x[q] - m);
-      z = fmaxf(warp_sum(z), 1.f);   // at least the largest's 1, where one is on
-    }
-#pragma unroll
-    for (int q = 0; q < NPL; ++q) {
-      const int e = lane * NPL + q;
-      const float b = e < p.E && p.bias ? __ldg(p.bias + e) : 0.f;
-      top = fmaxf(top, fabsf(b));
-      c[q] = x[q] == -INFINITY ? -INFINITY : (p.sigmoid ? key_sigmoid(x[q]) : expf(x[q] - m) / z) + b;
-      key[q] = e < p.E ? f32_order_key(c[q] + 0.f) : 0u;
-    }
-    const float near = near_of(p, z, warp_max(top));
-    // as below, but without taking anything off: only to see whether the choice is firm
-    uint32_t left[NPL];
-#pragma unroll
-    for (int q = 0; q < NPL; ++q) left[q] = key[q];
-    float before = INFINITY;
-    close = false;
+// The same in 64 bits for sigmoid scores, where 32 were too few: of each group's keys, those that can be
+// among its two largest, one a lane. keys: the warp's keys; second: lane g's group's second largest; list
+// and sums: 32 of shared memory each. false: more than 32 such keys.
+template <int DT>
+__device__ __noinline__ bool choose_groups_exactly(const RouteParams& p, int64_t t, const float* keys, float second,
+                                                   float near, int lane, int* list, double* sums, uint32_t* kept) {
+  int n = 0;
+  __syncwarp();
 #pragma unroll 1
-    for (int r = 0; r <= p.k; ++r) {
-      uint32_t bk = 0u;
-#pragma unroll
-      for (int q = 0; q < NPL; ++q) bk = max(bk, left[q]);
-      const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, bk);
-      const float v = f32_from_order_key(g);
-      if (g == 0u || v == -INFINITY) break;   // experts that are off go by index: nothing to tell apart
-      close |= before - v <= near;
-      before = v;
-      const int src = __ffs(__ballot_sync(0xFFFFFFFFu, bk == g)) - 1;
-      bool got = false;
-#pragma unroll
-      for (int q = 0; q < NPL; ++q)
-        if (lane == src && !got && left[q] == g) { left[q] = 0u; got = true; }
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane, g = min(e / p.per, 31);
+    const float b = __shfl_sync(0xFFFFFFFFu, second, g);
+    const bool take = e < p.E && keys[e] != -INFINITY && keys[e] >= b - near;
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, take);
+    const int at = n + __popc(who & ((1u << lane) - 1));
+    if (take && at < 32) list[at] = e;
+    n += __popc(who);
+  }
+  if (n > 32) return false;
+  sums[lane] = -(double)INFINITY;
+  __syncwarp();
+  double key = -(double)INFINITY;
+  int g = -1;
+  if (lane < n) {
+    const int e = list[lane];
+    const float v = fminf(load_one<DT>(p.logits, t * p.stride + e), FLT_MAX);
+    key = 1.0 / (1.0 + exp(-(double)v)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+    g = e / p.per;
+  }
+  int rank = 0;
+  double runner_up = 0.0;   // of the lane's group, for its first
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int o = 0; o < n; ++o) {
+      const double w = __shfl_sync(0xFFFFFFFFu, key, o);
+      const int og = __shfl_sync(0xFFFFFFFFu, g, o), orank = __shfl_sync(0xFFFFFFFFu, rank, o);
+      if (og != g) continue;
+      if (pass == 0) rank += (w > key || (w == key && o < lane)) ? 1 : 0;
+      else if (orank == 1 && p.group_top == 2) runner_up = w;
     }
   }
-  if (close) {
-    __syncwarp();
-    route_exact<NPL>(p, x, keys, lane, &my_e);
-    return my_e;
-  }
+  if (lane < n && rank == 0) sums[g] = key + runner_up;
+  __syncwarp();
+  const unsigned long long score = lane < p.groups ? f64_order_key(sums[lane]) : 0ull;
+  int place = 0;
 #pragma unroll 1
-  for (int r = 0; r < p.k; ++r) {
-    uint32_t bk = 0u;
-#pragma unroll
-    for (int q = 0; q < NPL; ++q) bk = max(bk, key[q]);
-    const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, bk);
-    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, bk == g)) - 1;
-    int wq = 0;
-    bool got = false;
-#pragma unroll
-    for (int q = 0; q < NPL; ++q)
-      if (!got && key[q] == g) { wq = q; got = true; if (lane == src) key[q] = 0u; }
-    const int e = src * NPL + __shfl_sync(0xFFFFFFFFu, wq, src);
-    if (lane == r) my_e = e;
+  for (int o = 0; o < p.groups; ++o) {
+    const unsigned long long w = __shfl_sync(0xFFFFFFFFu, score, o);
+    place += (w > score || (w == score && o < lane)) ? 1 : 0;
   }
-  return my_e;
+  *kept = __ballot_sync(0xFFFFFFFFu, lane < p.groups && place < p.top_groups);
+  __syncwarp();
+  return true;
+}
+
+MOE_DEV float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // Nearly all rows: the k-th largest of the lanes' largest keys is at most the k-th largest key, and few
 // keys lie above it (about 10 for k = 8). These, each in a lane of its own and in the order of their
 // indexes, are ranked by counting; with a bias or groups, keys closer than `near` are ranked again in
 // 64 bits, one evaluation a lane.
-// Bound by its instructions, some 500 a row of 512 (65,536 rows of 512 bf16 logits: see the launch).
+// What bounds it is its instructions, a warp's per row, not the 16 bytes a lane that it reads.
 template <int DT, int NPL, bool VEC, bool KEYED>
-__global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_experts_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(const RouteParams p) {
   __shared__ double s_keys[kRouteWarps][32 * NPL];
+  __shared__ float s_bias[KEYED ? 32 * NPL : 1];   // [q][lane]
   __shared__ int s_list[kRouteWarps][32];
   __shared__ float s_sorted[kRouteWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* s_f = reinterpret_cast<float*>(s_keys[warp]);
   pdl_wait();
   pdl_launch_dependents();
-  float bias[NPL], largest_bias = 0.f;
+  float largest_bias = 0.f;
   if (KEYED) {
-#pragma unroll
-    for (int q = 0; q < NPL; ++q) {
-      const int e = lane * NPL + q;
-      bias[q] = e >= p.E ? -INFINITY : p.bias ? __ldg(p.bias + e) : 0.f;   // -inf: never among the chosen
-      if (e < p.E) largest_bias = fmaxf(largest_bias, fabsf(bias[q]));
+    for (int i = threadIdx.x; i < 32 * NPL; i += 32 * kRouteWarps) {
+      const int e = (i & 31) * NPL + (i >> 5);
+      s_bias[i] = e >= p.E ? -INFINITY : p.bias ? __ldg(p.bias + e) : 0.f;   // -inf: never among the chosen
     }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < NPL; ++q)
+      if (lane * NPL + q < p.E) largest_bias = fmaxf(largest_bias, fabsf(s_bias[32 * q + lane]));
     largest_bias = warp_max(largest_bias);
   }
   // lanes a group has, where it is a run of 1, 2, 4, ... whole lanes
@@ -354,14 +340,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_exp
 
   for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < p.T; t += (int64_t)gridDim.x * kRouteWarps) {
     float c[NPL];
-    const bool finite = load_finite<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, c);
-    bool slow = __any_sync(0xFFFFFFFFu, !finite);
+    const bool odd = __any_sync(0xFFFFFFFFu, !load_finite<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, c));
+    if (odd) load_logits<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, c);
+    bool slow = false;
     float m = 0.f, z = 1.f, near = 0.f;
-    if (!p.sigmoid && (KEYED || !p.renormalise)) {   // c becomes the numerators; experts past E give 0
+    if (!p.sigmoid && (KEYED || !p.renormalise)) {   // c becomes the numerators; what is off or past E gives 0
       m = c[0];
 #pragma unroll
       for (int q = 1; q < NPL; ++q) m = fmaxf(m, c[q]);
-      m = warp_max(slow ? 0.f : m);
+      m = fmaxf(warp_max(m), -FLT_MAX);   // also where nothing is on
       z = 0.f;
 #pragma unroll
       for (int q = 0; q < NPL; ++q) {
@@ -375,48 +362,70 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_exp
       near = near_of(p, z, largest_bias);
       if (p.sigmoid) {
 #pragma unroll
-        for (int q = 0; q < NPL; ++q) c[q] = key_sigmoid(c[q]) + bias[q];
+        for (int q = 0; q < NPL; ++q) c[q] = key_sigmoid(c[q]) + s_bias[32 * q + lane];
       } else {
         const float scale = 1.f / z;
 #pragma unroll
-        for (int q = 0; q < NPL; ++q) c[q] = fmaf(c[q], scale, bias[q]);
+        for (int q = 0; q < NPL; ++q) c[q] = fmaf(c[q], scale, s_bias[32 * q + lane]);
+      }
+      if (odd) {
+        float x[NPL];
+        load_logits<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, x);
+#pragma unroll
+        for (int q = 0; q < NPL; ++q)
+          if (x[q] == -INFINITY) c[q] = -INFINITY;
       }
     }
 
     float top = c[0];   // the lane's largest key among those that may be chosen
+#pragma unroll
+    for (int q = 1; q < NPL; ++q) top = fmaxf(top, c[q]);
     if (KEYED && p.groups > 1) {
-      float a = c[0], b = -INFINITY;   // the two largest keys
-      bool close;
+      float a = -INFINITY, b = -INFINITY;   // lane g: the two largest keys of group g
       if (run) {
+        a = c[0];
 #pragma unroll
         for (int q = 1; q < NPL; ++q) {
           b = fmaxf(b, fminf(a, c[q]));
           a = fmaxf(a, c[q]);
         }
-        top = a;
         for (int o = 1; o < run; o <<= 1) {
           const float oa = __shfl_xor_sync(0xFFFFFFFFu, a, o), ob = __shfl_xor_sync(0xFFFFFFFFu, b, o);
           b = fmaxf(fmaxf(b, ob), fminf(a, oa));
           a = fmaxf(a, oa);
         }
-        const float score = p.group_top == 2 && p.per > 1 ? a + b : a;
-        const uint32_t kept = choose_groups(p, score, lane % run == 0 && lane / run < p.groups, near, lane, close);
-        if (!(kept >> (lane - lane % run) & 1u)) top = -INFINITY;
+        a = __shfl_sync(0xFFFFFFFFu, a, (lane * run) & 31);
+        b = __shfl_sync(0xFFFFFFFFu, b, (lane * run) & 31);
       } else {
         __syncwarp();
 #pragma unroll
-        for (int q = 0; q < NPL; ++q)
-          if (lane * NPL + q < p.E) s_f[lane * NPL + q] = c[q];
+        for (int q = 0; q < NPL; ++q) s_f[lane * NPL + q] = c[q];
         __syncwarp();
-        a = -INFINITY;
         if (lane < p.groups)
           for (int i = 0; i < p.per; ++i) {
             const float v = s_f[lane * p.per + i];
             b = fmaxf(b, fminf(a, v));
             a = fmaxf(a, v);
           }
-        const float score = p.group_top == 2 && p.per > 1 ? a + b : a;
-        const uint32_t kept = choose_groups(p, score, lane < p.groups, near, lane, close);
+      }
+      // an expert that is off adds nothing
+      const float score = p.group_top == 2 && b != -INFINITY ? a + b : a;
+      bool close;
+      uint32_t kept = choose_groups(p, score, near, lane, close);
+      if (close) {
+        slow = true;
+        if (p.sigmoid) {
+          if (run) {
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < NPL; ++q) s_f[lane * NPL + q] = c[q];
+          }
+          slow = !choose_groups_exactly<DT>(p, t, s_f, b, near, lane, s_list[warp], s_keys[warp] + 16 * NPL, &kept);
+        }
+      }
+      if (run) {
+        if (!(kept >> (lane / run) & 1u)) top = -INFINITY;
+      } else {
         top = -INFINITY;
 #pragma unroll
         for (int q = 0; q < NPL; ++q) {
@@ -425,19 +434,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_exp
           top = fmaxf(top, c[q]);
         }
       }
-      slow |= close;
-    } else {
-#pragma unroll
-      for (int q = 1; q < NPL; ++q) top = fmaxf(top, c[q]);
     }
 
     // the short list
-    uint32_t left = f32_order_key(top + 0.f), bound = 0u;
+    uint32_t left = lane_key(top + 0.f, lane), bound = 0u;
     for (int r = 0; r < p.k; ++r) {
       bound = __reduce_max_sync(0xFFFFFFFFu, left);
-      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, left == bound)) - 1) left = 0u;
+      if (left == bound) left = 0u;
     }
-    const float least = f32_from_order_key(max(bound, kOff)) - near;
+    const float least = f32_from_order_key(max(bound & ~31u, kOff)) - near;
     uint32_t listed = 0u;
 #pragma unroll
     for (int q = 0; q < NPL; ++q) listed |= c[q] >= least ? 1u << q : 0u;
@@ -450,9 +455,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_exp
       if (lane >= o) at += v;
     }
     const int n = __shfl_sync(0xFFFFFFFFu, at, 31);
-    slow |= bound <= kOff || n > 32;
+    slow |= (bound & ~31u) <= kOff || n > 32;
 
     int e = 0, rank = lane;   // the lane's expert, and its place among the chosen
+    float v = 0.f;            // its logit
     if (!slow) {
       at -= count;
       __syncwarp();
@@ -461,18 +467,19 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_exp
         listed &= listed - 1;
       }
       __syncwarp();
-      float key = -INFINITY, b = 0.f, v = 0.f;
+      float key = -INFINITY, b = 0.f;
+      rank = 32;
       if (lane < n) {
         e = s_list[warp][lane];
-        v = load_one<DT>(p.logits, t * p.stride + e) + 0.f;   // the row is in L1
-        if (KEYED && p.bias) b = __ldg(p.bias + e);
+        v = fminf(load_one<DT>(p.logits, t * p.stride + e), FLT_MAX) + 0.f;   // the row is in L1
+        if (KEYED) b = s_bias[32 * (e % NPL) + e / NPL];
         key = !KEYED ? v : p.sigmoid ? key_sigmoid(v) + b : fmaf(expf(v - m), 1.f / z, b);
+        rank = 0;
       }
-      rank = lane < n ? 0 : 32;
 #pragma unroll 4
       for (int o = 0; o < n; ++o) {
         const float w = __shfl_sync(0xFFFFFFFFu, key, o);
-        if (lane < n) rank += (w > key || (w == key && o < lane)) ? 1 : 0;
+        rank += (w > key || (w == key && o < lane)) ? 1 : 0;   // lanes past n stay at 32 and more
       }
       if (KEYED) {
         __syncwarp();
@@ -484,9 +491,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_exp
             const unsigned long long exact =
                 lane < n ? f64_order_key(1.0 / (1.0 + exp(-(double)v)) + (double)b) : 0ull;
             rank = lane < n ? 0 : 32;
+#pragma unroll 1
             for (int o = 0; o < n; ++o) {
               const unsigned long long w = __shfl_sync(0xFFFFFFFFu, exact, o);
-              if (lane < n) rank += (w > exact || (w == exact && o < lane)) ? 1 : 0;
+              rank += (w > exact || (w == exact && o < lane)) ? 1 : 0;
             }
           } else {   // the row's sum has to be exact too
             slow = true;
@@ -495,36 +503,22 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_exp
       }
     }
     if (slow) {
-      e = route_slowly<DT, NPL, VEC, KEYED>(p, t, s_keys[warp], lane);
+      e = route_exact<DT>(p, t, KEYED, s_keys[warp], lane);
       rank = lane;
-      if (!p.renormalise && !p.sigmoid) {   // the sums, of the experts that are on
-        float x[NPL];
-        load_logits<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, x);
-        m = x[0];
-#pragma unroll
-        for (int q = 1; q < NPL; ++q) m = fmaxf(m, x[q]);
-        m = warp_max(m);
-        z = 0.f;
-#pragma unroll
-        for (int q = 0; q < NPL; ++q) z += x[q] == -INFINITY ? 0.f : expf(x[q] - m);
-        z = warp_sum(z);
-      }
+      v = lane < p.k ? load_one<DT>(p.logits, t * p.stride + e) : 0.f;
+      v = isnan(v) ? -INFINITY : fminf(v, FLT_MAX);
     }
 
-    const bool mine = rank < p.k;
-    float v = mine ? load_one<DT>(p.logits, t * p.stride + e) : -INFINITY;
-    if (isnan(v)) v = -INFINITY;
-    v = fminf(v, FLT_MAX);
-    const bool on = v != -INFINITY;
-    float w;
+    const bool mine = rank < p.k, on = mine && v != -INFINITY;
+    float s = 0.f, w;
     if (p.renormalise) {
-      // the scores' ratios alone count: e^(a - max a) / c with s = e^a / c, which no logit over- or underflows
-      const float a = p.sigmoid ? fminf(v, 0.f) : v;
+      // the scores' ratios alone count: e^(a - max a) / d with s = e^a / d, which no logit over- or underflows
+      const float a = on ? p.sigmoid ? fminf(v, 0.f) : v : -INFINITY;
       const float most = warp_max(a);
-      float s = on ? expf(a - most) : 0.f;
-      if (p.sigmoid) s /= 1.f + expf(-fabsf(v));
+      if (on) s = expf(a - most);
+      if (p.sigmoid) s *= rcp(1.f + expf(-fabsf(v)));
       const float sum = warp_sum(s);
-      w = sum > 0.f ? p.scale * (s / sum) : 0.f;
+      w = sum > 0.f ? p.scale * (s * rcp(sum)) : 0.f;
     } else {
       w = p.scale * (on ? (p.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - m) / z) : 0.f);
     }
@@ -561,7 +555,7 @@ MOE_DEV void store_one(void* p, int64_t i, float v) {
 }
 
 template <int DT, int NPL, bool VEC>
-__global__ void __launch_bounds__(32 * kRouteWarps, NPL == 16 ? 6 : 8) route_backward_kernel(const RouteBackParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps, 8) route_backward_kernel(const RouteBackParams p) {
   __shared__ float s_row[kRouteWarps][32 * NPL];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = s_row[warp];
@@ -672,7 +666,7 @@ cudaError_t launch_route(const P& p, int dtype, bool vec, cudaStream_t s) {
   // no more CTAs than are resident at once: each warp keeps its experts' biases, and a second wave of a
   // few CTAs would run alone
   const int64_t blocks = ((int64_t)p.T + kRouteWarps - 1) / kRouteWarps;
-  const int per_sm = p.E > 256 ? 6 : 8;
+  const int per_sm = 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks < num_sms * per_sm ? blocks : num_sms * per_sm));
   cfg.blockDim = dim3(32 * kRouteWarps);
