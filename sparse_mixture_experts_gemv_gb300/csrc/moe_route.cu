@@ -51,41 +51,52 @@ MOE_DEV float load_one(const void* p, int64_t i) {
   return __half2float(__ushort_as_half(v));
 }
 
-// The lane's NPL logits of a row; -inf for experts past E. VEC: rows start on
-// 16-byte boundaries and E is a multiple of what one 16-byte load holds.
+// The lane's NPL logits of a row as they are, -inf for experts past E; false where one is not
+// finite. VEC: rows start on 16-byte boundaries and E is a multiple of what one 16-byte load holds.
 template <int DT, int NPL, bool VEC>
-MOE_DEV void load_raw(const void* logits, int64_t row0, int E, int lane, float (&x)[NPL]) {
+MOE_DEV bool load_raw(const void* logits, int64_t row0, int E, int lane, float (&x)[NPL]) {
   constexpr int per16 = DT == MOE_DTYPE_F32 ? 4 : 8;
+  constexpr uint32_t kOffPair = DT == MOE_DTYPE_F32 ? 0xFF800000u : DT == MOE_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+  float zero = 0.f;   // NaN from infinities and NaN
   if constexpr (VEC && NPL % per16 == 0) {
     const char* p = static_cast<const char*>(logits) + (row0 + lane * NPL) * (16 / per16);
 #pragma unroll
     for (int c = 0; c < NPL / per16; ++c) {
-      uint32_t w[4] = {0, 0, 0, 0};
+      uint4 v = make_uint4(kOffPair, kOffPair, kOffPair, kOffPair);
       const bool in = lane * NPL + c * per16 < E;
-      if (in) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + c);
-        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-      }
+      if (in) v = __ldg(reinterpret_cast<const uint4*>(p) + c);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float y[per16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (DT == MOE_DTYPE_F32) {
-          x[4 * c + i] = in ? __uint_as_float(w[i]) : -INFINITY;
+          y[i] = __uint_as_float(w[i]);
         } else if (DT == MOE_DTYPE_BF16) {
-          x[(8 * c + 2 * i) % NPL] = in ? bf16_lo(w[i]) : -INFINITY;
-          x[(8 * c + 2 * i + 1) % NPL] = in ? bf16_hi(w[i]) : -INFINITY;
+          y[(2 * i) % per16] = bf16_lo(w[i]);
+          y[(2 * i + 1) % per16] = bf16_hi(w[i]);
         } else {
-          x[(8 * c + 2 * i) % NPL] = in ? __half2float(__ushort_as_half((uint16_t)w[i])) : -INFINITY;
-          x[(8 * c + 2 * i + 1) % NPL] = in ? __half2float(__ushort_as_half((uint16_t)(w[i] >> 16))) : -INFINITY;
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          y[(2 * i) % per16] = f.x;
+          y[(2 * i + 1) % per16] = f.y;
         }
       }
+      float chunk = 0.f;
+#pragma unroll
+      for (int i = 0; i < per16; ++i) {
+        chunk = fmaf(y[i], 0.f, chunk);
+        x[c * per16 + i] = y[i];
+      }
+      if (in) zero += chunk;
     }
   } else {
 #pragma unroll
     for (int q = 0; q < NPL; ++q) {
       const int e = lane * NPL + q;
       x[q] = e < E ? load_one<DT>(logits, row0 + e) : -INFINITY;
+      zero = fmaf(e < E ? x[q] : 0.f, 0.f, zero);
     }
   }
+  return zero == 0.f;
 }
 
 // The same with NaN as -inf and +inf as the largest finite value.
@@ -98,17 +109,6 @@ MOE_DEV void load_logits(const void* logits, int64_t row0, int E, int lane, floa
     x[q] = fminf(x[q], FLT_MAX) + 0.0f;   // -0 becomes +0: equal logits have equal keys
   }
 }
-
-// The same for rows of finite logits, as they are; false where the lane has one that is not.
-template <int DT, int NPL, bool VEC>
-MOE_DEV bool load_finite(const void* logits, int64_t row0, int E, int lane, float (&x)[NPL]) {
-  load_raw<DT, NPL, VEC>(logits, row0, E, lane, x);
-  float zero = 0.f;
-#pragma unroll
-  for (int q = 0; q < NPL; ++q) zero = fmaf(lane * NPL + q < E ? x[q] : 0.f, 0.f, zero);   // NaN from inf and NaN
-  return zero == 0.f;
-}
-
 
 MOE_DEV float warp_max(float v) {
   return f32_from_order_key(__reduce_max_sync(0xFFFFFFFFu, f32_order_key(v)));
@@ -315,7 +315,8 @@ MOE_DEV float rcp(float v) {
 template <int DT, int NPL, bool VEC, bool KEYED>
 __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(const RouteParams p) {
   __shared__ double s_keys[kRouteWarps][32 * NPL];
-  __shared__ float s_bias[KEYED ? 32 * NPL : 1];   // [q][lane]
+  constexpr int kVec = NPL < 4 ? NPL : 4;
+  __shared__ __align__(16) float s_bias[KEYED ? 32 * NPL : 4];   // [q / kVec][lane][kVec]
   __shared__ int s_list[kRouteWarps][32];
   __shared__ float s_sorted[kRouteWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -325,13 +326,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
   float largest_bias = 0.f;
   if (KEYED) {
     for (int i = threadIdx.x; i < 32 * NPL; i += 32 * kRouteWarps) {
-      const int e = (i & 31) * NPL + (i >> 5);
+      const int e = (i / kVec & 31) * NPL + i / (32 * kVec) * kVec + i % kVec;
       s_bias[i] = e >= p.E ? -INFINITY : p.bias ? __ldg(p.bias + e) : 0.f;   // -inf: never among the chosen
     }
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < NPL; ++q)
-      if (lane * NPL + q < p.E) largest_bias = fmaxf(largest_bias, fabsf(s_bias[32 * q + lane]));
+    for (int i = lane; i < 32 * NPL; i += 32)
+      if (s_bias[i] != -INFINITY) largest_bias = fmaxf(largest_bias, fabsf(s_bias[i]));
     largest_bias = warp_max(largest_bias);
   }
   // lanes a group has, where it is a run of 1, 2, 4, ... whole lanes
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
 
   for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < p.T; t += (int64_t)gridDim.x * kRouteWarps) {
     float c[NPL];
-    const bool odd = __any_sync(0xFFFFFFFFu, !load_finite<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, c));
+    const bool odd = __any_sync(0xFFFFFFFFu, !load_raw<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, c));
     if (odd) load_logits<DT, NPL, VEC>(p.logits, t * p.stride, p.E, lane, c);
     bool slow = false;
     float m = 0.f, z = 1.f, near = 0.f;
@@ -360,13 +360,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
     }
     if (KEYED) {
       near = near_of(p, z, largest_bias);
+      float bias[NPL];
+#pragma unroll
+      for (int q = 0; q < NPL; q += kVec) {
+        const float* b = s_bias + (q * 32 + lane * kVec);
+        if constexpr (kVec == 4) *reinterpret_cast<float4*>(bias + q) = *reinterpret_cast<const float4*>(b);
+        else *reinterpret_cast<float2*>(bias + q) = *reinterpret_cast<const float2*>(b);
+      }
       if (p.sigmoid) {
 #pragma unroll
-        for (int q = 0; q < NPL; ++q) c[q] = key_sigmoid(c[q]) + s_bias[32 * q + lane];
+        for (int q = 0; q < NPL; ++q) c[q] = key_sigmoid(c[q]) + bias[q];
       } else {
         const float scale = 1.f / z;
 #pragma unroll
-        for (int q = 0; q < NPL; ++q) c[q] = fmaf(c[q], scale, s_bias[32 * q + lane]);
+        for (int q = 0; q < NPL; ++q) c[q] = fmaf(c[q], scale, bias[q]);
       }
       if (odd) {
         float x[NPL];
@@ -378,9 +385,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
     }
 
     float top = c[0];   // the lane's largest key among those that may be chosen
+    if (!KEYED || p.groups == 1) {
 #pragma unroll
-    for (int q = 1; q < NPL; ++q) top = fmaxf(top, c[q]);
-    if (KEYED && p.groups > 1) {
+      for (int q = 1; q < NPL; ++q) top = fmaxf(top, c[q]);
+    } else {
       float a = -INFINITY, b = -INFINITY;   // lane g: the two largest keys of group g
       if (run) {
         a = c[0];
@@ -389,6 +397,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
           b = fmaxf(b, fminf(a, c[q]));
           a = fmaxf(a, c[q]);
         }
+        top = a;
         for (int o = 1; o < run; o <<= 1) {
           const float oa = __shfl_xor_sync(0xFFFFFFFFu, a, o), ob = __shfl_xor_sync(0xFFFFFFFFu, b, o);
           b = fmaxf(fmaxf(b, ob), fminf(a, oa));
@@ -472,7 +481,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
       if (lane < n) {
         e = s_list[warp][lane];
         v = fminf(load_one<DT>(p.logits, t * p.stride + e), FLT_MAX) + 0.f;   // the row is in L1
-        if (KEYED) b = s_bias[32 * (e % NPL) + e / NPL];
+        if (KEYED) b = s_bias[(e % NPL / kVec * 32 + e / NPL) * kVec + e % kVec];
         key = !KEYED ? v : p.sigmoid ? key_sigmoid(v) + b : fmaf(expf(v - m), 1.f / z, b);
         rank = 0;
       }
