@@ -71,7 +71,7 @@ MOE_DEV void dot_rows(const int8_t* const (&p)[R], const uint4* q, int nch, int 
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[r][t] = 0;
-#pragma unroll 2
+#pragma unroll T == 1 ? 4 : 2
   for (int c = lane; c < nch; c += 32) {
     uint4 w[R];
 #pragma unroll
@@ -101,8 +101,11 @@ struct StreamParams {
   int out_dtype, T, N, K;
 };
 
+// CTAs an SM holds at once, by tokens: what their accumulators and loads in flight leave of the registers.
+constexpr int stream_ctas(int tokens) { return tokens >= 4 ? 2 : 3; }
+
 template <int DT, int T>
-__global__ void __launch_bounds__(kThreads, T >= 4 ? 2 : 3) int8_stream_kernel(const StreamParams p) {
+__global__ void __launch_bounds__(kThreads, stream_ctas(T)) int8_stream_kernel(const StreamParams p) {
   extern __shared__ uint4 q[];   // [T][K / 16]
   __shared__ uint32_t red[kWarps][kMaxStreamT];
   __shared__ float s_scale[kMaxStreamT];
@@ -148,7 +151,8 @@ cudaError_t launch_stream_t(const StreamParams& p, int num_sms, cudaStream_t s) 
   const int64_t blocks = (p.N + kWarps * kRows - 1) / (kWarps * kRows);
   const int chunks = (p.T + T - 1) / T;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks < num_sms * 4 ? blocks : num_sms * 4), chunks);
+  const int64_t resident = num_sms * stream_ctas(T);   // each quantizes the tokens once and takes many rows
+  cfg.gridDim = dim3((unsigned)(blocks < resident ? blocks : resident), chunks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -189,7 +193,8 @@ struct ExpertsParams {
 
 constexpr int kFeatures = 2 * kWarps;   // intermediate features of a CTA: two a warp (four rows)
 
-// h of one choice (blockIdx.y) and kFeatures features.
+// h of one choice (blockIdx.y) and kFeatures features. As soon as the expert is known its rows are
+// requested into L2, two contiguous pieces: they come while the token is being quantized.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 3) int8_experts_up_kernel(const ExpertsParams p) {
   extern __shared__ uint4 q[];   // [H / 16]
@@ -201,13 +206,16 @@ __global__ void __launch_bounds__(kThreads, 3) int8_experts_up_kernel(const Expe
   for (int64_t a = blockIdx.y; a < (int64_t)p.T * p.k; a += gridDim.y) {
     const int e = __ldg(p.idx + a);
     if (e < 0 || e >= p.E) continue;
+    const int64_t row0 = (int64_t)e * 2 * p.I;
+    const int c0 = blockIdx.x * kFeatures;
+    if (threadIdx.x < 2)
+      prefetch_l2_bulk(p.gate_up + (row0 + (threadIdx.x ? p.I : 0) + c0) * p.H, (uint32_t)(min(kFeatures, p.I - c0) * p.H));
     __syncthreads();
     quantize_rows_to_smem<DT>(static_cast<const uint16_t*>(p.x) + a / p.k * p.H, p.H, nullptr, 1, p.H, q, s_scale, red);
     __syncthreads();
-    const int f0 = blockIdx.x * kFeatures + 2 * warp;
+    const int f0 = c0 + 2 * warp;
     if (f0 >= p.I) continue;
     const int f1 = min(f0 + 1, p.I - 1);
-    const int64_t row0 = (int64_t)e * 2 * p.I;
     const int8_t* rows[4] = {p.gate_up + (row0 + f0) * p.H, p.gate_up + (row0 + p.I + f0) * p.H,
                              p.gate_up + (row0 + f1) * p.H, p.gate_up + (row0 + p.I + f1) * p.H};
     int acc[4][1];
@@ -221,74 +229,92 @@ __global__ void __launch_bounds__(kThreads, 3) int8_experts_up_kernel(const Expe
   }
 }
 
-constexpr int kDownThreads = 128;
-constexpr int kDownChannels = 2 * (kDownThreads / 32);
+constexpr int kDownChannels = kWarps;   // channels of a CTA: one a warp
 constexpr int kMaxChoices = MOE_ROUTE_MAX_TOP_K;
 
-// out of one token (blockIdx.y) and kDownChannels channels, all its choices.
-// Dynamic shared memory: `held` quantized rows of h.
-__global__ void __launch_bounds__(kDownThreads, 6) int8_experts_down_kernel(const ExpertsParams p, int held) {
+// out of one token (blockIdx.y) and kDownChannels channels, all its choices. Dynamic shared memory:
+// `held` quantized rows of h. The rows of the weights are known before h is: they are requested
+// into L2 while the kernel before is still at work. (Reading idx and the weights' addresses ahead of
+// the wait is sound: that kernel lets this one start only after its own wait, when all that the
+// caller had enqueued is done.)
+__global__ void __launch_bounds__(kThreads, 4) int8_experts_down_kernel(const ExpertsParams p, int held) {
   extern __shared__ uint4 q[];   // [held][I / 16]
   __shared__ float s_scale[kMaxChoices];
   __shared__ int s_e[kMaxChoices];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nch = p.I / 16;
+  const int c0 = blockIdx.x * kDownChannels;
+  if (threadIdx.x < p.k) {
+    const int e = __ldg(p.idx + (int64_t)blockIdx.y * p.k + threadIdx.x);
+    if (e >= 0 && e < p.E)
+      prefetch_l2_bulk(p.down + ((int64_t)e * p.H + c0) * p.I, (uint32_t)(min(kDownChannels, p.H - c0) * p.I));
+  }
   pdl_wait();
   pdl_launch_dependents();
+  const int ch = c0 + warp;
   for (int64_t t = blockIdx.y; t < p.T; t += gridDim.y) {
-    const int c0 = blockIdx.x * kDownChannels + 2 * warp, c1 = min(c0 + 1, p.H - 1);
-    float sum0 = 0.f, sum1 = 0.f;
+    float sum = 0.f;
     for (int j0 = 0; j0 < p.k; j0 += held) {
       const int nj = min(held, p.k - j0);
       __syncthreads();
-      for (int j = warp; j < nj; j += kDownThreads / 32) {
+      for (int j = warp; j < nj; j += kWarps) {
         const int64_t a = t * p.k + j0 + j;
         int e = __ldg(p.idx + a);
         if (e < 0 || e >= p.E) e = -1;
         if (e >= 0) {
-          float v[16];
+          const float weight = __ldg(p.weights + a);
+          const float* h = p.h + a * p.I;
+          float v[16], u[16];   // the row's first 1024 values stay in registers
           uint32_t m = 0;
-          for (int c = lane; c < nch; c += 32) {
-            load16_cg(p.h + a * p.I + 16 * c, v);
-            m = max(m, amax_bits(v));
+          if (lane < nch) {
+            load16_cg(h + 16 * lane, v);
+            m = amax_bits(v);
+          }
+          if (lane + 32 < nch) {
+            load16_cg(h + 16 * (lane + 32), u);
+            m = max(m, amax_bits(u));
+          }
+          for (int c = lane + 64; c < nch; c += 32) {
+            float w[16];
+            load16_cg(h + 16 * c, w);
+            m = max(m, amax_bits(w));
           }
           const RowScale r = row_scale(__reduce_max_sync(0xFFFFFFFFu, m));
-          for (int c = lane; c < nch; c += 32) {
-            load16_cg(p.h + a * p.I + 16 * c, v);
+          if (lane < nch) q[j * nch + lane] = quantize16(v, r);
+          if (lane + 32 < nch) q[j * nch + lane + 32] = quantize16(u, r);
+          for (int c = lane + 64; c < nch; c += 32) {
+            load16_cg(h + 16 * c, v);
             q[j * nch + c] = quantize16(v, r);
           }
-          if (lane == 0) s_scale[j] = r.scale * __ldg(p.weights + a);
+          if (lane == 0) s_scale[j] = r.scale * weight;
         }
         if (lane == 0) s_e[j] = e;
       }
       __syncthreads();
-      if (c0 < p.H) {
-        float ws0 = 0.f, ws1 = 0.f;   // lane j: the scales of choice j
-        if (lane < nj && s_e[lane] >= 0) {
-          ws0 = s_scale[lane] * __ldg(p.down_scale + (int64_t)s_e[lane] * p.H + c0);
-          ws1 = s_scale[lane] * __ldg(p.down_scale + (int64_t)s_e[lane] * p.H + c1);
-        }
-#pragma unroll 4
-        for (int j = 0; j < nj; ++j) {
-          const int e = s_e[j];
-          const float f0 = __shfl_sync(0xFFFFFFFFu, ws0, j), f1 = __shfl_sync(0xFFFFFFFFu, ws1, j);
-          if (e < 0) continue;
-          const int8_t* r0 = p.down + ((int64_t)e * p.H + c0) * p.I;
-          const int8_t* r1 = p.down + ((int64_t)e * p.H + c1) * p.I;
-          int a0 = 0, a1 = 0;
-          for (int c = lane; c < nch; c += 32) {
-            const uint4 w0 = ldg_stream(r0 + 16 * c), w1 = ldg_stream(r1 + 16 * c), xv = q[j * nch + c];
-            a0 = dot16(w0, xv, a0);
-            a1 = dot16(w1, xv, a1);
+      if (ch < p.H) {
+        float ws = 0.f;   // lane j: the scales of choice j
+        if (lane < nj && s_e[lane] >= 0) ws = s_scale[lane] * __ldg(p.down_scale + (int64_t)s_e[lane] * p.H + ch);
+        for (int cb = 0; cb < nch; cb += 32) {
+          const int c = cb + lane;
+          for (int jb = 0; jb < nj; jb += 8) {
+            uint4 w[8];   // eight choices' rows at once: all loads before the first product
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              w[i] = make_uint4(0, 0, 0, 0);
+              const int e = jb + i < nj ? s_e[jb + i] : -1;
+              if (e >= 0 && c < nch) w[i] = ldg_stream(p.down + ((int64_t)e * p.H + ch) * p.I + 16 * c);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float f = __shfl_sync(0xFFFFFFFFu, ws, jb + i);
+              if (jb + i < nj && s_e[jb + i] >= 0 && c < nch) sum += (float)dot16(w[i], q[(jb + i) * nch + c], 0) * f;
+            }
           }
-          sum0 += (float)a0 * f0;
-          sum1 += (float)a1 * f1;
         }
       }
     }
-    sum0 = warp_sum(sum0);
-    sum1 = warp_sum(sum1);
-    if (lane < 2 && c0 + lane < p.H) store(p.out, p.out_dtype, t * p.H + c0 + lane, lane ? sum1 : sum0);
+    sum = warp_sum(sum);
+    if (lane == 0 && ch < p.H) store(p.out, p.out_dtype, t * p.H + ch, sum);
   }
 }
 
@@ -575,7 +601,7 @@ cudaError_t launch_experts_stream(const ExpertsParams& p, int x_dtype, cudaStrea
   int held = 32 * 1024 / p.I;   // rows of h a CTA keeps: 32 KB, so that several CTAs share an SM
   held = held < 1 ? 1 : held < p.k ? held : p.k;
   const dim3 down((p.H + kDownChannels - 1) / kDownChannels, (unsigned)(p.T < 65535 ? p.T : 65535));
-  return launch_pdl(int8_experts_down_kernel, down, kDownThreads, (size_t)held * p.I, s, p, held);
+  return launch_pdl(int8_experts_down_kernel, down, kThreads, (size_t)held * p.I, s, p, held);
 }
 
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {

@@ -8,7 +8,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import DTYPE_CODES, check, invalid, raw_stream, run_on, vector, want
+from ._tensors import DTYPE_CODES, check, current_stream, invalid, run_on, vector, want
 
 
 @functools.lru_cache(maxsize=256)
@@ -75,7 +75,7 @@ def int8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale
     check(N.load().moe_quant_matmul(x.data_ptr(), code, x.stride(0), None if x_scale is None else x_scale.data_ptr(),
                                    w.data_ptr(), w.stride(0), w_scale.data_ptr(), out.data_ptr(),
                                    DTYPE_CODES[out_dtype], T, n, K, None if ws is None else ws.data_ptr(), need,
-                                   raw_stream(None, dev)), "moe_quant_matmul")
+                                   current_stream(dev)), "moe_quant_matmul")
     return out
 
 
@@ -127,10 +127,10 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
                                      down_scale.data_ptr())
     check(N.load().moe_quant_experts(cfg, ctypes.byref(w), x.data_ptr(), DTYPE_CODES[x.dtype], idx.data_ptr(),
                                     weights.data_ptr(), out.data_ptr(), T, ws.data_ptr(), need,
-                                    raw_stream(None, dev)), "moe_quant_experts")
+                                    current_stream(dev)), "moe_quant_experts")
     return out
 
 
 def int8_sync_status(stream: torch.cuda.Stream = None) -> int:
     """Waits for the stream; MOE_OK, or MOE_ERR_TIMEOUT if a product's bounded wait ran out since the last call."""
-    return N.load().moe_quant_sync_status(raw_stream(stream, torch.device("cuda", torch.cuda.current_device())))
+    return N.load().moe_quant_sync_status((stream or torch.cuda.current_stream()).cuda_stream)

@@ -9,7 +9,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import DTYPE_CODES, check, invalid, raw_stream, run_on, vector, want
+from ._tensors import DTYPE_CODES, check, current_stream, invalid, run_on, vector, want
 
 SCORES = {"softmax": N.MOE_SCORE_SOFTMAX, "sigmoid": N.MOE_SCORE_SIGMOID}
 
@@ -41,7 +41,7 @@ def _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise,
     check(N.load().moe_route_experts(_config(E, k, score, groups, top_groups, group_top, renormalise, scale),
                                      logits.data_ptr(), DTYPE_CODES[logits.dtype], logits.stride(0) if T > 1 else E,
                                      None if bias is None else bias.data_ptr(), T, idx.data_ptr(), weights.data_ptr(),
-                                     raw_stream(None, dev)), "moe_route_experts")
+                                     current_stream(dev)), "moe_route_experts")
     return idx, weights
 
 
@@ -105,5 +105,5 @@ def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, idx: t
     check(N.load().moe_route_experts_backward(_config(E, k, score, 1, 1, 1, renormalise, scale), logits.data_ptr(),
                                               DTYPE_CODES[logits.dtype], logits.stride(0) if T > 1 else E,
                                               idx.data_ptr(), d_weights.data_ptr(), T, d_logits.data_ptr(),
-                                              raw_stream(None, dev)), "moe_route_experts_backward")
+                                              current_stream(dev)), "moe_route_experts_backward")
     return d_logits
