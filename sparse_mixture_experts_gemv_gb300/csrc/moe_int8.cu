@@ -229,31 +229,35 @@ __global__ void __launch_bounds__(kThreads, 3) int8_experts_up_kernel(const Expe
   }
 }
 
-constexpr int kDownChannels = kWarps;   // channels of a CTA: one a warp
 constexpr int kMaxChoices = MOE_ROUTE_MAX_TOP_K;
 
-// out of one token (blockIdx.y) and kDownChannels channels, all its choices. Dynamic shared memory:
-// `held` quantized rows of h. The rows of the weights are known before h is: they are requested
-// into L2 while the kernel before is still at work. (Reading idx and the weights' addresses ahead of
-// the wait is sound: that kernel lets this one start only after its own wait, when all that the
-// caller had enqueued is done.)
-__global__ void __launch_bounds__(kThreads, 4) int8_experts_down_kernel(const ExpertsParams p, int held) {
+// out of one token (blockIdx.y) and CH channels a warp, all its choices. Dynamic shared memory: `held`
+// quantized rows of h; every CTA quantizes all of the token's, which more channels a warp keep from being
+// most of the work. The rows of the weights are known before h is: they are requested into L2 while the
+// kernel before is still at work. (Reading idx ahead of the wait is sound: that kernel lets this one start
+// only after its own wait, when all that the caller had enqueued is done.) The chunks of all the held
+// choices are one list: lane l takes chunks l, l + 32, ..., 8 / CH of them and CH channels at once, so that
+// eight loads are in flight and a chunk's place and token values serve CH channels.
+template <int CH>
+__global__ void __launch_bounds__(kThreads, 3) int8_experts_down_kernel(const ExpertsParams p, int held) {
   extern __shared__ uint4 q[];   // [held][I / 16]
   __shared__ float s_scale[kMaxChoices];
-  __shared__ int s_e[kMaxChoices];
+  __shared__ int s_e[kMaxChoices];   // -1: none
+  constexpr int kAtOnce = 8 / CH;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nch = p.I / 16;
-  const int c0 = blockIdx.x * kDownChannels;
+  const int c0 = blockIdx.x * kWarps * CH, ch0 = c0 + warp * CH;
   if (threadIdx.x < p.k) {
     const int e = __ldg(p.idx + (int64_t)blockIdx.y * p.k + threadIdx.x);
     if (e >= 0 && e < p.E)
-      prefetch_l2_bulk(p.down + ((int64_t)e * p.H + c0) * p.I, (uint32_t)(min(kDownChannels, p.H - c0) * p.I));
+      prefetch_l2_bulk(p.down + ((int64_t)e * p.H + c0) * p.I, (uint32_t)(min(kWarps * CH, p.H - c0) * p.I));
   }
   pdl_wait();
   pdl_launch_dependents();
-  const int ch = c0 + warp;
   for (int64_t t = blockIdx.y; t < p.T; t += gridDim.y) {
-    float sum = 0.f;
+    float sum[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) sum[i] = 0.f;
     for (int j0 = 0; j0 < p.k; j0 += held) {
       const int nj = min(held, p.k - j0);
       __syncthreads();
@@ -291,30 +295,46 @@ __global__ void __launch_bounds__(kThreads, 4) int8_experts_down_kernel(const Ex
         if (lane == 0) s_e[j] = e;
       }
       __syncthreads();
-      if (ch < p.H) {
-        float ws = 0.f;   // lane j: the scales of choice j
-        if (lane < nj && s_e[lane] >= 0) ws = s_scale[lane] * __ldg(p.down_scale + (int64_t)s_e[lane] * p.H + ch);
-        for (int cb = 0; cb < nch; cb += 32) {
-          const int c = cb + lane;
-          for (int jb = 0; jb < nj; jb += 8) {
-            uint4 w[8];   // eight choices' rows at once: all loads before the first product
+      if (ch0 < p.H) {
+        float ws[CH];   // lane j: the scales of choice j
+        const int my_e = lane < nj ? s_e[lane] : -1;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              w[i] = make_uint4(0, 0, 0, 0);
-              const int e = jb + i < nj ? s_e[jb + i] : -1;
-              if (e >= 0 && c < nch) w[i] = ldg_stream(p.down + ((int64_t)e * p.H + ch) * p.I + 16 * c);
-            }
+        for (int i = 0; i < CH; ++i)
+          ws[i] = my_e >= 0 && ch0 + i < p.H ? s_scale[lane] * __ldg(p.down_scale + (int64_t)my_e * p.H + ch0 + i) : 0.f;
+        int j = 0, c = lane;   // the lane's chunk: c of choice j
+        while (c >= nch) { c -= nch; ++j; }
+        for (int at = 0; at < nj * nch; at += 32 * kAtOnce) {
+          uint4 w[kAtOnce][CH];
+          int from[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float f = __shfl_sync(0xFFFFFFFFu, ws, jb + i);
-              if (jb + i < nj && s_e[jb + i] >= 0 && c < nch) sum += (float)dot16(w[i], q[(jb + i) * nch + c], 0) * f;
+          for (int u = 0; u < kAtOnce; ++u) {
+            const int e = j < nj ? s_e[j] : -1;
+            const int8_t* row = p.down + ((int64_t)max(e, 0) * p.H + ch0) * p.I + 16 * c;
+            from[u] = e >= 0 ? j : -1;
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              w[u][i] = e >= 0 && ch0 + i < p.H ? ldg_stream(row + (int64_t)i * p.I) : make_uint4(0, 0, 0, 0);
+            c += 32;
+            while (c >= nch) { c -= nch; ++j; }
+          }
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u) {
+            const int chunk = at + 32 * u + lane;
+            const uint4 xv = from[u] >= 0 ? q[chunk] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const float f = __shfl_sync(0xFFFFFFFFu, ws[i], from[u] & 31);
+              if (from[u] >= 0) sum[i] += (float)dot16(w[u][i], xv, 0) * f;
             }
           }
         }
       }
     }
-    sum = warp_sum(sum);
-    if (lane == 0 && ch < p.H) store(p.out, p.out_dtype, t * p.H + ch, sum);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const float f = warp_sum(sum[i]);
+      if (lane == i && ch0 + i < p.H) store(p.out, p.out_dtype, t * p.H + ch0 + i, f);
+    }
   }
 }
 
@@ -348,11 +368,15 @@ MOE_DEV void quantize16_f16(const void* x, int64_t i, const RowScale s, uint4& l
       o[2 * c + 1] = int_pair_f16((int8_t)(w[c] >> 16), (int8_t)(w[c] >> 24));
     }
   } else {
-    float v[16];
+    float v[16], q[16];
     if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(x) + i, v);
     else load16<DT>(x, i, v);
+    quantize16(v, s, q);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) o[c] = int_pair_f16(quantize(v[2 * c], s), quantize(v[2 * c + 1], s));
+    for (int c = 0; c < 8; ++c) {
+      const __half2 h = __floats2half2_rn(q[2 * c], q[2 * c + 1]);
+      o[c] = *reinterpret_cast<const uint32_t*>(&h);
+    }
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
@@ -591,7 +615,7 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int block, size_t smem, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-cudaError_t launch_experts_stream(const ExpertsParams& p, int x_dtype, cudaStream_t s) {
+cudaError_t launch_experts_stream(const ExpertsParams& p, int x_dtype, int num_sms, cudaStream_t s) {
   const int64_t choices = (int64_t)p.T * p.k;
   const dim3 up((p.I + kFeatures - 1) / kFeatures, (unsigned)(choices < 65535 ? choices : 65535));
   cudaError_t e = x_dtype == MOE_DTYPE_BF16
@@ -600,8 +624,16 @@ cudaError_t launch_experts_stream(const ExpertsParams& p, int x_dtype, cudaStrea
   if (e != cudaSuccess) return e;
   int held = 32 * 1024 / p.I;   // rows of h a CTA keeps: 32 KB, so that several CTAs share an SM
   held = held < 1 ? 1 : held < p.k ? held : p.k;
-  const dim3 down((p.H + kDownChannels - 1) / kDownChannels, (unsigned)(p.T < 65535 ? p.T : 65535));
-  return launch_pdl(int8_experts_down_kernel, down, kThreads, (size_t)held * p.I, s, p, held);
+  // as many channels a warp as leave two CTAs an SM
+  const int64_t want = (int64_t)p.T * p.H / (2 * kWarps * num_sms);
+  const auto down = [&](int ch) {
+    return dim3((p.H + kWarps * ch - 1) / (kWarps * ch), (unsigned)(p.T < 65535 ? p.T : 65535));
+  };
+  const size_t smem = (size_t)held * p.I;
+  if (want < 2) return launch_pdl(int8_experts_down_kernel<1>, down(1), kThreads, smem, s, p, held);
+  if (want < 4) return launch_pdl(int8_experts_down_kernel<2>, down(2), kThreads, smem, s, p, held);
+  if (want < 8) return launch_pdl(int8_experts_down_kernel<4>, down(4), kThreads, smem, s, p, held);
+  return launch_pdl(int8_experts_down_kernel<8>, down(8), kThreads, smem, s, p, held);
 }
 
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
@@ -905,7 +937,7 @@ moe_status_t moe_quant_experts(const moe_int8_experts_config_t* c, const moe_int
   p.I = c->intermediate;
   p.out_dtype = x_dtype;
   const cudaError_t e = T <= kStreamTokens
-                            ? launch_experts_stream(p, x_dtype, (cudaStream_t)stream)
+                            ? launch_experts_stream(p, x_dtype, device_sms(), (cudaStream_t)stream)
                             : launch_experts_tensor(p, c, x_dtype, (uint8_t*)workspace_dev, device_sms(),
                                                     (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : moe::record_cuda_failure(e, "moe_quant_experts");

@@ -79,33 +79,48 @@ MOE_DEV RowScale row_scale(uint32_t bits) {
 
 // x / scale to the nearest whole number, halves to the even one, decided on the real
 // quotient: a row's half of the largest value is a tie but for the scale's rounding.
-// The product with the reciprocal is off by less than 1e-4, so its rounding is at
-// most one off, which the exact remainder x - q * scale tells (one rounding, far
-// below what it is compared with).
-MOE_DEV int quantize(float x, const RowScale r) {
-  float q;
+// The product with the reciprocal is off by less than 1e-5, and adding 3 * 2^22 rounds it
+// to a whole number: at most one off, and only where the exact remainder x - q * scale
+// (one rounding, far below what it is compared with) reaches half a scale. That is rare,
+// so that the values of a chunk are looked at together.
+constexpr float kRound = 12582912.f;
+MOE_DEV void quantize16(const float (&v)[16], const RowScale r, float (&q)[16]) {
   if (r.inv != 0.f) {
-    q = rintf(x * r.inv);
-    const float d = fmaf(-q, r.scale, x), half = 0.5f * r.scale;
-    const bool odd = (int)q & 1;
-    if (d > half || (d == half && odd)) q += 1.f;
-    else if (d < -half || (d == -half && odd)) q -= 1.f;
+    const float half = 0.5f * r.scale;
+    float worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      q[i] = fmaf(v[i], r.inv, kRound) - kRound;
+      worst = fmaxf(worst, fabsf(fmaf(-q[i], r.scale, v[i])));
+    }
+    if (worst >= half) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float d = fmaf(-q[i], r.scale, v[i]);
+        const bool odd = (int)q[i] & 1;
+        if (d > half || (d == half && odd)) q[i] += 1.f;
+        else if (d < -half || (d == -half && odd)) q[i] -= 1.f;
+      }
+    }
   } else {
-    q = r.scale > 0.f ? rintf(x / r.scale) : 0.f;   // 0 for a scale that underflowed, and for NaN
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {   // 0 for a scale that underflowed, and for NaN
+      const float t = r.scale > 0.f ? rintf(v[i] / r.scale) : 0.f;
+      q[i] = fminf(fmaxf(t, -127.f), 127.f);
+    }
   }
-  return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
-MOE_DEV uint32_t pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 0xFF) | ((uint32_t)(b & 0xFF) << 8) | ((uint32_t)(c & 0xFF) << 16) | ((uint32_t)d << 24);
+// The low byte of q + 3 * 2^22 is q's.
+MOE_DEV uint32_t pack4(const float* q) {
+  const uint32_t a = __float_as_uint(q[0] + kRound), b = __float_as_uint(q[1] + kRound),
+                 c = __float_as_uint(q[2] + kRound), d = __float_as_uint(q[3] + kRound);
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 MOE_DEV uint4 quantize16(const float (&v)[16], const RowScale r) {
-  uint4 o;
-  o.x = pack4(quantize(v[0], r), quantize(v[1], r), quantize(v[2], r), quantize(v[3], r));
-  o.y = pack4(quantize(v[4], r), quantize(v[5], r), quantize(v[6], r), quantize(v[7], r));
-  o.z = pack4(quantize(v[8], r), quantize(v[9], r), quantize(v[10], r), quantize(v[11], r));
-  o.w = pack4(quantize(v[12], r), quantize(v[13], r), quantize(v[14], r), quantize(v[15], r));
-  return o;
+  float q[16];
+  quantize16(v, r, q);
+  return make_uint4(pack4(q), pack4(q + 4), pack4(q + 8), pack4(q + 12));
 }
 
 MOE_DEV int dot16(const uint4 w, const uint4 x, int acc) {
