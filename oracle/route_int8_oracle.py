@@ -91,7 +91,8 @@ def quantize(x):
     """(q, scale as held in fp32, distance of each quotient from the nearest half) of the rows of x."""
     x = np.asarray(x, dtype=np.float64)
     amax = np.abs(x).max(axis=-1, keepdims=True)
-    scale = np.where(amax > 0, (amax / 127).astype(np.float32).astype(np.float64), 1.0)
+    inv = np.float64(np.float32(1) / np.float32(127))   # both the constant and the product rounded to fp32
+    scale = np.where(amax > 0, (amax * inv).astype(np.float32).astype(np.float64), 1.0)
     r = np.divide(x, scale, out=np.zeros_like(x), where=scale > 0)
     q = np.clip(np.rint(r), -127, 127)
     return q, scale[..., 0], np.abs(np.abs(r - np.floor(r)) - 0.5)

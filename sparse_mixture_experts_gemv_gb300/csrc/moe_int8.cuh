@@ -72,7 +72,7 @@ MOE_DEV RowScale row_scale(uint32_t bits) {
   RowScale r;
   const float amax = __uint_as_float(bits);
   if (bits >= 0x7F800000u) r.scale = __uint_as_float(0x7FC00000u);   // NaN: the whole row
-  else r.scale = bits ? amax / 127.f : 1.f;
+  else r.scale = bits ? amax * (1.f / 127.f) : 1.f;   // the constant rounded to fp32, then the product
   r.inv = r.scale >= 0x1p-100f ? 1.f / r.scale : 0.f;   // 0: divide (also for NaN)
   return r;
 }
