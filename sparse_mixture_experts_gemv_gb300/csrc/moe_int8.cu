@@ -350,49 +350,113 @@ struct PrepareParams {
   float* scale;           // [rows]
 };
 
-MOE_DEV uint32_t int_pair_f16(int a, int b) {
-  const __half2 h = __halves2half2(__int2half_rn(a), __int2half_rn(b));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 16 elements of a row as whole numbers in f16.
+// A row as a warp reads and writes it: pieces of 4 fp32, else 8 elements a lane, consecutive lanes
+// next to each other in both, so that every access of the warp is one contiguous run.
 template <int DT>
-MOE_DEV void quantize16_f16(const void* x, int64_t i, const RowScale s, uint4& lo, uint4& hi) {
-  uint32_t o[8];
-  if constexpr (DT == MOE_DTYPE_S8) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(x) + i));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      o[2 * c] = int_pair_f16((int8_t)w[c], (int8_t)(w[c] >> 8));
-      o[2 * c + 1] = int_pair_f16((int8_t)(w[c] >> 16), (int8_t)(w[c] >> 24));
+struct Piece {
+  static constexpr int kN = DT == MOE_DTYPE_F32 ? 4 : 8;
+  uint32_t w[DT == MOE_DTYPE_S8 ? 2 : 4];
+  // elements i ... of x; fp32 was written earlier in this call
+  MOE_DEV void load(const void* x, int64_t i) {
+    if constexpr (DT == MOE_DTYPE_S8) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(x) + i));
+      w[0] = u.x; w[1] = u.y;
+    } else {
+      const uint4 u = DT == MOE_DTYPE_F32 ? ldg_cg(static_cast<const float*>(x) + i)
+                                          : __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i));
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
     }
-  } else {
-    float v[16], q[16];
-    if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(x) + i, v);
-    else load16<DT>(x, i, v);
-    quantize16(v, s, q);
+  }
+  MOE_DEV void values(float (&v)[kN]) const {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < (int)(sizeof(w) / 4); ++c) {
+      if constexpr (DT == MOE_DTYPE_F32) {
+        v[c] = __uint_as_float(w[c]);
+      } else if constexpr (DT == MOE_DTYPE_BF16) {
+        v[2 * c] = bf16_lo(w[c]);
+        v[2 * c + 1] = bf16_hi(w[c]);
+      } else if constexpr (DT == MOE_DTYPE_F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[c]));
+        v[2 * c] = f.x;
+        v[2 * c + 1] = f.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * c + i] = (float)(int8_t)(w[c] >> (8 * i));
+      }
+    }
+  }
+  // whole numbers as f16 pairs: kN / 2 words
+  MOE_DEV void quantized(const RowScale s, uint32_t (&o)[kN / 2]) const {
+    float v[kN], q[kN];
+    values(v);
+    if constexpr (DT == MOE_DTYPE_S8) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) q[i] = v[i];
+    } else {
+      quantize(v, s, q);
+    }
+#pragma unroll
+    for (int c = 0; c < kN / 2; ++c) {
       const __half2 h = __floats2half2_rn(q[2 * c], q[2 * c + 1]);
       o[c] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+};
+template <int W>
+MOE_DEV void store_words(void* p, const uint32_t (&o)[W]) {
+  if constexpr (W == 2) *static_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+  else *static_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The scale of a row, found by one warp.
-template <int DT>
-MOE_DEV RowScale warp_row_scale(const void* x, int64_t row0, int nch, int lane) {
-  float v[16];
+// The row of K elements at x + i, quantized by one warp and handed out piece by piece: put(element
+// index, words) is called by whole warps, a lane past K64 with an index of -1. The first kKept pieces
+// a lane stay in registers between the search for the largest value and the quantization.
+template <int DT, class Put>
+MOE_DEV float quantize_row(const void* x, int64_t i, int K, int K64, int lane, Put put) {
+  constexpr int kN = Piece<DT>::kN, kKept = 8;
+  Piece<DT> kept[kKept];
+  RowScale s = {};
   uint32_t m = 0;
-  for (int c = lane; c < nch; c += 32) {
-    if (DT == MOE_DTYPE_F32) load16_cg(static_cast<const float*>(x) + row0 + 16 * c, v);
-    else load16<DT>(x, row0 + 16 * c, v);
-    m = max(m, amax_bits(v));
+#pragma unroll
+  for (int c = 0; c < kKept; ++c) {
+    const int at = (32 * c + lane) * kN;
+    if (at < K) kept[c].load(x, i + at);
   }
-  return row_scale(__reduce_max_sync(0xFFFFFFFFu, m));
+  if constexpr (DT != MOE_DTYPE_S8) {
+#pragma unroll
+    for (int c = 0; c < kKept; ++c)
+      if ((32 * c + lane) * kN < K) {
+        float v[kN];
+        kept[c].values(v);
+        m = max(m, amax_bits(v));
+      }
+    for (int at = (32 * kKept + lane) * kN; at < K; at += 32 * kN) {
+      Piece<DT> piece;
+      float v[kN];
+      piece.load(x, i + at);
+      piece.values(v);
+      m = max(m, amax_bits(v));
+    }
+    s = row_scale(__reduce_max_sync(0xFFFFFFFFu, m));
+  }
+#pragma unroll
+  for (int c = 0; c < kKept; ++c) {
+    const int at = (32 * c + lane) * kN;
+    uint32_t o[kN / 2] = {};
+    if (at < K) kept[c].quantized(s, o);
+    if (32 * c * kN < K64) put(at < K64 ? at : -1, o);
+  }
+  for (int base = 32 * kKept * kN; base < K64; base += 32 * kN) {
+    const int at = base + lane * kN;
+    uint32_t o[kN / 2] = {};
+    if (at < K) {
+      Piece<DT> piece;
+      piece.load(x, i + at);
+      piece.quantized(s, o);
+    }
+    put(at < K64 ? at : -1, o);
+  }
+  return s.scale;
 }
 
 constexpr int kPrepareThreads = 256;
@@ -402,20 +466,15 @@ template <int DT>
 __global__ void __launch_bounds__(kPrepareThreads) int8_prepare_kernel(const PrepareParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, nch = p.K / 16;
+  const int lane = threadIdx.x & 31;
   const int rows = p.num_rows ? min(p.rows, ldg_cg_s32(p.num_rows)) : p.rows;
   constexpr int kW = kPrepareThreads / 32;
   for (int64_t r = (int64_t)blockIdx.x * kW + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * kW) {
-    uint4* q = reinterpret_cast<uint4*>(p.q + r * p.K64);
-    RowScale s = {};
-    if constexpr (DT != MOE_DTYPE_S8) s = warp_row_scale<DT>(p.x, r * p.stride, nch, lane);
-    for (int c = lane; c < p.K64 / 16; c += 32) {
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      if (c < nch) quantize16_f16<DT>(p.x, r * p.stride + 16 * c, s, lo, hi);
-      q[2 * c] = lo;
-      q[2 * c + 1] = hi;
-    }
-    if (lane == 0) p.scale[r] = DT == MOE_DTYPE_S8 ? p.x_scale[r] : s.scale;
+    __half* q = p.q + r * p.K64;
+    const float scale = quantize_row<DT>(p.x, r * p.stride, p.K, p.K64, lane, [&](int at, const auto& o) {
+      if (at >= 0) store_words(q + at, o);
+    });
+    if (lane == 0) p.scale[r] = DT == MOE_DTYPE_S8 ? p.x_scale[r] : scale;
   }
 }
 
@@ -461,7 +520,7 @@ __global__ void __launch_bounds__(kGroupThreads) int8_count_kernel(const GroupPa
 // chunk the order is the shared-memory atomics': every row is computed by itself, so no
 // result depends on it.
 template <int DT>
-__global__ void __launch_bounds__(kGroupThreads) int8_group_kernel(const GroupParams p) {
+__global__ void __launch_bounds__(kGroupThreads, 1) int8_group_kernel(const GroupParams p) {
   static_assert(kGroupThreads >= MOE_INT8_MAX_EXPERTS, "one thread an expert");
   __shared__ int cursor[MOE_INT8_MAX_EXPERTS], all[MOE_INT8_MAX_EXPERTS], before[MOE_INT8_MAX_EXPERTS], sums[2][32];
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
@@ -515,7 +574,6 @@ __global__ void __launch_bounds__(kGroupThreads) int8_group_kernel(const GroupPa
     if (i == kGroupThreads - 1) { p.counts[0] = blocks; p.counts[1] = rows; }
   }
   __syncthreads();
-  const int nch = p.H / 16;
   const int t1 = min(p.T, ((int)blockIdx.x + 1) * p.chunk);
   for (int t = blockIdx.x * p.chunk + warp; t < t1; t += kGroupThreads / 32) {
     int at = -1;
@@ -524,21 +582,13 @@ __global__ void __launch_bounds__(kGroupThreads) int8_group_kernel(const GroupPa
       if (e >= 0 && e < p.E) at = atomicAdd(&cursor[e], 1);
       p.pos[(int64_t)t * p.k + lane] = at;
     }
-    const RowScale s = warp_row_scale<DT>(p.x, (int64_t)t * p.H, nch, lane);
-    if (at >= 0) p.scale[at] = s.scale;
-    for (int c0 = 0; c0 < p.H64 / 16; c0 += 32) {
-      const int ch = c0 + lane;
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      if (ch < nch) quantize16_f16<DT>(p.x, (int64_t)t * p.H + 16 * ch, s, lo, hi);
+    const float scale = quantize_row<DT>(p.x, (int64_t)t * p.H, p.H, p.H64, lane, [&](int i, const auto& o) {
       for (int j = 0; j < p.k; ++j) {
         const int to = __shfl_sync(0xFFFFFFFFu, at, j);
-        if (to >= 0 && ch < p.H64 / 16) {
-          uint4* q = reinterpret_cast<uint4*>(p.q + (int64_t)to * p.H64) + 2 * ch;
-          q[0] = lo;
-          q[1] = hi;
-        }
+        if (to >= 0 && i >= 0) store_words(p.q + (int64_t)to * p.H64 + i, o);
       }
-    }
+    });
+    if (at >= 0) p.scale[at] = scale;
   }
 }
 

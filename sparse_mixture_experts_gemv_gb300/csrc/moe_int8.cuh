@@ -55,10 +55,11 @@ MOE_DEV void load16_cg(const float* p, float (&v)[16]) {
 
 // max of the bit patterns of |v|: an infinity or a NaN stays above every finite
 // value, so that a row's largest pattern also says whether the row is finite.
-MOE_DEV uint32_t amax_bits(const float (&v)[16]) {
+template <int N>
+MOE_DEV uint32_t amax_bits(const float (&v)[N]) {
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < N; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   return a;
 }
 
@@ -84,18 +85,19 @@ MOE_DEV RowScale row_scale(uint32_t bits) {
 // (one rounding, far below what it is compared with) reaches half a scale. That is rare,
 // so that the values of a chunk are looked at together.
 constexpr float kRound = 12582912.f;
-MOE_DEV void quantize16(const float (&v)[16], const RowScale r, float (&q)[16]) {
+template <int N>
+MOE_DEV void quantize(const float (&v)[N], const RowScale r, float (&q)[N]) {
   if (r.inv != 0.f) {
     const float half = 0.5f * r.scale;
     float worst = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < N; ++i) {
       q[i] = fmaf(v[i], r.inv, kRound) - kRound;
       worst = fmaxf(worst, fabsf(fmaf(-q[i], r.scale, v[i])));
     }
     if (worst >= half) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < N; ++i) {
         const float d = fmaf(-q[i], r.scale, v[i]);
         const bool odd = (int)q[i] & 1;
         if (d > half || (d == half && odd)) q[i] += 1.f;
@@ -104,7 +106,7 @@ MOE_DEV void quantize16(const float (&v)[16], const RowScale r, float (&q)[16]) 
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {   // 0 for a scale that underflowed, and for NaN
+    for (int i = 0; i < N; ++i) {   // 0 for a scale that underflowed, and for NaN
       const float t = r.scale > 0.f ? rintf(v[i] / r.scale) : 0.f;
       q[i] = fminf(fmaxf(t, -127.f), 127.f);
     }
@@ -119,7 +121,7 @@ MOE_DEV uint32_t pack4(const float* q) {
 }
 MOE_DEV uint4 quantize16(const float (&v)[16], const RowScale r) {
   float q[16];
-  quantize16(v, r, q);
+  quantize(v, r, q);
   return make_uint4(pack4(q), pack4(q + 4), pack4(q + 8), pack4(q + 12));
 }
 

@@ -107,24 +107,25 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
     E, I = gate_up.shape[0], gate_up.shape[1] // 2
     if down.shape != (E, H, I) or down.dtype is not torch.int8:
         invalid(what, f"down must be int8 [{E}, {H}, {I}]")
-    for name, t, shape in (("gate_up_scale", gate_up_scale, (E, 2 * I)), ("down_scale", down_scale, (E, H))):
-        if t.shape != shape or t.dtype is not torch.float32:
-            invalid(what, f"{name} must be fp32 {list(shape)}")
-    for name, t in (("gate_up", gate_up), ("gate_up_scale", gate_up_scale), ("down", down), ("down_scale", down_scale)):
-        if t.device != dev or not t.is_contiguous():
-            invalid(what, f"{name} must be on {dev} and without gaps")
-        if t.data_ptr() % 16:
-            invalid(what, f"{name} must start on a 16-byte boundary")
+    if gate_up_scale.shape != (E, 2 * I) or gate_up_scale.dtype is not torch.float32:
+        invalid(what, f"gate_up_scale must be fp32 [{E}, {2 * I}]")
+    if down_scale.shape != (E, H) or down_scale.dtype is not torch.float32:
+        invalid(what, f"down_scale must be fp32 [{E}, {H}]")
+    w = N.moe_int8_experts_weights_t(gate_up.data_ptr(), gate_up_scale.data_ptr(), down.data_ptr(),
+                                     down_scale.data_ptr())
+    if (w.gate_up_dev | w.gate_up_scale_dev | w.down_dev | w.down_scale_dev) & 15 or not (
+            gate_up.is_contiguous() and gate_up_scale.is_contiguous() and down.is_contiguous() and
+            down_scale.is_contiguous()) or not (
+            gate_up.device == gate_up_scale.device == down.device == down_scale.device == dev):
+        invalid(what, f"the weights and their scales must be on {dev}, without gaps and on 16-byte boundaries")
     x, idx, weights = x.contiguous(), idx.contiguous(), weights.contiguous()
-    if x.data_ptr() % 16:
+    if x.data_ptr() & 15:
         x = x.clone()
     out = torch.empty((T, H), dtype=x.dtype, device=dev)
     if T == 0:
         return out
     cfg, need = _experts_config(E, k, H, I, T)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    w = N.moe_int8_experts_weights_t(gate_up.data_ptr(), gate_up_scale.data_ptr(), down.data_ptr(),
-                                     down_scale.data_ptr())
     check(N.load().moe_quant_experts(cfg, ctypes.byref(w), x.data_ptr(), DTYPE_CODES[x.dtype], idx.data_ptr(),
                                     weights.data_ptr(), out.data_ptr(), T, ws.data_ptr(), need,
                                     current_stream(dev)), "moe_quant_experts")

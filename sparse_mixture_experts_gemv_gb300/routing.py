@@ -35,7 +35,7 @@ def _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise,
     T, E = logits.shape
     dev = logits.device
     if bias is not None:
-        bias = vector(bias.detach(), "bias", E, "route_experts", dev)
+        bias = vector(bias, "bias", E, "route_experts", dev)
     idx = torch.empty((T, k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
     check(N.load().moe_route_experts(_config(E, k, score, groups, top_groups, group_top, renormalise, scale),
