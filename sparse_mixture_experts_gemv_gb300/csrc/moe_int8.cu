@@ -593,12 +593,12 @@ __global__ void __launch_bounds__(kGroupThreads, 1) int8_group_kernel(const Grou
 }
 
 struct CombineParams {
-  const __half* y;           // [rows][H]: integer sums times 1 / factor
+  const __half* y;           // [rows][H]: integer sums times down scale / (factor * norm)
   const float* h_scale;      // [rows]
   const int* idx;
   const int* pos;            // grouped row of each choice, -1: none
   const float* weights;
-  const float* down_scale;   // [E][H]
+  const float* norms;        // [E]
   void* out;
   int T, k, H, out_dtype;
   float factor;
@@ -606,10 +606,10 @@ struct CombineParams {
 
 constexpr int kCombineThreads = 256;
 
-// out[t] = sum_j weights[t, j] h_scale y_j down_scale[e_j], eight channels a thread.
+// out[t] = sum_j weights[t, j] h_scale factor norm[e_j] y_j, eight channels a thread.
 __global__ void __launch_bounds__(kCombineThreads) int8_combine_kernel(const CombineParams p) {
   __shared__ float s_f[MOE_ROUTE_MAX_TOP_K];
-  __shared__ int s_e[MOE_ROUTE_MAX_TOP_K], s_pos[MOE_ROUTE_MAX_TOP_K];
+  __shared__ int s_pos[MOE_ROUTE_MAX_TOP_K];
   pdl_wait();
   pdl_launch_dependents();
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
@@ -618,27 +618,24 @@ __global__ void __launch_bounds__(kCombineThreads) int8_combine_kernel(const Com
       const int64_t a = t * p.k + threadIdx.x;
       const int at = ldg_cg_s32(p.pos + a);
       s_pos[threadIdx.x] = at;
-      s_e[threadIdx.x] = __ldg(p.idx + a);
-      s_f[threadIdx.x] = at >= 0 ? __ldg(p.weights + a) * (ldg_cg_f32(p.h_scale + at) * p.factor) : 0.f;
+      s_f[threadIdx.x] = at >= 0 ? __ldg(p.weights + a) * ldg_cg_f32(p.h_scale + at) *
+                                       (p.factor * ldg_cg_f32(p.norms + __ldg(p.idx + a))) : 0.f;
     }
     __syncthreads();
     for (int c = threadIdx.x * 8; c < p.H; c += kCombineThreads * 8) {
       float acc[8] = {};
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < p.k; ++j) {
         const int at = s_pos[j];
         if (at < 0) continue;
         const float f = s_f[j];
         const uint4 y = ldg_cg(p.y + (int64_t)at * p.H + c);
-        const float4* ws = reinterpret_cast<const float4*>(p.down_scale + (int64_t)s_e[j] * p.H + c);
-        const float4 w0 = __ldg(ws), w1 = __ldg(ws + 1);
         const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&yw[i]));
-          acc[2 * i] += f * w[2 * i] * v.x;
-          acc[2 * i + 1] += f * w[2 * i + 1] * v.y;
+          acc[2 * i] += f * v.x;
+          acc[2 * i + 1] += f * v.y;
         }
       }
       uint32_t o[4];
@@ -754,7 +751,7 @@ cudaError_t launch_matmul_tensor(const StreamParams& p, int x_dtype, uint8_t* ws
 
 // Scratch of the experts' call. y takes h's place, which is dead by then.
 struct ExpertsWorkspace {
-  int64_t h, q, x_scale, hq, h_scale, chunk_counts, pos, blocks, counts, bytes;
+  int64_t h, q, x_scale, hq, h_scale, norms, chunk_counts, pos, blocks, counts, bytes;
   int block, max_blocks, chunk, chunks;
 };
 ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T) {
@@ -779,6 +776,7 @@ ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T
   w.x_scale = take(rows * 4);
   w.hq = take(rows * pad64(I) * 2);
   w.h_scale = take(rows * 4);
+  w.norms = take((int64_t)c->num_experts * 4);
   w.chunk_counts = take((int64_t)w.chunks * c->num_experts * 4);
   w.pos = take(rows * 4);
   w.blocks = take((int64_t)w.max_blocks * 16);
@@ -832,6 +830,10 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   g.row_scale = a.scale;
   g.w_scale = p.gate_up_scale;
   g.out = ws + w.h;
+  g.norm_scales = p.down_scale;
+  g.norms = (float*)(ws + w.norms);
+  g.num_norms = p.E;
+  g.norm_row = p.H;
   e = launch_gemm(kUp, g, num_sms, s);
   if (e != cudaSuccess) return e;
 
@@ -847,9 +849,11 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   e = launch_prepare(b, MOE_DTYPE_F32, num_sms, s);
   if (e != cudaSuccess) return e;
 
-  // the down sums (at most 127 * 128 * I) fit f16 once divided by a power of two, and whole numbers
-  // times it are never below f16's normal range: the rounding to 11 bits is relative, and far below
-  // that of the output
+  // The down sums (at most 127 * 128 * I) fit f16 once divided by a power of two, and still do after their
+  // channel's scale over the expert's norm. The rounding to 11 bits is relative and far below that
+  // of a bf16 output, unless a channel's scale is some 2^-16 of its expert's largest: such a channel's
+  // values lose bits, which it adds next to nothing with. (Held as they are, and scaled in the weighted
+  // sum, each value took its 4-byte scale along there: 42 us of a call at T = 4096, Qwen-shaped.)
   float factor = 1.f;
   while (127.f * 128.f * (float)p.I > 65504.f * factor) factor *= 2.f;
   g.a = p.down;
@@ -861,7 +865,7 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   g.K = p.I;
   g.channels = p.H;
   g.rows_per_group = p.H;
-  g.w_scale = nullptr;
+  g.w_scale = p.down_scale;
   g.out = ws + w.h;
   g.factor = 1.f / factor;
   e = launch_gemm(kDown, g, num_sms, s);
@@ -873,7 +877,7 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   c.idx = p.idx;
   c.pos = a.pos;
   c.weights = p.weights;
-  c.down_scale = p.down_scale;
+  c.norms = g.norms;
   c.out = p.out;
   c.T = p.T;
   c.k = p.k;

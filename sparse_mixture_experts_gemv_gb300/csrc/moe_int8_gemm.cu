@@ -18,7 +18,7 @@
 //
 // One persistent CTA an SM, warp-specialised:
 //   warp 0        weights by TMA              warp 2  tokens by TMA
-//   warp 1        issues the MMAs             warp 3  idle
+//   warp 1        issues the MMAs             warp 3  up: the experts' largest down scales
 //   warps 4-11    converters: two groups of four, each half of a step's K
 //   warps 12-15   epilogue of the previous tile while the next one accumulates
 // A step is 128 of K: eight MMAs. What the issuing warp does between two steps (a wait,
@@ -70,6 +70,9 @@ struct Params {
   void* out;
   int out_dtype;
   int wide;                  // dense: 16-bit results whose rows are 16-byte aligned
+  const float* norm_scales;
+  float* norms;
+  int num_norms, norm_row;
   float factor;
 };
 
@@ -387,6 +390,17 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
         if (++es == p.b_stages) { es = 0; eph ^= 1; }
       }
     }
+  } else if (KIND == kUp && warp == 3) {
+    // ------------------------------------------- the experts' largest down scales
+    for (int e = blockIdx.x; e < p.num_norms; e += gridDim.x) {
+      uint32_t m = 0;
+      for (int i = lane; i < p.norm_row; i += 32)
+        m = max(m, __float_as_uint(__ldg(p.norm_scales + (int64_t)e * p.norm_row + i)) & 0x7FFFFFFFu);
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      // the next power of two; 1 where there is none in fp32's normal range
+      const uint32_t exponent = (m >> 23) + 1;
+      if (lane == 0) p.norms[e] = m >= 0x00800000u && exponent < 0xFE ? __uint_as_float(exponent << 23) : 1.f;
+    }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3;
@@ -405,6 +419,8 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       const bool in = ch < p.channels;
       float w0 = 0.f, w1 = 0.f;
       if (in && KIND == kDense) w0 = __ldg(p.w_scale + ch);
+      if (in && KIND == kDown)
+        w0 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + ch) * (p.factor / ldg_cg_f32(p.norms + t.e));
       if (in && KIND == kUp) {
         w0 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + ch);
         w1 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + p.channels + ch);
@@ -440,7 +456,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
             float f[4];
             if (KIND == kDown) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(v[i + j]) * p.factor;
+              for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(v[i + j]) * w0;
             } else {
               const float4 xs = *reinterpret_cast<const float4*>(cs + c0 + i);
               f[0] = __uint_as_float(v[i]) * xs.x * w0;
@@ -584,6 +600,10 @@ cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStrea
   p.out = a.out;
   p.out_dtype = a.out_dtype;
   p.wide = a.out_dtype != MOE_DTYPE_F32 && a.channels % 8 == 0 && !((uintptr_t)a.out & 15);
+  p.norm_scales = a.norm_scales;
+  p.norms = a.norms;
+  p.num_norms = a.num_norms;
+  p.norm_row = a.norm_row;
   p.factor = a.factor;
   const size_t smem = (size_t)p.b_stages * p.b_bytes + (size_t)p.raw_stages * kRawBytes + kFixedSmem;
   const int64_t tiles = (int64_t)p.tiles_m * (kind == kDense ? p.tiles_t : a.max_blocks);

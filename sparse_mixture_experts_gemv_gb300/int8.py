@@ -105,6 +105,8 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
     if gate_up.dim() != 3 or gate_up.shape[2] != H or gate_up.shape[1] % 2 or gate_up.dtype is not torch.int8:
         invalid(what, f"gate_up must be int8 [E, 2I, {H}]")
     E, I = gate_up.shape[0], gate_up.shape[1] // 2
+    if E == 0 or I == 0:
+        invalid(what, "there must be an expert and an intermediate feature")
     if down.shape != (E, H, I) or down.dtype is not torch.int8:
         invalid(what, f"down must be int8 [{E}, {H}, {I}]")
     if gate_up_scale.shape != (E, 2 * I) or gate_up_scale.dtype is not torch.float32:
