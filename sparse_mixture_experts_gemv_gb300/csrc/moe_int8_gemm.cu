@@ -437,16 +437,21 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
           // lower lanes take the even columns, upper lanes the odd ones: each sends its partner the
           // other column's half of the pair
           float* dst = static_cast<float*>(p.out) + ((int64_t)t.row0 + c0 + (lane >> 4)) * p.channels + ch;
+          const bool upper = lane >= 16;
+          const float* xs = cs + c0 + (lane >> 4);
+          float h[16];   // all of them before the first store: nothing of it waits for a branch
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const bool upper = lane >= 16;
             const float keep = __uint_as_float(upper ? v[2 * i + 1] : v[2 * i]);
             const float got = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[2 * i] : v[2 * i + 1]), 16);
-            const int c = 2 * i + (lane >> 4);
-            if (in && c < nc) {
-              const float xs = cs[c0 + c];
-              dst[(int64_t)2 * i * p.channels] = fast_swiglu((upper ? got : keep) * xs * w0, (upper ? keep : got) * xs * w1);
-            }
+            const float x = xs[2 * i];
+            h[i] = fast_swiglu((upper ? got : keep) * x * w0, (upper ? keep : got) * x * w1);
+          }
+          const int limit = in ? nc - (lane >> 4) : 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (2 * i < limit) *dst = h[i];
+            dst += 2 * p.channels;
           }
         } else if (KIND == kDown || p.wide) {
           // 16-bit results: turned in shared memory, so that a token's 32 channels leave in 16-byte pieces
