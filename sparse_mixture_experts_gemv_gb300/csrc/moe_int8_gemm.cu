@@ -408,23 +408,38 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     uint16_t* turn = s_turn + quad * 1024;    // 32 tokens x 32 channels
     const bool f16_out = p.out_dtype == MOE_DTYPE_F16;
     uint32_t tc = 0;
+    const auto channel = [&](const Tile& t) {
+      return KIND == kUp ? t.mt * 64 + quad * 16 + (lane & 15) : t.mt * kChannels + quad * 32 + lane;
+    };
+    // A tile and its lane's scales are loaded a tile ahead: on a short tile their latency would show.
+    const auto scales = [&](const Tile& t, float& a, float& b) {
+      const int ch = channel(t);
+      const float* w = p.w_scale + (KIND == kDense ? 0 : (int64_t)t.e * p.rows_per_group) + ch;
+      a = ch < p.channels ? __ldg(w) : 0.f;
+      b = 1.f;
+      if (KIND == kUp && ch < p.channels) b = __ldg(w + p.channels);
+      if (KIND == kDown) b = ldg_cg_f32(p.norms + t.e);
+    };
+    Tile next = {};
+    float next0 = 0.f, next1 = 1.f;
+    if ((int)blockIdx.x < total) {
+      next = decode<KIND>(p, blockIdx.x);
+      scales(next, next0, next1);
+    }
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++tc) {
-      const Tile t = decode<KIND>(p, tile);
+      const Tile t = next;
+      const float w0 = KIND == kDown ? next0 * (p.factor / next1) : next0, w1 = next1;
       const uint32_t ab = tc & 1;
       __syncwarp();
       if (KIND != kDown) {
         for (int c = lane; c < t.rows; c += 32) cs[c] = ldg_cg_f32(p.row_scale + t.row0 + c);
       }
-      const int ch = KIND == kUp ? t.mt * 64 + quad * 16 + (lane & 15) : t.mt * kChannels + quad * 32 + lane;
-      const bool in = ch < p.channels;
-      float w0 = 0.f, w1 = 0.f;
-      if (in && KIND == kDense) w0 = __ldg(p.w_scale + ch);
-      if (in && KIND == kDown)
-        w0 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + ch) * (p.factor / ldg_cg_f32(p.norms + t.e));
-      if (in && KIND == kUp) {
-        w0 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + ch);
-        w1 = __ldg(p.w_scale + (int64_t)t.e * p.rows_per_group + p.channels + ch);
+      if (tile + (int)gridDim.x < total) {
+        next = decode<KIND>(p, tile + gridDim.x);
+        scales(next, next0, next1);
       }
+      const int ch = channel(t);
+      const bool in = ch < p.channels;
       __syncwarp();
       if (!warp_wait(smem_u32(&d_full[ab]), (tc >> 1) & 1, abort_flag)) break;
       tc_fence_after();
