@@ -692,8 +692,15 @@ int dtype_size(int d) { return d == MOE_DTYPE_S8 ? 1 : d == MOE_DTYPE_F32 ? 4 : 
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
-// Tokens up to which the weights are streamed through the dot-product units.
-constexpr int kStreamTokens = 8;
+// Which of the two a product takes. The tensor cores cost a launch more and convert every weight byte; the
+// dot-product units read the weights once for each eight tokens and take a quarter of a product's
+// multiply-adds in instructions. GB300, us a call, dot products / tensor cores: 32 x 2,048 x 2,048 15 / 20,
+// 64 x 2,048 x 2,048 26 / 19; 16 x 4,096 x 4,096 19 / 23, 24 x 4,096 x 4,096 33 / 21; 4 x 4,096 x 16,384
+// 19.5 / 21, 8 x 4,096 x 16,384 29 / 21.
+bool stream_matmul(int64_t T, int64_t N, int64_t K) { return T <= 4 || T * N * K <= 200000000; }
+// Experts (H 2,048, I 512, 8 of 256): 16 tokens 89 / 93, 24 tokens 114 / 113; (2,048, 512, 2 of 16): 23 / 32
+// and 28 / 33, 32 tokens 36 / 33; (1,024, 512, 4 of 64): 27 / 35 and 31 / 36, 32 tokens 43 / 37.
+bool stream_experts(int64_t T) { return T <= 16; }
 
 cudaError_t launch_prepare(const PrepareParams& p, int dtype, int num_sms, cudaStream_t s) {
   const int64_t blocks = ((int64_t)p.rows + kPrepareThreads / 32 - 1) / (kPrepareThreads / 32);
@@ -709,16 +716,16 @@ cudaError_t launch_prepare(const PrepareParams& p, int dtype, int num_sms, cudaS
 struct MatmulWorkspace {
   int64_t q, scale, bytes;
 };
-MatmulWorkspace matmul_workspace(int64_t T, int64_t K) {
+MatmulWorkspace matmul_workspace(int64_t T, int64_t N, int64_t K) {
   MatmulWorkspace w = {};
-  if (T <= kStreamTokens) return w;
+  if (stream_matmul(T, N, K)) return w;
   w.scale = pad256(T * pad64(K) * 2);
   w.bytes = w.scale + pad256(T * 4);
   return w;
 }
 
 cudaError_t launch_matmul_tensor(const StreamParams& p, int x_dtype, uint8_t* ws, int num_sms, cudaStream_t s) {
-  const MatmulWorkspace w = matmul_workspace(p.T, p.K);
+  const MatmulWorkspace w = matmul_workspace(p.T, p.N, p.K);
   PrepareParams a = {};
   a.x = p.x;
   a.stride = p.x_stride;
@@ -739,7 +746,10 @@ cudaError_t launch_matmul_tensor(const StreamParams& p, int x_dtype, uint8_t* ws
   g.b_stride = a.K64;
   g.K = p.K;
   g.channels = p.N;
-  const int tiles = (p.T + kMaxBlock - 1) / kMaxBlock;   // as few token tiles as there can be, of even size
+  // token tiles of even size: as few as there can be, or as many as give every SM a tile
+  const int fewest = (p.T + kMaxBlock - 1) / kMaxBlock, most = (p.T + 15) / 16;
+  const int spread = num_sms / ((p.N + 127) / 128);
+  const int tiles = spread < fewest ? fewest : spread < most ? spread : most;
   g.block = ((p.T + tiles - 1) / tiles + 15) / 16 * 16;
   g.T = p.T;
   g.row_scale = a.scale;
@@ -757,7 +767,7 @@ struct ExpertsWorkspace {
 ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T) {
   ExpertsWorkspace w = {};
   const int64_t rows = T * c->top_k, H = c->hidden, I = c->intermediate;
-  if (T <= kStreamTokens) {
+  if (stream_experts(T)) {
     w.bytes = pad256(rows * I * 4);
     return w;
   }
@@ -904,7 +914,7 @@ extern "C" {
 
 moe_status_t moe_quant_matmul_workspace(int32_t T, int32_t N, int32_t K, int32_t x_dtype, int64_t* bytes) {
   if (!bytes || T < 0 || N < 0 || K < 1 || x_dtype < MOE_DTYPE_F32 || x_dtype > MOE_DTYPE_S8) return MOE_ERR_INVALID_ARG;
-  *bytes = moe::int8::matmul_workspace(T, K).bytes;
+  *bytes = moe::int8::matmul_workspace(T, N, K).bytes;
   return MOE_OK;
 }
 
@@ -928,7 +938,7 @@ moe_status_t moe_quant_matmul(const void* x_dev, int32_t x_dtype, int64_t x_stri
   if (overlap(x_dev, ((T - 1) * x_stride + K) * xs, out_dev, (int64_t)T * N * os) ||
       overlap(w_dev, (N - 1) * w_stride + K, out_dev, (int64_t)T * N * os))
     return MOE_ERR_INVALID_ARG;
-  const int64_t need = matmul_workspace(T, K).bytes;
+  const int64_t need = matmul_workspace(T, N, K).bytes;
   if (need && (!workspace_dev || workspace_bytes < need || (uintptr_t)workspace_dev & 255)) return MOE_ERR_INVALID_ARG;
   const StreamParams p = {x_dev, x_stride, x_scale_dev, w_dev, w_stride, w_scale_dev, out_dev, out_dtype, T, N, K};
   cudaStream_t s = (cudaStream_t)stream;
@@ -990,7 +1000,7 @@ moe_status_t moe_quant_experts(const moe_int8_experts_config_t* c, const moe_int
   p.H = c->hidden;
   p.I = c->intermediate;
   p.out_dtype = x_dtype;
-  const cudaError_t e = T <= kStreamTokens
+  const cudaError_t e = stream_experts(T)
                             ? launch_experts_stream(p, x_dtype, device_sms(), (cudaStream_t)stream)
                             : launch_experts_tensor(p, c, x_dtype, (uint8_t*)workspace_dev, device_sms(),
                                                     (cudaStream_t)stream);

@@ -71,6 +71,51 @@ def test_shapes(T, K, n):
         _close(M.int8_matmul(x, w, ws, out_dtype=torch.float32), ref, 0, torch.float32)
 
 
+@pytest.mark.parametrize("T,K,n", [(5, 4096, 10001), (9, 4096, 5500), (17, 2064, 6001), (31, 2048, 4096), (65, 1040, 3001),
+                                   (96, 1104, 2000), (193, 1552, 700), (385, 272, 2049), (1000, 336, 700),
+                                   (1200, 128, 1501), (2048, 80, 1352)])
+def test_shapes_on_the_tensor_cores(T, K, n):
+    """Products too large for the dot-product units: tiles of every number of tokens, ragged in all directions."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    w, ws = _ints(n, K, seed=n), _scales(n, seed=n)
+    q, qs = _ints(T, K, seed=T, lo=-20, hi=21), _scales(T, seed=T)
+    ref = o.matmul(_np(q), _np(w), _np(ws), _np(qs))
+    for out in DT.values():
+        _close(M.int8_matmul(q, w, ws, qs, out_dtype=out), ref, 0, out)
+    for dtype in DT:
+        x = _x(T, K, dtype, seed=T)
+        _close(M.int8_matmul(x, w, ws, out_dtype=torch.float32), o.matmul(_np(x), _np(w), _np(ws)), 0, torch.float32)
+
+
+def test_rows_that_are_not_finite_on_the_tensor_cores():
+    import sparse_mixture_experts_gemv_gb300 as M
+    w, ws = _ints(2000, 1040), _scales(2000)
+    x = _x(130, 1040, "bf16")
+    want = M.int8_matmul(x, w, ws)
+    x[3, 5], x[77, 1039], x[129] = float("inf"), float("nan"), 0
+    got = M.int8_matmul(x, w, ws)
+    assert torch.isnan(got[3]).all() and torch.isnan(got[77]).all() and (got[129] == 0).all()
+    others = [t for t in range(129) if t not in (3, 77)]
+    assert torch.equal(got[others], want[others])
+
+
+@pytest.mark.parametrize("T", [7, 24])
+def test_largest_sums_on_the_tensor_cores(T):
+    """As below, with sums up to 2^28 of one sign: kept to 24 bits in the accumulators."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    K, n = 16384, 2048
+    w = torch.full((n, K), 127, dtype=torch.int8)
+    w[1::3] = -128
+    w[2::3, ::2] = -127
+    x = torch.full((T, K), -128, dtype=torch.int8)
+    x[0] = 127
+    ws, xs = torch.ones(n), torch.ones(T)
+    got = M.int8_matmul(x.cuda(), w.cuda(), ws.cuda(), xs.cuda(), out_dtype=torch.float32)
+    ref = o.matmul(_np(x), _np(w), _np(ws), _np(xs))
+    mag = np.abs(_np(x)) @ np.abs(_np(w)).T
+    _close(got, ref, K / 16 * 2 * STEP, torch.float32, mag)
+
+
 @pytest.mark.parametrize("T", [1, 4, 20, 150])
 def test_largest_sums(T):
     """All values at their largest, -128 among them: sums up to 2^27 and sums that cancel."""
@@ -138,6 +183,9 @@ def test_strides_alignment_and_defaults():
     import sparse_mixture_experts_gemv_gb300 as M
     base, wb = _x(300, 320, "bf16"), _ints(200, 272)
     ws = _scales(200)
+    big, big_ws = _ints(3000, 272, seed=3), _scales(3000, seed=3)
+    for x, w in ((base[:, :256], big[:, :256]), (base[:, 8:264], big[:, 16:]), (base[:, 3:259], big[:, 5:261])):
+        _close(M.int8_matmul(x, w, big_ws), o.matmul(_np(x), _np(w), _np(big_ws)), 0, torch.bfloat16)
     for T in (3, 300):
         for x, w in ((base[:T, :256], wb[:, :256]), (base[:T, 8:264], wb[:, 16:]), (base[:T, 3:259], wb[:, 5:261]),
                      (base[:T, :256].t().contiguous().t(), wb[:, :256]), (base[:, :256][:2 * T:2], wb[:, :256])):
@@ -168,7 +216,7 @@ def test_refusals():
 
 def test_streams_graph_and_repeats():
     import sparse_mixture_experts_gemv_gb300 as M
-    w, ws = _ints(777, 512), _scales(777)
+    w, ws = _ints(1777, 512), _scales(1777)
     for T in (1, 8, 300):
         x = _x(T, 512, "bf16")
         want = M.int8_matmul(x, w, ws)
