@@ -213,14 +213,12 @@ __global__ void __launch_bounds__(kThreads, 3) int8_experts_up_kernel(const Expe
     __syncthreads();
     quantize_rows_to_smem<DT>(static_cast<const uint16_t*>(p.x) + a / p.k * p.H, p.H, nullptr, 1, p.H, q, s_scale, red);
     __syncthreads();
-    const int f0 = c0 + 2 * warp;
-    if (f0 >= p.I) continue;
-    const int f1 = min(f0 + 1, p.I - 1);
+    const int f0 = min(c0 + 2 * warp, p.I - 1), f1 = min(f0 + 1, p.I - 1);   // a warp past the end repeats the last
     const int8_t* rows[4] = {p.gate_up + (row0 + f0) * p.H, p.gate_up + (row0 + p.I + f0) * p.H,
                              p.gate_up + (row0 + f1) * p.H, p.gate_up + (row0 + p.I + f1) * p.H};
     int acc[4][1];
     dot_rows<1, 4>(rows, q, p.H / 16, lane, acc);
-    if (lane < 2 && f0 + lane < p.I) {
+    if (lane < 2 && c0 + 2 * warp + lane < p.I) {
       const float* ws = p.gate_up_scale + row0 + f0 + lane;
       const float g = (float)(lane ? acc[2][0] : acc[0][0]) * s_scale[0] * __ldg(ws);
       const float u = (float)(lane ? acc[3][0] : acc[1][0]) * s_scale[0] * __ldg(ws + p.I);
@@ -479,9 +477,9 @@ __global__ void __launch_bounds__(kPrepareThreads) int8_prepare_kernel(const Pre
 }
 
 // Choices in the order of their experts, and each one's token as whole numbers in f16 in
-// that order. Two launches over the same chunks of tokens: the first counts each chunk's
-// choices by expert; in the second every CTA adds the counts up for itself (which
-// rows its chunk's choices take), and copies its tokens to their rows, k each. Gathering the
+// that order, k copies. Every CTA finds out for itself which rows its chunk of tokens takes:
+// from all choices, or, where they are many, from their counts by expert and chunk that a
+// launch before has taken. (At 32,768 choices both take some 3 us, a launch more for the counts.) Gathering the
 // rows inside the product instead took a copy of four rows at a time, whose issue alone
 // made the up product 683 us at T = 4096 (Qwen-shaped).
 struct GroupParams {
@@ -490,7 +488,7 @@ struct GroupParams {
   int T, k, E, H, H64;       // H64: H rounded up to 64
   int chunk, chunks;         // tokens of a CTA
   int block, max_blocks;
-  int* chunk_counts;         // [chunks][E]
+  int* chunk_counts;         // [chunks][E]; NULL: count all choices
   __half* q;                 // [rows][H64], zeros behind H
   float* scale;              // [rows]
   int* pos;                  // [T][k]: grouped row, -1 where there is none
@@ -531,7 +529,17 @@ __global__ void __launch_bounds__(kGroupThreads, 1) int8_group_kernel(const Grou
   __syncthreads();
   // several threads an expert where there are few experts: part q of n takes chunks q, q + n, ...
   const int parts = max(1, kGroupThreads / p.E), part = i / p.E;
-  if (part < parts) {
+  if (!p.chunk_counts) {
+    const int choices = p.T * p.k, first = blockIdx.x * p.chunk * p.k;
+#pragma unroll 4
+    for (int a = i; a < choices; a += kGroupThreads) {
+      const int e = __ldg(p.idx + a);
+      if (e >= 0 && e < p.E) {
+        atomicAdd(&all[e], 1);
+        if (a < first) atomicAdd(&before[e], 1);
+      }
+    }
+  } else if (part < parts) {
     const int e = i - part * p.E;
     int sum = 0, own = 0;
 #pragma unroll 8
@@ -759,6 +767,9 @@ cudaError_t launch_matmul_tensor(const StreamParams& p, int x_dtype, uint8_t* ws
   return launch_gemm(kDense, g, num_sms, s);
 }
 
+// Whether a launch counts the choices of each chunk first.
+bool count_first(int64_t choices) { return choices > 32768; }
+
 // Scratch of the experts' call. y takes h's place, which is dead by then.
 struct ExpertsWorkspace {
   int64_t h, q, x_scale, hq, h_scale, norms, chunk_counts, pos, blocks, counts, bytes;
@@ -787,7 +798,7 @@ ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T
   w.hq = take(rows * pad64(I) * 2);
   w.h_scale = take(rows * 4);
   w.norms = take((int64_t)c->num_experts * 4);
-  w.chunk_counts = take((int64_t)w.chunks * c->num_experts * 4);
+  w.chunk_counts = take(count_first(rows) ? (int64_t)w.chunks * c->num_experts * 4 : 0);
   w.pos = take(rows * 4);
   w.blocks = take((int64_t)w.max_blocks * 16);
   w.counts = take(8);
@@ -811,13 +822,14 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   a.chunks = w.chunks;
   a.block = w.block;
   a.max_blocks = w.max_blocks;
-  a.chunk_counts = (int*)(ws + w.chunk_counts);
+  a.chunk_counts = count_first(rows) ? (int*)(ws + w.chunk_counts) : nullptr;
   a.q = (__half*)(ws + w.q);
   a.scale = (float*)(ws + w.x_scale);
   a.pos = (int*)(ws + w.pos);
   a.blocks = (int4*)(ws + w.blocks);
   a.counts = (int*)(ws + w.counts);
-  cudaError_t e = launch_pdl(int8_count_kernel, dim3(w.chunks), kGroupThreads, 0, s, a);
+  cudaError_t e = cudaSuccess;
+  if (a.chunk_counts) e = launch_pdl(int8_count_kernel, dim3(w.chunks), kGroupThreads, 0, s, a);
   if (e != cudaSuccess) return e;
   e = x_dtype == MOE_DTYPE_BF16 ? launch_pdl(int8_group_kernel<MOE_DTYPE_BF16>, dim3(w.chunks), kGroupThreads, 0, s, a)
                                 : launch_pdl(int8_group_kernel<MOE_DTYPE_F16>, dim3(w.chunks), kGroupThreads, 0, s, a);

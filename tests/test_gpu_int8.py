@@ -280,6 +280,18 @@ def test_experts(T, E, k, H, I, dtype):
     _check_experts(x, idx, w, ex, got)
 
 
+def test_more_choices_than_are_counted_at_once():
+    """T * k above 32,768: sampled tokens against the same tokens in a call of their own."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    T, E, k, H, I = 4500, 20, 8, 64, 32
+    x, (idx, w), ex = _x(T, H, "bf16"), _choices(T, E, k), _experts(E, H, I)
+    idx[5] = -1
+    got = M.int8_experts(x, idx, w, *ex)
+    some = torch.tensor([0, 1, 5, 31, 32, 2222, 4463, 4464, 4499], device="cuda")
+    assert (got[5] == 0).all()
+    _check_experts(x[some], idx[some], w[some], ex, got[some])
+
+
 @pytest.mark.parametrize("T", [3, 100])
 def test_choices_left_out_and_uneven_loads(T):
     import sparse_mixture_experts_gemv_gb300 as M
