@@ -231,9 +231,9 @@ constexpr int kMaxChoices = MOE_ROUTE_MAX_TOP_K;
 
 // out of one token (blockIdx.y) and CH channels a warp, all its choices. Dynamic shared memory: `held`
 // quantized rows of h; every CTA quantizes all of the token's, which more channels a warp keep from being
-// most of the work. The rows of the weights are known before h is: they are requested into L2 while the
-// kernel before is still at work. (Reading idx ahead of the wait is sound: that kernel lets this one start
-// only after its own wait, when all that the caller had enqueued is done.) The chunks of all the held
+// most of the work. (Ling-shaped, T = 4: of 42 us for both kernels the tokens' quantization here is 5, the
+// rows 13. Requesting the rows into L2 ahead of h, by this kernel or the one before, made it 45 and 46.5.)
+// The chunks of all the held
 // choices are one list: lane l takes chunks l, l + 32, ..., 8 / CH of them and CH channels at once, so that
 // eight loads are in flight and a chunk's place and token values serve CH channels.
 template <int CH>
@@ -245,11 +245,6 @@ __global__ void __launch_bounds__(kThreads, 3) int8_experts_down_kernel(const Ex
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nch = p.I / 16;
   const int c0 = blockIdx.x * kWarps * CH, ch0 = c0 + warp * CH;
-  if (threadIdx.x < p.k) {
-    const int e = __ldg(p.idx + (int64_t)blockIdx.y * p.k + threadIdx.x);
-    if (e >= 0 && e < p.E)
-      prefetch_l2_bulk(p.down + ((int64_t)e * p.H + c0) * p.I, (uint32_t)(min(kWarps * CH, p.H - c0) * p.I));
-  }
   pdl_wait();
   pdl_launch_dependents();
   for (int64_t t = blockIdx.y; t < p.T; t += gridDim.y) {
