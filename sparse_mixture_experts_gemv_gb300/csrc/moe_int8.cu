@@ -700,7 +700,8 @@ int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 // multiply-adds in instructions. GB300, us a call, dot products / tensor cores: 32 x 2,048 x 2,048 15 / 20,
 // 64 x 2,048 x 2,048 26 / 19; 16 x 4,096 x 4,096 19 / 23, 24 x 4,096 x 4,096 33 / 21; 4 x 4,096 x 16,384
 // 19.5 / 21, 8 x 4,096 x 16,384 29 / 21.
-bool stream_matmul(int64_t T, int64_t N, int64_t K) { return T <= 4 || T * N * K <= 200000000; }
+// (Eight tokens are a row of the grid, which has 65,535: many rows of a tiny product go to the tensor cores.)
+bool stream_matmul(int64_t T, int64_t N, int64_t K) { return T <= 4 || (T <= 4096 && T * N * K <= 200000000); }
 // Experts (H 2,048, I 512, 8 of 256): 16 tokens 89 / 93, 24 tokens 114 / 113; (2,048, 512, 2 of 16): 23 / 32
 // and 28 / 33, 32 tokens 36 / 33; (1,024, 512, 4 of 64): 27 / 35 and 31 / 36, 32 tokens 43 / 37.
 bool stream_experts(int64_t T) { return T <= 16; }

@@ -87,6 +87,14 @@ def test_shapes_on_the_tensor_cores(T, K, n):
         _close(M.int8_matmul(x, w, ws, out_dtype=torch.float32), o.matmul(_np(x), _np(w), _np(ws)), 0, torch.float32)
 
 
+def test_very_many_rows_of_a_tiny_product():
+    import sparse_mixture_experts_gemv_gb300 as M
+    T = 600000
+    q, qs, w, ws = _ints(T, 16), _scales(T), _ints(3, 16), _scales(3)
+    got = M.int8_matmul(q, w, ws, qs, out_dtype=torch.float32)
+    _close(got, o.matmul(_np(q), _np(w), _np(ws), _np(qs)), 0, torch.float32)
+
+
 def test_rows_that_are_not_finite_on_the_tensor_cores():
     import sparse_mixture_experts_gemv_gb300 as M
     w, ws = _ints(2000, 1040), _scales(2000)
