@@ -26,13 +26,15 @@ def _experts_config(E, k, H, I, T):
     return ctypes.byref(cfg), b.value
 
 
-def _rows(t, what, name):
-    """A matrix whose rows the kernels can read: 16-byte addresses and row strides."""
-    size = t.element_size()
-    if t.stride(1) != 1 or t.stride(0) < t.shape[1] or t.stride(0) * size % 16 or t.data_ptr() % 16:
+def _rows(t, K, what, name):
+    """A matrix whose rows the kernels can read (16-byte addresses and row strides), its address and row stride."""
+    size, ptr = t.element_size(), t.data_ptr()
+    stride, inner = t.stride()
+    if inner != 1 or stride < K or (ptr | stride * size) & 15:
         t = t.clone(memory_format=torch.contiguous_format)
-        want(t.shape[1] * size % 16 == 0, what, f"the rows of {name} must be a multiple of 16 bytes long")
-    return t
+        ptr, stride = t.data_ptr(), K
+        want(K * size % 16 == 0, what, f"the rows of {name} must be a multiple of 16 bytes long")
+    return t, ptr, stride
 
 
 def int8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale: torch.Tensor = None,
@@ -48,34 +50,37 @@ def int8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale
     if stream is not None:
         return run_on(stream, int8_matmul, x, w, w_scale, x_scale, out_dtype)
     what = "int8_matmul"
-    if not x.is_cuda or x.dim() != 2 or x.dtype not in DTYPE_CODES:
+    code = DTYPE_CODES.get(x.dtype)
+    if code is None or not x.is_cuda or x.dim() != 2:
         invalid(what, "x must be a CUDA tensor [T, K] of int8, bf16, fp16 or fp32")
     T, K = x.shape
     dev = x.device
-    if w.dim() != 2 or w.dtype is not torch.int8 or w.shape[1] != K or w.device != dev:
+    if w.dtype is not torch.int8 or w.dim() != 2 or w.shape[1] != K or w.device != dev:
         invalid(what, f"w must be int8 [N, {K}] on {dev}")
     n = w.shape[0]
     w_scale = vector(w_scale, "w_scale", n, what, dev)
-    quantized = x.dtype is torch.int8
+    quantized = code == N.MOE_DTYPE_S8
     if quantized != (x_scale is not None):
         invalid(what, "x_scale goes with int8 x, and with no other")
     if quantized:
         x_scale = vector(x_scale, "x_scale", T, what, dev)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if quantized else x.dtype
-    if out_dtype not in DTYPE_CODES or out_dtype is torch.int8:
+    out_code = DTYPE_CODES.get(out_dtype)
+    if out_code is None or out_code == N.MOE_DTYPE_S8:
         invalid(what, "out_dtype must be bf16, fp16 or fp32")
     out = torch.empty((T, n), dtype=out_dtype, device=dev)
     if T == 0 or n == 0:
         return out
-    x, w = _rows(x, what, "x"), _rows(w, what, "w")
-    code = DTYPE_CODES[x.dtype]
+    x, x_ptr, x_stride = _rows(x, K, what, "x")
+    w, w_ptr, w_stride = _rows(w, K, what, "w")
     need = _matmul_workspace(T, n, K, code)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    check(N.load().moe_quant_matmul(x.data_ptr(), code, x.stride(0), None if x_scale is None else x_scale.data_ptr(),
-                                   w.data_ptr(), w.stride(0), w_scale.data_ptr(), out.data_ptr(),
-                                   DTYPE_CODES[out_dtype], T, n, K, None if ws is None else ws.data_ptr(), need,
-                                   current_stream(dev)), "moe_quant_matmul")
+    status = N.load().moe_quant_matmul(x_ptr, code, x_stride, None if x_scale is None else x_scale.data_ptr(), w_ptr,
+                                       w_stride, w_scale.data_ptr(), out.data_ptr(), out_code, T, n, K,
+                                       None if ws is None else ws.data_ptr(), need, current_stream(dev))
+    if status:
+        check(status, "moe_quant_matmul")
     return out
 
 

@@ -11,6 +11,7 @@ import torch
 from . import _native as N
 from ._tensors import DTYPE_CODES, check, current_stream, invalid, run_on, vector, want
 
+LOGIT_CODES = {t: c for t, c in DTYPE_CODES.items() if t is not torch.int8}
 SCORES = {"softmax": N.MOE_SCORE_SOFTMAX, "sigmoid": N.MOE_SCORE_SIGMOID}
 
 
@@ -23,25 +24,29 @@ def _config(E, k, score, groups, top_groups, group_top, renormalise, scale):
 
 
 def _logits(what, logits):
-    if not logits.is_cuda or logits.dim() != 2 or logits.dtype not in DTYPE_CODES or logits.dtype is torch.int8:
+    """The logits with their dtype's code, shape and row stride, copied where rows have gaps inside."""
+    code = LOGIT_CODES.get(logits.dtype)
+    if code is None or not logits.is_cuda or logits.dim() != 2:
         invalid(what, "logits must be a CUDA tensor [T, E] of fp32, bf16 or fp16")
-    if logits.stride(1) != 1 or logits.stride(0) < logits.shape[1]:
-        logits = logits.contiguous()
-    return logits
+    T, E = logits.shape
+    stride, inner = logits.stride()
+    if inner != 1 or stride < E:
+        logits, stride = logits.contiguous(), E
+    return logits, code, T, E, stride if T > 1 else E   # one row has no next one: its stride may be anything
 
 
 def _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise, scale):
-    logits = _logits("route_experts", logits)
-    T, E = logits.shape
+    logits, code, T, E, stride = _logits("route_experts", logits)
     dev = logits.device
     if bias is not None:
         bias = vector(bias, "bias", E, "route_experts", dev)
     idx = torch.empty((T, k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    check(N.load().moe_route_experts(_config(E, k, score, groups, top_groups, group_top, renormalise, scale),
-                                     logits.data_ptr(), DTYPE_CODES[logits.dtype], logits.stride(0) if T > 1 else E,
-                                     None if bias is None else bias.data_ptr(), T, idx.data_ptr(), weights.data_ptr(),
-                                     current_stream(dev)), "moe_route_experts")
+    status = N.load().moe_route_experts(_config(E, k, score, groups, top_groups, group_top, renormalise, scale),
+                                        logits.data_ptr(), code, stride, None if bias is None else bias.data_ptr(), T,
+                                        idx.data_ptr(), weights.data_ptr(), current_stream(dev))
+    if status:
+        check(status, "moe_route_experts")
     return idx, weights
 
 
@@ -92,8 +97,7 @@ def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, idx: t
     if stream is not None:
         return run_on(stream, route_experts_backward, d_weights, logits, idx, score, renormalise, scale)
     what = "route_experts_backward"
-    logits = _logits(what, logits)
-    T, E = logits.shape
+    logits, code, T, E, stride = _logits(what, logits)
     dev = logits.device
     want(idx.dim() == 2 and idx.shape[0] == T and idx.dtype is torch.int32 and idx.device == dev, what,
          "idx must be int32 [T, k] on the logits' device")
@@ -103,7 +107,7 @@ def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, idx: t
     idx, d_weights = idx.contiguous(), d_weights.contiguous()
     d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
     check(N.load().moe_route_experts_backward(_config(E, k, score, 1, 1, 1, renormalise, scale), logits.data_ptr(),
-                                              DTYPE_CODES[logits.dtype], logits.stride(0) if T > 1 else E,
+                                              code, stride,
                                               idx.data_ptr(), d_weights.data_ptr(), T, d_logits.data_ptr(),
                                               current_stream(dev)), "moe_route_experts_backward")
     return d_logits
