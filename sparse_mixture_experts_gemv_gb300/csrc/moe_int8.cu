@@ -104,6 +104,8 @@ struct StreamParams {
 // CTAs an SM holds at once, by tokens: what their accumulators and loads in flight leave of the registers.
 constexpr int stream_ctas(int tokens) { return tokens >= 4 ? 2 : 3; }
 
+// 157,184 x 2,560 and one token: 58.6 us, 6.9 TB/s of weights and results, the rate of a copy; 1,024 x
+// 2,048: 6 us, of which the launch and the token's quantization are most.
 template <int DT, int T>
 __global__ void __launch_bounds__(kThreads, stream_ctas(T)) int8_stream_kernel(const StreamParams p) {
   extern __shared__ uint4 q[];   // [T][K / 16]
@@ -194,7 +196,8 @@ struct ExpertsParams {
 constexpr int kFeatures = 2 * kWarps;   // intermediate features of a CTA: two a warp (four rows)
 
 // h of one choice (blockIdx.y) and kFeatures features. As soon as the expert is known its rows are
-// requested into L2, two contiguous pieces: they come while the token is being quantized.
+// requested into L2, two contiguous pieces: they come while the token is being quantized. Ling-shaped, T = 4:
+// 24 us for 115 MB of distinct rows, 4.8 TB/s (31 us without the request); Qwen-shaped, T = 1: 8 us, latency.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 3) int8_experts_up_kernel(const ExpertsParams p) {
   extern __shared__ uint4 q[];   // [H / 16]
@@ -454,7 +457,7 @@ MOE_DEV float quantize_row(const void* x, int64_t i, int K, int K64, int lane, P
 
 constexpr int kPrepareThreads = 256;
 
-// Rows as whole numbers in f16, and their scales: one warp a row.
+// Rows as whole numbers in f16, and their scales: one warp a row. 32,768 rows of 512 fp32: 21 us, 4.8 TB/s.
 template <int DT>
 __global__ void __launch_bounds__(kPrepareThreads) int8_prepare_kernel(const PrepareParams p) {
   pdl_wait();
@@ -509,6 +512,7 @@ __global__ void __launch_bounds__(kGroupThreads) int8_count_kernel(const GroupPa
   for (int e = threadIdx.x; e < p.E; e += kGroupThreads) p.chunk_counts[(int64_t)blockIdx.x * p.E + e] = count[e];
 }
 
+// 4,096 tokens of 2,048, k = 8: 28 us, for 134 MB of rows written.
 // An expert's rows are cut evenly into blocks of at most p.block. Within an expert and a
 // chunk the order is the shared-memory atomics': every row is computed by itself, so no
 // result depends on it.
@@ -609,7 +613,8 @@ struct CombineParams {
 
 constexpr int kCombineThreads = 256;
 
-// out[t] = sum_j weights[t, j] h_scale factor norm[e_j] y_j, eight channels a thread.
+// out[t] = sum_j weights[t, j] h_scale factor norm[e_j] y_j, eight channels a thread. Reading y bounds it:
+// 4,096 tokens, k = 8, H = 2,048: 31 us, 4.9 TB/s.
 __global__ void __launch_bounds__(kCombineThreads) int8_combine_kernel(const CombineParams p) {
   __shared__ float s_f[MOE_ROUTE_MAX_TOP_K];
   __shared__ int s_pos[MOE_ROUTE_MAX_TOP_K];

@@ -311,7 +311,9 @@ MOE_DEV float rcp(float v) {
 // keys lie above it (about 10 for k = 8). These, each in a lane of its own and in the order of their
 // indexes, are ranked by counting; with a bias or groups, keys closer than `near` are ranked again in
 // 64 bits, one evaluation a lane.
-// What bounds it is its instructions, a warp's per row, not the 16 bytes a lane that it reads.
+// What bounds it is its instructions, a warp's per row, not what it reads: 65,536 rows of 512 bf16 logits
+// with a bias and groups take 75 us, 909 instructions a row with 69% of the issue slots busy (all keys through k
+// rounds of a warp: 457 us); 4,096 rows of 256 without 6 us.
 template <int DT, int NPL, bool VEC, bool KEYED>
 __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(const RouteParams p) {
   __shared__ double s_keys[kRouteWarps][32 * NPL];
@@ -545,7 +547,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
 //   softmax:       dl[e] = s[e] (ds[e] - sum_j ds[j] s[j]);  sigmoid: dl[e] = s[e] (1 - s[e]) ds[e]
 // For the renormalised softmax the last sum is 0 and s[e] ds[e] = r[e] (d[e] - sum_i d[i] r[i]) with
 // the ratios r = s / S, and for the renormalised sigmoid dl = r (1 - s) (d - sum d r): only the chosen
-// logits are read then. All rows are written whole.
+// logits are read then. All rows are written whole. 8,191 rows of 256 fp32: 7 us, most of it the rows'
+// way through shared memory.
 struct RouteBackParams {
   const void* logits;
   int64_t stride;
