@@ -700,13 +700,14 @@ int dtype_size(int d) { return d == MOE_DTYPE_S8 ? 1 : d == MOE_DTYPE_F32 ? 4 : 
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
-// Which of the two a product takes. The tensor cores cost a launch more and convert every weight byte; the
-// dot-product units read the weights once for each eight tokens and take a quarter of a product's
-// multiply-adds in instructions. GB300, us a call, dot products / tensor cores: 32 x 2,048 x 2,048 15 / 20,
-// 64 x 2,048 x 2,048 26 / 19; 16 x 4,096 x 4,096 19 / 23, 24 x 4,096 x 4,096 33 / 21; 4 x 4,096 x 16,384
-// 19.5 / 21, 8 x 4,096 x 16,384 29 / 21.
-// (Eight tokens are a row of the grid, which has 65,535: many rows of a tiny product go to the tensor cores.)
-bool stream_matmul(int64_t T, int64_t N, int64_t K) { return T <= 4 || (T <= 4096 && T * N * K <= 200000000); }
+// Which of the two a product takes. The tensor cores cost a launch more (some 5 us) and are as fast with 64 tokens
+// as with one; the dot-product units read the weights once for each eight tokens, and their time goes by the
+// results, each of which a warp adds up. GB300, us a call, dot products / tensor cores, tokens x K x channels:
+//   2 x 2,560 x 157,184  66 / 74     4 x 2,560 x 157,184  81 / 72      4 x 1,024 x 32,768   16 / 20
+//   4 x 4,096 x 16,384   20 / 22     8 x 4,096 x 16,384   30 / 23     32 x 2,048 x 2,048    15 / 18
+//  64 x 2,048 x 2,048    26 / 16   128 x 2,048 x 512      15 / 16    256 x 2,048 x 512      28 / 17
+//  16 x 16,384 x 4,096   57 / 89   512 x 128 x 128        12 / 19  1,024 x 128 x 128        21 / 17
+bool stream_matmul(int64_t T, int64_t N) { return T <= 2 || T * N <= (T <= 4 ? 131072 : 65536); }
 // Experts (H 2,048, I 512, 8 of 256): 16 tokens 89 / 93, 24 tokens 114 / 113; (2,048, 512, 2 of 16): 23 / 32
 // and 28 / 33, 32 tokens 36 / 33; (1,024, 512, 4 of 64): 27 / 35 and 31 / 36, 32 tokens 43 / 37.
 bool stream_experts(int64_t T) { return T <= 16; }
@@ -727,7 +728,7 @@ struct MatmulWorkspace {
 };
 MatmulWorkspace matmul_workspace(int64_t T, int64_t N, int64_t K) {
   MatmulWorkspace w = {};
-  if (stream_matmul(T, N, K)) return w;
+  if (stream_matmul(T, N)) return w;
   w.scale = pad256(T * pad64(K) * 2);
   w.bytes = w.scale + pad256(T * 4);
   return w;
