@@ -600,21 +600,18 @@ __global__ void __launch_bounds__(kGroupThreads, 1) int8_group_kernel(const Grou
 }
 
 struct CombineParams {
-  const __half* y;           // [rows][H]: integer sums times down scale / (factor * norm)
+  const float* y;            // [rows][H]: integer sums times the channel's scale
   const float* h_scale;      // [rows]
-  const int* idx;
   const int* pos;            // grouped row of each choice, -1: none
   const float* weights;
-  const float* norms;        // [E]
   void* out;
   int T, k, H, out_dtype;
-  float factor;
 };
 
 constexpr int kCombineThreads = 256;
 
-// out[t] = sum_j weights[t, j] h_scale factor norm[e_j] y_j, eight channels a thread. Reading y bounds it:
-// 4,096 tokens, k = 8, H = 2,048: 31 us, 4.9 TB/s.
+// out[t] = sum_j weights[t, j] h_scale_j y_j, four channels a thread. Reading y bounds it: 4,096 tokens, k = 8,
+// H = 2,048: 45 us, 6 TB/s.
 __global__ void __launch_bounds__(kCombineThreads) int8_combine_kernel(const CombineParams p) {
   __shared__ float s_f[MOE_ROUTE_MAX_TOP_K];
   __shared__ int s_pos[MOE_ROUTE_MAX_TOP_K];
@@ -626,31 +623,25 @@ __global__ void __launch_bounds__(kCombineThreads) int8_combine_kernel(const Com
       const int64_t a = t * p.k + threadIdx.x;
       const int at = ldg_cg_s32(p.pos + a);
       s_pos[threadIdx.x] = at;
-      s_f[threadIdx.x] = at >= 0 ? __ldg(p.weights + a) * ldg_cg_f32(p.h_scale + at) *
-                                       (p.factor * ldg_cg_f32(p.norms + __ldg(p.idx + a))) : 0.f;
+      s_f[threadIdx.x] = at >= 0 ? __ldg(p.weights + a) * ldg_cg_f32(p.h_scale + at) : 0.f;
     }
     __syncthreads();
-    for (int c = threadIdx.x * 8; c < p.H; c += kCombineThreads * 8) {
-      float acc[8] = {};
+    for (int c = threadIdx.x * 4; c < p.H; c += kCombineThreads * 4) {
+      float acc[4] = {};
 #pragma unroll 8
       for (int j = 0; j < p.k; ++j) {
         const int at = s_pos[j];
         if (at < 0) continue;
         const float f = s_f[j];
         const uint4 y = ldg_cg(p.y + (int64_t)at * p.H + c);
-        const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&yw[i]));
-          acc[2 * i] += f * v.x;
-          acc[2 * i + 1] += f * v.y;
-        }
+        acc[0] += f * __uint_as_float(y.x);
+        acc[1] += f * __uint_as_float(y.y);
+        acc[2] += f * __uint_as_float(y.z);
+        acc[3] += f * __uint_as_float(y.w);
       }
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[i] = (uint32_t)to_16(p.out_dtype, acc[2 * i]) | ((uint32_t)to_16(p.out_dtype, acc[2 * i + 1]) << 16);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.H + c) = make_uint4(o[0], o[1], o[2], o[3]);
+      const uint32_t lo = (uint32_t)to_16(p.out_dtype, acc[0]) | ((uint32_t)to_16(p.out_dtype, acc[1]) << 16);
+      const uint32_t hi = (uint32_t)to_16(p.out_dtype, acc[2]) | ((uint32_t)to_16(p.out_dtype, acc[3]) << 16);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + t * p.H + c) = make_uint2(lo, hi);
     }
   }
 }
@@ -774,7 +765,7 @@ bool count_first(int64_t choices) { return choices > 32768; }
 
 // Scratch of the experts' call. y takes h's place, which is dead by then.
 struct ExpertsWorkspace {
-  int64_t h, q, x_scale, hq, h_scale, norms, chunk_counts, pos, blocks, counts, bytes;
+  int64_t h, q, x_scale, hq, h_scale, chunk_counts, pos, blocks, counts, bytes;
   int block, max_blocks, chunk, chunks;
 };
 ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T) {
@@ -794,12 +785,11 @@ ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T
   w.chunks = (int)((T + w.chunk - 1) / w.chunk);
   int64_t at = 0;
   const auto take = [&at](int64_t bytes) { const int64_t o = at; at += pad256(bytes); return o; };
-  w.h = take(rows * (I * 4 > H * 2 ? I * 4 : H * 2));
+  w.h = take(rows * (I > H ? I : H) * 4);
   w.q = take(rows * pad64(H) * 2);
   w.x_scale = take(rows * 4);
   w.hq = take(rows * pad64(I) * 2);
   w.h_scale = take(rows * 4);
-  w.norms = take((int64_t)c->num_experts * 4);
   w.chunk_counts = take(count_first(rows) ? (int64_t)w.chunks * c->num_experts * 4 : 0);
   w.pos = take(rows * 4);
   w.blocks = take((int64_t)w.max_blocks * 16);
@@ -854,10 +844,6 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   g.row_scale = a.scale;
   g.w_scale = p.gate_up_scale;
   g.out = ws + w.h;
-  g.norm_scales = p.down_scale;
-  g.norms = (float*)(ws + w.norms);
-  g.num_norms = p.E;
-  g.norm_row = p.H;
   e = launch_gemm(kUp, g, num_sms, s);
   if (e != cudaSuccess) return e;
 
@@ -873,13 +859,6 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   e = launch_prepare(b, MOE_DTYPE_F32, num_sms, s);
   if (e != cudaSuccess) return e;
 
-  // The down sums (at most 127 * 128 * I) fit f16 once divided by a power of two, and still do after their
-  // channel's scale over the expert's norm. The rounding to 11 bits is relative and far below that
-  // of a bf16 output, unless a channel's scale is some 2^-16 of its expert's largest: such a channel's
-  // values lose bits, which it adds next to nothing with. (Held as they are, and scaled in the weighted
-  // sum, each value took its 4-byte scale along there: 42 us of a call at T = 4096, Qwen-shaped.)
-  float factor = 1.f;
-  while (127.f * 128.f * (float)p.I > 65504.f * factor) factor *= 2.f;
   g.a = p.down;
   g.a_rows = (int64_t)p.E * p.H;
   g.a_stride = p.I;
@@ -891,23 +870,19 @@ cudaError_t launch_experts_tensor(const ExpertsParams& p, const moe_int8_experts
   g.rows_per_group = p.H;
   g.w_scale = p.down_scale;
   g.out = ws + w.h;
-  g.factor = 1.f / factor;
   e = launch_gemm(kDown, g, num_sms, s);
   if (e != cudaSuccess) return e;
 
   CombineParams c = {};
-  c.y = (const __half*)(ws + w.h);
+  c.y = (const float*)(ws + w.h);
   c.h_scale = b.scale;
-  c.idx = p.idx;
   c.pos = a.pos;
   c.weights = p.weights;
-  c.norms = g.norms;
   c.out = p.out;
   c.T = p.T;
   c.k = p.k;
   c.H = p.H;
   c.out_dtype = p.out_dtype;
-  c.factor = factor;
   return launch_pdl(int8_combine_kernel, dim3((unsigned)(p.T < num_sms * 8 ? p.T : num_sms * 8)), kCombineThreads, 0, s, c);
 }
 

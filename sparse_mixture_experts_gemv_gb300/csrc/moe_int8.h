@@ -8,7 +8,7 @@ namespace moe {
 namespace int8 {
 
 constexpr int kMaxBlock = 192;   // tokens of a tensor-core tile: two accumulators of so many columns
-                                 // and four operand slots fill tensor memory
+                                 // and two operand slots fill tensor memory
 
 enum GemmKind { kDense = 0, kUp = 1, kDown = 2 };
 
@@ -31,15 +31,8 @@ struct GemmArgs {
   int T;                      // dense: tokens
   const float* row_scale;     // dense, up: scale of each row of b
   const float* w_scale;       // dense: [N]; up: [E][2I]; down: [E][H]
-  void* out;                  // dense: [T][N] out_dtype; up: fp32 h [rows][I]; down: f16 y [rows][H]
-  int out_dtype;
-  // A power of two per expert, at least its largest down scale: found by the up product on the side,
-  // which reads scales [num_norms][norm_row] and writes norms; down multiplies its sums by
-  // factor * w_scale / norms, which keeps them in f16's range.
-  const float* norm_scales;
-  float* norms;
-  int num_norms, norm_row;
-  float factor;
+  void* out;                  // dense: [T][N] out_dtype; up: fp32 h [rows][I]; down: fp32 y [rows][H]
+  int out_dtype;              // dense
 };
 int device_sms();   // of the current device
 cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStream_t s);

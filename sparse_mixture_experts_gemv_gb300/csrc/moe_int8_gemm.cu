@@ -18,7 +18,7 @@
 //
 // One persistent CTA an SM, warp-specialised:
 //   warp 0        weights by TMA              warp 2  tokens by TMA
-//   warp 1        issues the MMAs             warp 3  up: the experts' largest down scales
+//   warp 1        issues the MMAs             warp 3  idle
 //   warps 4-11    converters: two groups of four, each half of a step's K
 //   warps 12-15   epilogue of the previous tile while the next one accumulates
 // A step is 128 of K: eight MMAs. What the issuing warp does between two steps (a wait,
@@ -27,8 +27,9 @@
 // Tensor memory: two accumulators of 192 columns, two operand slots of 64.
 //
 // GB300: dense 4,096 x 2,048 x 4,096 50 us (1.37 PFLOP/s, tensor pipe 56% busy); up and down products of
-// 32,768 choices of 256 experts (H 2,048, I 512) 147 and 84 us, 4.9 TB/s of memory traffic each, their epilogues
-// (SwiGLU; f16 sums) next: without those the two take some 50 us less together.
+// 32,768 choices of 256 experts (H 2,048, I 512) 148 and 98 us, 4.9 and 5.3 TB/s of memory traffic, their epilogues
+// next: without its one the down product takes 83. (Its sums were f16 once, 85 us: an output channel whose scales lie
+// far below its expert's largest lost them, and every output took 2^-11 of its terms along.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -74,10 +75,6 @@ struct Params {
   void* out;
   int out_dtype;
   int wide;                  // dense: 16-bit results whose rows are 16-byte aligned
-  const float* norm_scales;
-  float* norms;
-  int num_norms, norm_row;
-  float factor;
 };
 
 // A copy's issue costs about as much as 8 KB, so that every step is one copy of weights (up: two) and one
@@ -394,22 +391,11 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
         if (++es == p.b_stages) { es = 0; eph ^= 1; }
       }
     }
-  } else if (KIND == kUp && warp == 3) {
-    // ------------------------------------------- the experts' largest down scales
-    for (int e = blockIdx.x; e < p.num_norms; e += gridDim.x) {
-      uint32_t m = 0;
-      for (int i = lane; i < p.norm_row; i += 32)
-        m = max(m, __float_as_uint(__ldg(p.norm_scales + (int64_t)e * p.norm_row + i)) & 0x7FFFFFFFu);
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
-      // the next power of two; 1 where there is none in fp32's normal range
-      const uint32_t exponent = (m >> 23) + 1;
-      if (lane == 0) p.norms[e] = m >= 0x00800000u && exponent < 0xFE ? __uint_as_float(exponent << 23) : 1.f;
-    }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3;
     float* cs = s_scale + quad * kMaxBlock;   // the warp's copy of the tile's token scales
-    uint16_t* turn = s_turn + quad * 1024;    // 32 tokens x 32 channels
+    uint16_t* turn = s_turn + quad * 1024;    // 32 tokens x 32 channels of 16 bits, or 16 x 32 of fp32
     const bool f16_out = p.out_dtype == MOE_DTYPE_F16;
     uint32_t tc = 0;
     const auto channel = [&](const Tile& t) {
@@ -422,7 +408,6 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       a = ch < p.channels ? __ldg(w) : 0.f;
       b = 1.f;
       if (KIND == kUp && ch < p.channels) b = __ldg(w + p.channels);
-      if (KIND == kDown) b = ldg_cg_f32(p.norms + t.e);
     };
     Tile next = {};
     float next0 = 0.f, next1 = 1.f;
@@ -432,7 +417,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++tc) {
       const Tile t = next;
-      const float w0 = KIND == kDown ? next0 * (p.factor / next1) : next0, w1 = next1;
+      const float w0 = next0, w1 = next1;
       const uint32_t ab = tc & 1;
       __syncwarp();
       if (KIND != kDown) {
@@ -472,26 +457,38 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
             if (2 * i < limit) *dst = h[i];
             dst += 2 * p.channels;
           }
-        } else if (KIND == kDown || p.wide) {
+        } else if (KIND == kDown) {
+          // fp32, 16 tokens at a time turned in shared memory, so that a token's 32 channels leave in 16-byte
+          // pieces (stored as they are, 4 bytes a lane, 30 us more). The rows' scales wait for the weighted sum:
+          // their loads ahead of every tile took 36 us.
+          float* turn4 = reinterpret_cast<float*>(turn);
+          const int ch4 = t.mt * kChannels + quad * 32 + (lane & 7) * 4;
+#pragma unroll
+          for (int half = 0; half < 32; half += 16) {
+            if (half >= nc) break;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) turn4[i * 32 + lane] = __uint_as_float(v[half + i]) * w0;
+            __syncwarp();
+            float* dst = static_cast<float*>(p.out) + ((int64_t)t.row0 + c0 + half + (lane >> 3)) * p.channels + ch4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (ch4 < p.channels && half + 4 * i + (lane >> 3) < nc)
+                *reinterpret_cast<float4*>(dst + (int64_t)4 * i * p.channels) =
+                    *reinterpret_cast<const float4*>(turn4 + (4 * i + (lane >> 3)) * 32 + (lane & 7) * 4);
+            __syncwarp();
+          }
+        } else if (p.wide) {
           // 16-bit results: turned in shared memory, so that a token's 32 channels leave in 16-byte pieces
           // (stored as they are, 2 bytes a lane, a tile of 192 tokens took 26,000 cycles)
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            float f[4];
-            if (KIND == kDown) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(v[i + j]) * w0;
-            } else {
-              const float4 xs = *reinterpret_cast<const float4*>(cs + c0 + i);
-              f[0] = __uint_as_float(v[i]) * xs.x * w0;
-              f[1] = __uint_as_float(v[i + 1]) * xs.y * w0;
-              f[2] = __uint_as_float(v[i + 2]) * xs.z * w0;
-              f[3] = __uint_as_float(v[i + 3]) * xs.w * w0;
-            }
+            const float4 xs = *reinterpret_cast<const float4*>(cs + c0 + i);
+            const float f[4] = {__uint_as_float(v[i]) * xs.x * w0, __uint_as_float(v[i + 1]) * xs.y * w0,
+                                __uint_as_float(v[i + 2]) * xs.z * w0, __uint_as_float(v[i + 3]) * xs.w * w0};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              turn[(i + j) * 32 + lane] = KIND == kDown || f16_out ? __half_as_ushort(__float2half_rn(f[j]))
-                                                                   : __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));
+              turn[(i + j) * 32 + lane] = f16_out ? __half_as_ushort(__float2half_rn(f[j]))
+                                                  : __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));
           }
           __syncwarp();
           const int ch8 = t.mt * kChannels + quad * 32 + (lane & 3) * 8;
@@ -624,11 +621,6 @@ cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStrea
   p.out = a.out;
   p.out_dtype = a.out_dtype;
   p.wide = a.out_dtype != MOE_DTYPE_F32 && a.channels % 8 == 0 && !((uintptr_t)a.out & 15);
-  p.norm_scales = a.norm_scales;
-  p.norms = a.norms;
-  p.num_norms = a.num_norms;
-  p.norm_row = a.norm_row;
-  p.factor = a.factor;
   const size_t smem = (size_t)p.b_stages * p.b_bytes + (size_t)p.raw_stages * kRawBytes + kFixedSmem;
   const int64_t tiles = (int64_t)p.tiles_m * (kind == kDense ? p.tiles_t : a.max_blocks);
   const int grid = (int)(tiles < num_sms ? tiles : num_sms);
