@@ -430,7 +430,9 @@ typedef struct {
  * numbers are told apart however close they are, up to the rounding of 64 bits. A
  * logit of -inf or NaN turns its expert off for the token: it ranks below all
  * others, in order of index, with weight 0 (all weights are 0 where none is on);
- * +inf counts as the largest finite fp32 value. T == 0 is a no-op.
+ * +inf counts as the largest finite fp32 value. * A bias of NaN counts as -inf and one of +inf as the largest finite fp32 value: an
+ * expert whose bias is -inf ranks below all others too and adds nothing to its group's
+ * sum, but is on: chosen for want of others, it has its score's weight. T == 0 is a no-op.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (limits above), MOE_ERR_CUDA.
  */
 moe_status_t moe_route_experts(const moe_route_config_t* cfg, const void* logits_dev, int32_t logits_dtype,

@@ -20,13 +20,18 @@ def scores(row, score):
 
 
 def choose(row, k, score, bias=None, groups=1, top_groups=1, group_top=2):
+    """The k chosen experts. A bias of NaN counts as -inf, one of +inf as the largest finite fp32 value; a key of
+    -inf ranks below all others and adds nothing to its group."""
     x = np.asarray(row, dtype=np.float64)
+    if bias is not None:
+        bias = np.asarray(bias, np.float64)
+        bias = np.where(np.isnan(bias), -np.inf, np.minimum(bias, np.finfo(np.float32).max))
     E = len(x)
     s, on = scores(row, score)
     if bias is None and (groups == 1 or top_groups == groups):
         key = np.where(on, x, -np.inf)
     else:
-        key = np.where(on, s + (0.0 if bias is None else np.asarray(bias, np.float64)), -np.inf)
+        key = np.where(on, s + (0.0 if bias is None else bias), -np.inf)
     left = list(range(E))
     if groups > 1 and top_groups < groups:
         per = E // groups

@@ -8,6 +8,8 @@
 //   w[j]   = scale * s[idx[j]] (/ sum_i s[idx[i]])
 // A logit of -inf or NaN turns its expert off for the token: it ranks below every
 // expert that is on, and its weight is 0; +inf counts as the largest finite value.
+// A bias is read the same way, and so a key is a finite number or -inf, never NaN:
+// comparisons of keys, and differences of finite ones, always say something.
 //
 // One warp serves one token; lane l holds the NPL consecutive experts l * NPL ...
 // so that a row is read with 16-byte loads, a lower lane means a lower index, and
@@ -110,6 +112,12 @@ MOE_DEV void load_logits(const void* logits, int64_t row0, int E, int lane, floa
   }
 }
 
+// The bias of expert e: NaN as -inf, +inf as the largest finite value.
+MOE_DEV float load_bias(const float* bias, int e) {
+  const float b = __ldg(bias + e);
+  return isnan(b) ? -INFINITY : fminf(b, FLT_MAX);
+}
+
 MOE_DEV float warp_max(float v) {
   return f32_from_order_key(__reduce_max_sync(0xFFFFFFFFu, f32_order_key(v)));
 }
@@ -157,7 +165,7 @@ __device__ __noinline__ int route_exact(const RouteParams& p, int64_t t, bool ke
     const double v = keys[e];
     if (v == kNone) continue;
     const double u = exp(softmax ? v - top : -v);
-    keys[e] = (softmax ? u / sum : 1.0 / (1.0 + u)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+    keys[e] = (softmax ? u / sum : 1.0 / (1.0 + u)) + (p.bias ? (double)load_bias(p.bias, e) : 0.0);
   }
   __syncwarp();
   if (p.groups > 1) {
@@ -271,7 +279,7 @@ __device__ __noinline__ bool choose_groups_exactly(const RouteParams& p, int64_t
   if (lane < n) {
     const int e = list[lane];
     const float v = fminf(load_one<DT>(p.logits, t * p.stride + e), FLT_MAX);
-    key = 1.0 / (1.0 + exp(-(double)v)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+    key = 1.0 / (1.0 + exp(-(double)v)) + (p.bias ? (double)load_bias(p.bias, e) : 0.0);
     g = e / p.per;
   }
   int rank = 0;
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
   if (KEYED) {
     for (int i = threadIdx.x; i < 32 * NPL; i += 32 * kRouteWarps) {
       const int e = (i / kVec & 31) * NPL + i / (32 * kVec) * kVec + i % kVec;
-      s_bias[i] = e >= p.E ? -INFINITY : p.bias ? __ldg(p.bias + e) : 0.f;   // -inf: never among the chosen
+      s_bias[i] = e >= p.E ? -INFINITY : p.bias ? load_bias(p.bias, e) : 0.f;   // past E: never chosen
     }
     __syncthreads();
     for (int i = lane; i < 32 * NPL; i += 32)
@@ -419,8 +427,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(cons
             a = fmaxf(a, v);
           }
       }
-      // an expert that is off adds nothing
-      const float score = p.group_top == 2 && b != -INFINITY ? a + b : a;
+      // a key of -inf adds nothing; two of the largest or lowest values leave no infinity, whose differences
+      // from another are none
+      const float score = p.group_top == 2 && b != -INFINITY ? fminf(fmaxf(a + b, -FLT_MAX), FLT_MAX) : a;
       bool close;
       uint32_t kept = choose_groups(p, score, near, lane, close);
       if (close) {

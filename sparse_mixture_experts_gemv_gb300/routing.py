@@ -75,7 +75,8 @@ def route_experts(logits: torch.Tensor, k: int, score: str = "softmax", bias: to
     (a bias for balance). groups > 1: consecutive experts form groups; the top_groups groups
     whose group_top (1 or 2) largest keys add up to most stay. The weights are the scores
     without the bias, divided by their sum if renormalise, times scale. Equal keys go by the
-    lower index; a logit of -inf or NaN turns its expert off for the row.
+    lower index; a logit of -inf or NaN turns its expert off for the row. A bias of
+    -inf or NaN ranks its expert below all others in every row, one of +inf above them.
 
     Returns (idx int32 [T, k], weights fp32 [T, k]), in descending order of the keys. The
     weights are differentiable with respect to the logits.
