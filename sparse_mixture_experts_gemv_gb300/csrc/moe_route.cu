@@ -20,6 +20,7 @@
 // the logit), so the choice is exact. Otherwise scores are computed in 32 bits,
 // and a choice is kept only if the keys it separates are further apart than the
 // 32-bit errors can reach; where a pair is closer, the keys are taken in 64 bits.
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -568,11 +569,15 @@ struct RouteBackParams {
   float scale;
 };
 
+// Rounded to 16 bits, to nearest even; a NaN stays one.
+template <int DT>
+MOE_DEV uint32_t to_half(float v) {
+  return DT == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
 template <int DT>
 MOE_DEV void store_one(void* p, int64_t i, float v) {
   if (DT == MOE_DTYPE_F32) static_cast<float*>(p)[i] = v;
-  else if (DT == MOE_DTYPE_BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16_rne(v);
-  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+  else static_cast<uint16_t*>(p)[i] = (uint16_t)to_half<DT>(v);
 }
 
 template <int DT, int NPL, bool VEC>
@@ -643,11 +648,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_backward_kernel(con
           if (DT == MOE_DTYPE_F32) {
             w[i] = __float_as_uint(row[4 * c + i]);
           } else {
-            const float lo = row[8 * c + 2 * i], hi = row[8 * c + 2 * i + 1];
-            w[i] = DT == MOE_DTYPE_BF16
-                       ? (uint32_t)f32_to_bf16_rne(lo) | ((uint32_t)f32_to_bf16_rne(hi) << 16)
-                       : (uint32_t)__half_as_ushort(__float2half_rn(lo)) |
-                             ((uint32_t)__half_as_ushort(__float2half_rn(hi)) << 16);
+            w[i] = to_half<DT>(row[8 * c + 2 * i]) | (to_half<DT>(row[8 * c + 2 * i + 1]) << 16);
           }
         }
         dst[c] = make_uint4(w[0], w[1], w[2], w[3]);

@@ -1,0 +1,31 @@
+"""What the gradient of route_experts does at its edges: values that are not finite come through."""
+import pytest
+
+from test_gpu_route_experts import DT, _make
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("E", [64, 33])      # rows in 16-byte pieces, and not
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_gradients_that_are_not_finite_come_through(dtype, E, score, renormalise):
+    import sparse_mixture_experts_gemv_gb300 as M
+    x = _make(6, E, dtype, 3)
+    idx, _ = M.route_experts(x, 4, score=score, renormalise=renormalise)
+    d = torch.randn(6, 4, generator=torch.Generator().manual_seed(1)).cuda()
+    want = M.route_experts_backward(d, x, idx, score, renormalise)
+    d[1, 2], d[4, 0], d[5, 3] = NAN, INF, -INF
+    got = M.route_experts_backward(d, x, idx, score, renormalise)
+    assert torch.equal(got[[0, 2, 3]], want[[0, 2, 3]])
+    # with a sum over the row's gradients all of its chosen take the value on, else the one alone
+    sums = renormalise or score == "softmax"
+    for t, j in ((1, 2), (4, 0), (5, 3)):
+        at = idx[t].long() if sums else idx[t, j:j + 1].long()
+        assert not torch.isfinite(got[t, at]).any(), (t, got[t, at])
+        assert torch.isnan(got[t, idx[t, j].long()]) == (sums or t == 1)
