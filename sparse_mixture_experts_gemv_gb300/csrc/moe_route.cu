@@ -624,8 +624,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_backward_kernel(con
       for (int q = 1; q < NPL; ++q) m = fmaxf(m, x[q]);
       m = warp_max(m);
       z = 0.f;
+      uint32_t off = 0u;   // they get 0 whatever the others' sum is
 #pragma unroll
       for (int q = 0; q < NPL; ++q) {
+        off |= x[q] == -INFINITY ? 1u << q : 0u;
         x[q] = x[q] == -INFINITY ? 0.f : expf(x[q] - m);
         z += x[q];
       }
@@ -634,7 +636,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_backward_kernel(con
 #pragma unroll
       for (int q = 0; q < NPL; ++q) {
         const int i = lane * NPL + q;
-        if (i < p.E) row[i] = z > 0.f ? x[q] / z * (row[i] - dot) : 0.f;
+        if (i < p.E) row[i] = off >> q & 1u ? 0.f : x[q] / z * (row[i] - dot);
       }
       __syncwarp();
     }

@@ -29,3 +29,22 @@ def test_gradients_that_are_not_finite_come_through(dtype, E, score, renormalise
         at = idx[t].long() if sums else idx[t, j:j + 1].long()
         assert not torch.isfinite(got[t, at]).any(), (t, got[t, at])
         assert torch.isnan(got[t, idx[t, j].long()]) == (sums or t == 1)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("E", [64, 33])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_experts_that_are_off_have_no_gradient_whatever_the_others_have(dtype, E, score, renormalise):
+    import sparse_mixture_experts_gemv_gb300 as M
+    x = _make(4, E, dtype, 5)
+    x[:, ::3] = -INF
+    x[2, 1] = NAN
+    x[3, 2:] = -INF                  # fewer on than chosen
+    idx, _ = M.route_experts(x, 4, score=score, renormalise=renormalise)
+    d = torch.randn(4, 4, generator=torch.Generator().manual_seed(1)).cuda()
+    d[0, 1], d[1, 0], d[2, 2], d[3, 0] = NAN, INF, NAN, NAN
+    got = M.route_experts_backward(d, x, idx, score, renormalise)
+    off = torch.isnan(x) | (x == -INF)
+    assert (got[off] == 0).all()
+    assert not torch.isfinite(got[~off]).all()
