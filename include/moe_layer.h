@@ -398,7 +398,7 @@ void moe_lmhead_destroy(moe_lmhead_t* head);
  * Routing to experts from given logits, and experts and projections in 8-bit
  * integers. These calls keep no state: the caller passes every buffer, and the
  * ones that need scratch say how much. Nothing allocates or synchronises; work is
- * enqueued on `stream`. (The pages name no such interface; it is this library's own.)
+ * enqueued on `stream`, which belongs to the current device, as every buffer does. (The pages name no such interface; it is this library's own.)
  * ------------------------------------------------------------------------ */
 typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_S8 = 3 } moe_dtype_t;
 

@@ -37,7 +37,21 @@ def current_stream(device) -> int:
     return _current(device.index)
 
 
-def run_on(stream, fn, *args, **kw):
-    """fn(*args) with `stream` as the current one, so that what it allocates belongs to that stream."""
+_device = torch._C._cuda_getDevice   # the current device's index, likewise
+
+
+def elsewhere(t) -> bool:
+    """Whether the tensor is on another device than the current one, on which a kernel would start."""
+    return t.is_cuda and t.get_device() != _device()
+
+
+def run_on(stream, fn, first, *args):
+    """fn(first, *args) on the device of the tensor `first`, with `stream` as the current one, so that what it
+    allocates belongs to that stream; None: the device's own current stream."""
+    if stream is None:
+        with torch.cuda.device(first.device):
+            return fn(first, *args)
+    if first.is_cuda and stream.device != first.device:
+        invalid(fn.__name__, f"the stream is on {stream.device}, the tensors are on {first.device}")
     with torch.cuda.stream(stream):
-        return fn(*args, **kw)
+        return fn(first, *args)

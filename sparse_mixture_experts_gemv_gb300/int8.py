@@ -8,7 +8,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import DTYPE_CODES, check, current_stream, invalid, run_on, vector, want
+from ._tensors import DTYPE_CODES, check, current_stream, elsewhere, invalid, run_on, vector, want
 
 
 @functools.lru_cache(maxsize=256)
@@ -47,7 +47,7 @@ def int8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale
     16. Rows may be apart (any stride(0)); rows off 16-byte boundaries are copied first.
     out_dtype: bf16, fp16 or fp32; by default x's, and bf16 for int8 x.
     """
-    if stream is not None:
+    if stream is not None or elsewhere(x):
         return run_on(stream, int8_matmul, x, w, w_scale, x_scale, out_dtype)
     what = "int8_matmul"
     code = DTYPE_CODES.get(x.dtype)
@@ -95,7 +95,7 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
     these four without gaps and on 16-byte boundaries. H and I are multiples of 16. x and the
     SwiGLU outputs are quantized for each token as in int8_matmul. Returns [T, H] in x's type.
     """
-    if stream is not None:
+    if stream is not None or elsewhere(x):
         return run_on(stream, int8_experts, x, idx, weights, gate_up, gate_up_scale, down, down_scale)
     what = "int8_experts"
     if not x.is_cuda or x.dim() != 2 or (x.dtype is not torch.bfloat16 and x.dtype is not torch.float16):
@@ -140,5 +140,7 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
 
 
 def int8_sync_status(stream: torch.cuda.Stream = None) -> int:
-    """Waits for the stream; MOE_OK, or MOE_ERR_TIMEOUT if a product's bounded wait ran out since the last call."""
-    return N.load().moe_quant_sync_status((stream or torch.cuda.current_stream()).cuda_stream)
+    """Waits for the stream; MOE_OK, or MOE_ERR_TIMEOUT if a product's bounded wait ran out on its device since the last call."""
+    stream = stream or torch.cuda.current_stream()
+    with torch.cuda.device(stream.device):
+        return N.load().moe_quant_sync_status(stream.cuda_stream)

@@ -9,7 +9,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import DTYPE_CODES, check, current_stream, invalid, run_on, vector, want
+from ._tensors import DTYPE_CODES, check, current_stream, elsewhere, invalid, run_on, vector, want
 
 LOGIT_CODES = {t: c for t, c in DTYPE_CODES.items() if t is not torch.int8}
 SCORES = {"softmax": N.MOE_SCORE_SOFTMAX, "sigmoid": N.MOE_SCORE_SIGMOID}
@@ -84,7 +84,7 @@ def route_experts(logits: torch.Tensor, k: int, score: str = "softmax", bias: to
     if top_groups is None:
         top_groups = groups
     args = (logits, k, score, bias, groups, top_groups, group_top, renormalise, scale)
-    if stream is not None:
+    if stream is not None or elsewhere(logits):
         return run_on(stream, route_experts, *args)
     if logits.requires_grad and torch.is_grad_enabled():
         return _RouteExperts.apply(*args)
@@ -95,7 +95,7 @@ def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, idx: t
                            renormalise: bool = True, scale: float = 1.0, stream: torch.cuda.Stream = None):
     """d_logits [T, E] in the logits' type from d_weights fp32 [T, k], with the idx that
     route_experts returned for these logits and the same score, renormalise and scale."""
-    if stream is not None:
+    if stream is not None or elsewhere(d_weights):
         return run_on(stream, route_experts_backward, d_weights, logits, idx, score, renormalise, scale)
     what = "route_experts_backward"
     logits, code, T, E, stride = _logits(what, logits)

@@ -1,0 +1,81 @@
+"""What the calls on torch tensors do before anything reaches a device, with stand-ins for the tensors and the
+current device: the tensors' own device becomes the current one, a stream of another device is refused."""
+import contextlib
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Stand:
+    """A CUDA tensor as far as the calls look before they run anything."""
+
+    is_cuda, requires_grad = True, False
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.device.index
+
+
+class Entered(Exception):
+    pass
+
+
+CALLS = {"route_experts": lambda M, t, **kw: M.route_experts(t, 2, **kw),
+         "route_experts_backward": lambda M, t, **kw: M.route_experts_backward(t, t, t, **kw),
+         "int8_matmul": lambda M, t, **kw: M.int8_matmul(t, t, t, **kw),
+         "int8_experts": lambda M, t, **kw: M.int8_experts(t, t, t, t, t, t, t, **kw)}
+
+
+def _switch_to(where):
+    def guard(device):
+        raise Entered(where, device)
+    return guard
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_the_tensors_device_becomes_the_current_one(call, monkeypatch):
+    import sparse_mixture_experts_gemv_gb300 as M
+    from sparse_mixture_experts_gemv_gb300 import _tensors
+    monkeypatch.setattr(_tensors, "_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", _switch_to("device"))
+    with pytest.raises(Entered) as e:
+        CALLS[call](M, Stand(1))
+    assert e.value.args == ("device", torch.device("cuda", 1))
+    with pytest.raises(AttributeError):      # on the current one it goes on at once, to what a stand-in has not
+        CALLS[call](M, Stand(0))
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_a_stream_of_another_device_is_refused(call, monkeypatch):
+    import sparse_mixture_experts_gemv_gb300 as M
+    from sparse_mixture_experts_gemv_gb300 import _tensors
+    monkeypatch.setattr(_tensors, "_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "stream", _switch_to("stream"))
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream"):
+        CALLS[call](M, Stand(0), stream=stream)
+    with pytest.raises(Entered) as e:
+        CALLS[call](M, Stand(1), stream=stream)
+    assert e.value.args == ("stream", stream)
+
+
+def test_the_status_is_read_on_the_streams_device(monkeypatch):
+    import sparse_mixture_experts_gemv_gb300 as M
+    from sparse_mixture_experts_gemv_gb300 import int8
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d.index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    lib = types.SimpleNamespace(moe_quant_sync_status=lambda s: seen.append((s, current[0])) or 0)
+    monkeypatch.setattr(int8.N, "load", lambda: lib)
+    assert M.int8_sync_status(types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=77)) == 0
+    assert seen == [(77, 1)] and current == [0]
