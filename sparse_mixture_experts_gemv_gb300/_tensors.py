@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native as N
 
@@ -35,6 +36,14 @@ _current = torch._C._cuda_getCurrentRawStream   # the current stream's handle wi
 
 def current_stream(device) -> int:
     return _current(device.index)
+
+
+def refuse_tangents(what: str, *tensors):
+    """Forward-mode derivatives: there are none, and a tangent is not dropped without a word."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                invalid(what, "has no forward-mode derivative, and an input has a tangent")
 
 
 _device = torch._C._cuda_getDevice   # the current device's index, likewise

@@ -9,7 +9,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import DTYPE_CODES, check, current_stream, elsewhere, invalid, run_on, vector, want
+from ._tensors import DTYPE_CODES, check, current_stream, elsewhere, invalid, refuse_tangents, run_on, vector, want
 
 LOGIT_CODES = {t: c for t, c in DTYPE_CODES.items() if t is not torch.int8}
 SCORES = {"softmax": N.MOE_SCORE_SOFTMAX, "sigmoid": N.MOE_SCORE_SIGMOID}
@@ -50,53 +50,7 @@ def _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise,
     return idx, weights
 
 
-class _RouteExperts(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, k, score, bias, groups, top_groups, group_top, renormalise, scale):
-        idx, weights = _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise, scale)
-        ctx.save_for_backward(logits, idx)
-        ctx.how = (score, renormalise, scale)
-        ctx.mark_non_differentiable(idx)
-        return idx, weights
-
-    @staticmethod
-    def backward(ctx, _, d_weights):
-        logits, idx = ctx.saved_tensors
-        d_logits = route_experts_backward(d_weights, logits, idx, *ctx.how)
-        return (d_logits,) + (None,) * 8
-
-
-def route_experts(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tensor = None, groups: int = 1,
-                  top_groups: int = None, group_top: int = 2, renormalise: bool = True, scale: float = 1.0,
-                  stream: torch.cuda.Stream = None):
-    """Chooses k experts for each row of logits [T, E] (fp32, bf16 or fp16).
-
-    score: "softmax" or "sigmoid". bias: fp32 [E], added to the scores for the choice alone
-    (a bias for balance). groups > 1: consecutive experts form groups; the top_groups groups
-    whose group_top (1 or 2) largest keys add up to most stay. The weights are the scores
-    without the bias, divided by their sum if renormalise, times scale. Equal keys go by the
-    lower index; a logit of -inf or NaN turns its expert off for the row. A bias of
-    -inf or NaN ranks its expert below all others in every row, one of +inf above them.
-
-    Returns (idx int32 [T, k], weights fp32 [T, k]), in descending order of the keys. The
-    weights are differentiable with respect to the logits.
-    """
-    if top_groups is None:
-        top_groups = groups
-    args = (logits, k, score, bias, groups, top_groups, group_top, renormalise, scale)
-    if stream is not None or elsewhere(logits):
-        return run_on(stream, route_experts, *args)
-    if logits.requires_grad and torch.is_grad_enabled():
-        return _RouteExperts.apply(*args)
-    return _forward(*args)
-
-
-def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, idx: torch.Tensor, score: str = "softmax",
-                           renormalise: bool = True, scale: float = 1.0, stream: torch.cuda.Stream = None):
-    """d_logits [T, E] in the logits' type from d_weights fp32 [T, k], with the idx that
-    route_experts returned for these logits and the same score, renormalise and scale."""
-    if stream is not None or elsewhere(d_weights):
-        return run_on(stream, route_experts_backward, d_weights, logits, idx, score, renormalise, scale)
+def _backward(d_weights, logits, idx, score, renormalise, scale):
     what = "route_experts_backward"
     logits, code, T, E, stride = _logits(what, logits)
     dev = logits.device
@@ -112,3 +66,71 @@ def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, idx: t
                                               idx.data_ptr(), d_weights.data_ptr(), T, d_logits.data_ptr(),
                                               current_stream(dev)), "moe_route_experts_backward")
     return d_logits
+
+
+class _RouteExperts(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, score, bias, groups, top_groups, group_top, renormalise, scale):
+        idx, weights = _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise, scale)
+        ctx.save_for_backward(logits, idx)
+        ctx.how = (score, renormalise, scale)
+        ctx.mark_non_differentiable(idx)
+        return idx, weights
+
+    @staticmethod
+    def backward(ctx, _, d_weights):
+        logits, idx = ctx.saved_tensors
+        return (route_experts_backward(d_weights, logits, idx, *ctx.how),) + (None,) * 8
+
+
+class _RouteGradient(torch.autograd.Function):
+    """The gradient as a step of a recorded graph: it has no derivative of its own, and says so when asked for one."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return _backward(*args)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("route_experts has no second derivative")
+
+
+def route_experts(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tensor = None, groups: int = 1,
+                  top_groups: int = None, group_top: int = 2, renormalise: bool = True, scale: float = 1.0,
+                  stream: torch.cuda.Stream = None):
+    """Chooses k experts for each row of logits [T, E] (fp32, bf16 or fp16).
+
+    score: "softmax" or "sigmoid". bias: fp32 [E], added to the scores for the choice alone
+    (a bias for balance). groups > 1: consecutive experts form groups; the top_groups groups
+    whose group_top (1 or 2) largest keys add up to most stay. The weights are the scores
+    without the bias, divided by their sum if renormalise, times scale. Equal keys go by the
+    lower index; a logit of -inf or NaN turns its expert off for the row. A bias of
+    -inf or NaN ranks its expert below all others in every row, one of +inf above them.
+
+    Returns (idx int32 [T, k], weights fp32 [T, k]), in descending order of the keys. The
+    weights are differentiable with respect to the logits, once: a second derivative is
+    refused when it is asked for, a forward-mode one at once.
+    """
+    if top_groups is None:
+        top_groups = groups
+    args = (logits, k, score, bias, groups, top_groups, group_top, renormalise, scale)
+    if stream is not None or elsewhere(logits):
+        return run_on(stream, route_experts, *args)
+    refuse_tangents("route_experts", logits)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _RouteExperts.apply(*args)
+    return _forward(*args)
+
+
+def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, idx: torch.Tensor, score: str = "softmax",
+                           renormalise: bool = True, scale: float = 1.0, stream: torch.cuda.Stream = None):
+    """d_logits [T, E] in the logits' type from d_weights fp32 [T, k], with the idx that
+    route_experts returned for these logits and the same score, renormalise and scale. It has
+    no derivative itself, and refuses one when it is asked for."""
+    if stream is not None or elsewhere(d_weights):
+        return run_on(stream, route_experts_backward, d_weights, logits, idx, score, renormalise, scale)
+    refuse_tangents("route_experts_backward", d_weights, logits)
+    args = (d_weights, logits, idx, score, renormalise, scale)
+    if torch.is_grad_enabled() and (d_weights.requires_grad or logits.requires_grad):
+        return _RouteGradient.apply(*args)
+    return _backward(*args)

@@ -1,4 +1,5 @@
-"""What the gradient of route_experts does at its edges: values that are not finite come through."""
+"""What the gradient of route_experts does at its edges: values that are not finite come through, and derivatives
+that there are none of are refused and not left out."""
 import pytest
 
 from test_gpu_route_experts import DT, _make
@@ -48,3 +49,48 @@ def test_experts_that_are_off_have_no_gradient_whatever_the_others_have(dtype, E
     off = torch.isnan(x) | (x == -INF)
     assert (got[off] == 0).all()
     assert not torch.isfinite(got[~off]).all()
+
+
+def test_a_second_derivative_is_refused():
+    import sparse_mixture_experts_gemv_gb300 as M
+    for loss in (lambda w: (w * w).sum(), lambda w: w[:, 0].sum()):     # gradients that depend on w, and do not
+        x = _make(5, 16, "fp32", 2).requires_grad_()
+        _, w = M.route_experts(x, 3, score="sigmoid")
+        g, = torch.autograd.grad(loss(w), x, create_graph=True)
+        assert g.requires_grad
+        with pytest.raises(RuntimeError, match="second derivative"):
+            ((g * g).sum() + (x * x).sum()).backward()
+    x = _make(5, 16, "fp32", 2).requires_grad_()
+    _, w = M.route_experts(x, 3, score="sigmoid")
+    want, = torch.autograd.grad((w * w).sum(), x, retain_graph=True)
+    got, = torch.autograd.grad((w * w).sum(), x, create_graph=True)
+    assert torch.equal(want, got.detach()) and not want.requires_grad
+
+
+def test_the_gradients_own_call_is_refused_the_same_way():
+    import sparse_mixture_experts_gemv_gb300 as M
+    x, d = _make(5, 16, "fp32", 2), torch.ones(5, 3, device="cuda")
+    idx, _ = M.route_experts(x, 3)
+    want = M.route_experts_backward(d, x, idx)
+    assert not want.requires_grad
+    for a, b in ((x.clone().requires_grad_(), d), (x, d.clone().requires_grad_())):
+        got = M.route_experts_backward(b, a, idx)
+        assert torch.equal(got.detach(), want)
+        with pytest.raises(RuntimeError, match="second derivative"):
+            got.sum().backward()
+        with torch.no_grad():
+            assert not M.route_experts_backward(b, a, idx).requires_grad
+
+
+def test_tangents_are_refused():
+    import sparse_mixture_experts_gemv_gb300 as M
+    from torch.autograd import forward_ad
+    x, d = _make(5, 16, "fp32", 2), torch.ones(5, 3, device="cuda")
+    idx, w = M.route_experts(x, 3)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        with pytest.raises(ValueError, match="tangent"):
+            M.route_experts(dual, 3)
+        with pytest.raises(ValueError, match="tangent"):
+            M.route_experts_backward(d, dual, idx)
+        assert torch.equal(M.route_experts(x, 3)[1], w)      # without one all is as ever

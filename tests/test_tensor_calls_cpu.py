@@ -79,3 +79,14 @@ def test_the_status_is_read_on_the_streams_device(monkeypatch):
     monkeypatch.setattr(int8.N, "load", lambda: lib)
     assert M.int8_sync_status(types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=77)) == 0
     assert seen == [(77, 1)] and current == [0]
+
+
+def test_tangents_are_refused():
+    from torch.autograd import forward_ad
+    from sparse_mixture_experts_gemv_gb300 import _tensors
+    x = torch.ones(3)
+    _tensors.refuse_tangents("call", x, None)
+    with forward_ad.dual_level():
+        _tensors.refuse_tangents("call", x, None)
+        with pytest.raises(ValueError, match="tangent"):
+            _tensors.refuse_tangents("call", x, None, forward_ad.make_dual(x, x))
