@@ -46,6 +46,15 @@ def refuse_tangents(what: str, *tensors):
                 invalid(what, "has no forward-mode derivative, and an input has a tangent")
 
 
+def refuse_gradients(what: str, *tensors):
+    """The call has no gradient: an input that records one would lose it without a word."""
+    refuse_tangents(what, *tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                invalid(what, "has no gradient, and an input requires one: detach it, or call under torch.no_grad()")
+
+
 _device = torch._C._cuda_getDevice   # the current device's index, likewise
 
 

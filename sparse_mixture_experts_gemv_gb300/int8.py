@@ -8,7 +8,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import DTYPE_CODES, check, current_stream, elsewhere, invalid, run_on, vector, want
+from ._tensors import DTYPE_CODES, check, current_stream, elsewhere, invalid, refuse_gradients, run_on, vector, want
 
 
 @functools.lru_cache(maxsize=256)
@@ -45,11 +45,13 @@ def int8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale
     fp32 without: each row is then quantized by the call to its largest magnitude / 127, to
     the nearest whole number (a row with an infinity or a NaN gives NaN). K is a multiple of
     16. Rows may be apart (any stride(0)); rows off 16-byte boundaries are copied first.
-    out_dtype: bf16, fp16 or fp32; by default x's, and bf16 for int8 x.
+    out_dtype: bf16, fp16 or fp32; by default x's, and bf16 for int8 x. There is no gradient:
+    inputs that require one are refused while gradients are recorded.
     """
     if stream is not None or elsewhere(x):
         return run_on(stream, int8_matmul, x, w, w_scale, x_scale, out_dtype)
     what = "int8_matmul"
+    refuse_gradients(what, x, w_scale, x_scale)
     code = DTYPE_CODES.get(x.dtype)
     if code is None or not x.is_cuda or x.dim() != 2:
         invalid(what, "x must be a CUDA tensor [T, K] of int8, bf16, fp16 or fp32")
@@ -94,10 +96,13 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
     rows, gate_up_scale fp32 [E, 2I]; down: int8 [E, H, I], down_scale fp32 [E, H];
     these four without gaps and on 16-byte boundaries. H and I are multiples of 16. x and the
     SwiGLU outputs are quantized for each token as in int8_matmul. Returns [T, H] in x's type.
+    There is no gradient: inputs that require one, weights with a router's graph among them,
+    are refused while gradients are recorded.
     """
     if stream is not None or elsewhere(x):
         return run_on(stream, int8_experts, x, idx, weights, gate_up, gate_up_scale, down, down_scale)
     what = "int8_experts"
+    refuse_gradients(what, x, weights, gate_up_scale, down_scale)
     if not x.is_cuda or x.dim() != 2 or (x.dtype is not torch.bfloat16 and x.dtype is not torch.float16):
         invalid(what, "x must be a CUDA tensor [T, H] of bf16 or fp16")
     T, H = x.shape

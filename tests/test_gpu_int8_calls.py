@@ -1,0 +1,38 @@
+"""int8_matmul and int8_experts: what they refuse, and the sizes at the ends of their ranges."""
+import pytest
+
+from test_gpu_int8 import _choices, _experts, _ints, _scales, _x
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.mark.parametrize("T", [2, 40])
+def test_inputs_that_record_a_gradient_are_refused(T):
+    """Neither call has one: an output without a graph would train nothing, and say nothing."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    x, w, ws = _x(T, 64, "bf16"), _ints(8, 64), _scales(8)
+    q, qs = _ints(T, 64), _scales(T)
+    (idx, weights), ex = _choices(T, 8, 2), _experts(8, 64, 32)
+    xe = _x(T, 64, "bf16")
+
+    def leaf(t):
+        return t.clone().requires_grad_()
+
+    calls = [lambda: M.int8_matmul(leaf(x), w, ws), lambda: M.int8_matmul(x, w, leaf(ws)),
+             lambda: M.int8_matmul(q, w, ws, leaf(qs)), lambda: M.int8_experts(leaf(xe), idx, weights, *ex),
+             lambda: M.int8_experts(xe, idx, leaf(weights), *ex),
+             lambda: M.int8_experts(xe, idx, weights, ex[0], leaf(ex[1]), *ex[2:]),
+             lambda: M.int8_experts(xe, idx, weights, *ex[:3], leaf(ex[3]))]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad():
+            assert not call().requires_grad
+    from torch.autograd import forward_ad
+    with forward_ad.dual_level():
+        with pytest.raises(ValueError, match="tangent"):
+            M.int8_matmul(forward_ad.make_dual(x, torch.ones_like(x)), w, ws)
+        with pytest.raises(ValueError, match="tangent"):
+            M.int8_experts(xe, idx, forward_ad.make_dual(weights, torch.ones_like(weights)), *ex)

@@ -90,3 +90,26 @@ def test_tangents_are_refused():
         _tensors.refuse_tangents("call", x, None)
         with pytest.raises(ValueError, match="tangent"):
             _tensors.refuse_tangents("call", x, None, forward_ad.make_dual(x, x))
+
+
+def test_inputs_that_record_a_gradient_are_refused():
+    from sparse_mixture_experts_gemv_gb300 import _tensors
+    x, leaf = torch.ones(3), torch.ones(3, requires_grad=True)
+    _tensors.refuse_gradients("call", x, None)
+    for t in (leaf, leaf * 2):
+        with pytest.raises(ValueError, match="gradient"):
+            _tensors.refuse_gradients("call", x, None, t)
+        with torch.no_grad():
+            _tensors.refuse_gradients("call", x, None, t)
+    _tensors.refuse_gradients("call", leaf.detach())
+
+
+def test_the_products_refuse_before_they_look_at_types():
+    import sparse_mixture_experts_gemv_gb300 as M
+    x, leaf = torch.ones(2, 16), torch.ones(2, 16, requires_grad=True)
+    for args in ((leaf, x, x), (x, x, leaf), (x, x, x, leaf)):
+        with pytest.raises(ValueError, match="gradient"):
+            M.int8_matmul(*args)
+    for at in (0, 2, 4, 6):
+        with pytest.raises(ValueError, match="gradient"):
+            M.int8_experts(*[leaf if i == at else x for i in range(7)])
