@@ -65,11 +65,21 @@ def elsewhere(t) -> bool:
 
 def run_on(stream, fn, first, *args):
     """fn(first, *args) on the device of the tensor `first`, with `stream` as the current one, so that what it
-    allocates belongs to that stream; None: the device's own current stream."""
+    allocates belongs to that stream; None: the device's own current stream. The allocator learns that the
+    inputs are in use on `stream`, and the outputs on the caller's: a tensor freed after the call is not handed
+    out again before both are done with it. (What comes first on which stream stays the caller's business.)"""
     if stream is None:
         with torch.cuda.device(first.device):
             return fn(first, *args)
     if first.is_cuda and stream.device != first.device:
         invalid(fn.__name__, f"the stream is on {stream.device}, the tensors are on {first.device}")
+    caller = torch.cuda.current_stream(first.device) if first.is_cuda else stream
     with torch.cuda.stream(stream):
-        return fn(first, *args)
+        out = fn(first, *args)
+    if caller != stream:
+        for t in (first, *args):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+        for t in out if isinstance(out, tuple) else (out,):
+            t.record_stream(caller)
+    return out

@@ -36,3 +36,24 @@ def test_inputs_that_record_a_gradient_are_refused(T):
             M.int8_matmul(forward_ad.make_dual(x, torch.ones_like(x)), w, ws)
         with pytest.raises(ValueError, match="tangent"):
             M.int8_experts(xe, idx, forward_ad.make_dual(weights, torch.ones_like(weights)), *ex)
+
+
+def test_tensors_freed_after_a_call_on_another_stream_are_not_handed_out_again():
+    """Neither an input nor an output of a call on another stream is given to someone else while it is in use."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    w, ws = _ints(64, 4096), _scales(64)
+    s = torch.cuda.Stream()
+    x = _x(64, 4096, "fp32")
+    at, keep = x.data_ptr(), x.clone()
+    M.int8_matmul(x, w, ws, stream=s)        # loads the kernels, which may wait for the GPU
+    torch.full((64, 4096), 3.0, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)       # the call below waits behind this, some 0.2 s
+    out = M.int8_matmul(x, w, ws, stream=s)
+    del x
+    again = [torch.full((64, 4096), 3.0, device="cuda") for _ in range(3)]
+    assert not s.query()
+    assert at not in [t.data_ptr() for t in again]
+    s.synchronize()
+    assert torch.equal(out, M.int8_matmul(keep, w, ws))

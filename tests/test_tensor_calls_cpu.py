@@ -55,6 +55,7 @@ def test_a_stream_of_another_device_is_refused(call, monkeypatch):
     from sparse_mixture_experts_gemv_gb300 import _tensors
     monkeypatch.setattr(_tensors, "_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "stream", _switch_to("stream"))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: None)
     stream = types.SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream"):
         CALLS[call](M, Stand(0), stream=stream)
@@ -113,3 +114,23 @@ def test_the_products_refuse_before_they_look_at_types():
     for at in (0, 2, 4, 6):
         with pytest.raises(ValueError, match="gradient"):
             M.int8_experts(*[leaf if i == at else x for i in range(7)])
+
+
+def test_the_allocator_learns_of_both_streams(monkeypatch):
+    from sparse_mixture_experts_gemv_gb300 import _tensors
+    device = torch.device("cuda", 0)
+    theirs, ours = types.SimpleNamespace(device=device, at=1), types.SimpleNamespace(device=device, at=2)
+    seen = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: ours)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch, "Tensor", Stand)
+    monkeypatch.setattr(Stand, "record_stream", lambda t, s: seen.append((t, s)), raising=False)
+    a, b, c, d = (Stand(0) for _ in range(4))
+    assert _tensors.run_on(theirs, lambda *args: c, a, 3, b, None) is c
+    assert seen == [(a, theirs), (b, theirs), (c, ours)]
+    seen.clear()
+    assert _tensors.run_on(theirs, lambda *args: (c, d), a) == (c, d)
+    assert seen == [(a, theirs), (c, ours), (d, ours)]
+    seen.clear()
+    _tensors.run_on(ours, lambda *args: c, a)
+    assert seen == []
