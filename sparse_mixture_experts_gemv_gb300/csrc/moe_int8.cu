@@ -698,7 +698,9 @@ int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 //   4 x 4,096 x 16,384   20 / 22     8 x 4,096 x 16,384   30 / 23     32 x 2,048 x 2,048    15 / 18
 //  64 x 2,048 x 2,048    26 / 16   128 x 2,048 x 512      15 / 16    256 x 2,048 x 512      28 / 17
 //  16 x 16,384 x 4,096   57 / 89   512 x 128 x 128        12 / 19  1,024 x 128 x 128        21 / 17
-bool stream_matmul(int64_t T, int64_t N) { return T <= 2 || T * N <= (T <= 4 ? 131072 : 65536); }
+// More tokens than 65,535, the CTAs of a grid's second dimension, always go to the tensor cores: with a long K a
+// CTA of the dot products holds one.
+bool stream_matmul(int64_t T, int64_t N) { return T <= 2 || (T <= 65535 && T * N <= (T <= 4 ? 131072 : 65536)); }
 // Experts (H 2,048, I 512, 8 of 256): 16 tokens 89 / 93, 24 tokens 114 / 113; (2,048, 512, 2 of 16): 23 / 32
 // and 28 / 33, 32 tokens 36 / 33; (1,024, 512, 4 of 64): 27 / 35 and 31 / 36, 32 tokens 43 / 37.
 bool stream_experts(int64_t T) { return T <= 16; }

@@ -57,3 +57,18 @@ def test_tensors_freed_after_a_call_on_another_stream_are_not_handed_out_again()
     assert at not in [t.data_ptr() for t in again]
     s.synchronize()
     assert torch.equal(out, M.int8_matmul(keep, w, ws))
+
+
+def test_most_rows_of_one_channel():
+    """65,536 rows of a K that leaves a CTA one row: more than a grid's second dimension takes."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    T, K = 65536, 49168
+    g = torch.Generator("cuda").manual_seed(0)
+    x = torch.randint(-127, 128, (T, K), generator=g, dtype=torch.int8, device="cuda")
+    w, one, xs = _ints(1, K), torch.ones(1, device="cuda"), torch.full((T,), 0.5, device="cuda")
+    got = M.int8_matmul(x, w, one, xs, out_dtype=torch.float32)
+    some = torch.tensor([0, 1, 191, 192, 32767, 40000, 65534, 65535], device="cuda")
+    ref = (x[some].double() * w.double()).sum(1) * 0.5
+    assert (ref.abs() * 2 < 2 ** 24).all() and torch.equal(got[some, 0].double(), ref)   # exact below 2^24
+    del x, got
+    torch.cuda.empty_cache()

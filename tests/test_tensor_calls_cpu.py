@@ -134,3 +134,14 @@ def test_the_allocator_learns_of_both_streams(monkeypatch):
     seen.clear()
     _tensors.run_on(ours, lambda *args: c, a)
     assert seen == []
+
+
+@pytest.mark.parametrize("K", [1024, 49168, 65536])
+def test_more_rows_than_a_grids_second_dimension(K):
+    """The dot-product kernel takes a row or more a CTA there: what may not fit needs the other one's workspace."""
+    import ctypes
+    from sparse_mixture_experts_gemv_gb300 import _native as N
+    need = ctypes.c_int64()
+    ws = N.load().moe_quant_matmul_workspace
+    assert ws(65536, 1, K, N.MOE_DTYPE_S8, ctypes.byref(need)) == N.MOE_OK and need.value > 65536 * K
+    assert ws(65535, 1, K, N.MOE_DTYPE_S8, ctypes.byref(need)) == N.MOE_OK and need.value == 0
