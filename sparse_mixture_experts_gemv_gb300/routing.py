@@ -19,6 +19,12 @@ SCORES = {"softmax": N.MOE_SCORE_SOFTMAX, "sigmoid": N.MOE_SCORE_SIGMOID}
 def _config(E, k, score, groups, top_groups, group_top, renormalise, scale):
     if score not in SCORES:
         invalid("route_experts", f"score must be one of {sorted(SCORES)}")
+    # kept by their values: a tensor, which would be kept by its identity, can change
+    if any(isinstance(v, torch.Tensor) for v in (k, groups, top_groups, group_top, renormalise, scale)):
+        invalid("route_experts", "k, groups, top_groups, group_top, renormalise and scale are plain values, not tensors")
+    for n in (k, groups, top_groups, group_top):
+        if not 0 <= n < 2 ** 31:
+            invalid("route_experts", f"k, groups, top_groups and group_top must be numbers of 31 bits, not {n}")
     return ctypes.byref(N.moe_route_config_t(E, k, SCORES[score], groups, top_groups, group_top,
                                              1 if renormalise else 0, scale))
 
@@ -40,11 +46,12 @@ def _forward(logits, k, score, bias, groups, top_groups, group_top, renormalise,
     dev = logits.device
     if bias is not None:
         bias = vector(bias, "bias", E, "route_experts", dev)
+    cfg = _config(E, k, score, groups, top_groups, group_top, renormalise, scale)
     idx = torch.empty((T, k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    status = N.load().moe_route_experts(_config(E, k, score, groups, top_groups, group_top, renormalise, scale),
-                                        logits.data_ptr(), code, stride, None if bias is None else bias.data_ptr(), T,
-                                        idx.data_ptr(), weights.data_ptr(), current_stream(dev))
+    status = N.load().moe_route_experts(cfg, logits.data_ptr(), code, stride,
+                                        None if bias is None else bias.data_ptr(), T, idx.data_ptr(),
+                                        weights.data_ptr(), current_stream(dev))
     if status:
         check(status, "moe_route_experts")
     return idx, weights

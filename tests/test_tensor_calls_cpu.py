@@ -145,3 +145,18 @@ def test_more_rows_than_a_grids_second_dimension(K):
     ws = N.load().moe_quant_matmul_workspace
     assert ws(65536, 1, K, N.MOE_DTYPE_S8, ctypes.byref(need)) == N.MOE_OK and need.value > 65536 * K
     assert ws(65535, 1, K, N.MOE_DTYPE_S8, ctypes.byref(need)) == N.MOE_OK and need.value == 0
+
+
+def test_a_routing_rule_is_kept_by_its_values():
+    """A tensor among them would be found again by its identity, with what it held the first time."""
+    from sparse_mixture_experts_gemv_gb300.routing import _config
+    plain = (64, 4, "softmax", 1, 1, 2, True, 2.0)
+    assert _config(*plain)._obj.scale == 2.0 and _config(*plain[:7], 3)._obj.scale == 3.0
+    scale = torch.tensor(2.0)
+    for at, t in ((7, scale), (7, scale.clone().requires_grad_()), (6, torch.tensor(True)), (1, torch.tensor(4))):
+        for _ in range(2):
+            with pytest.raises(ValueError, match="tensor"):
+                _config(*[t if i == at else v for i, v in enumerate(plain)])
+    for at, n in ((1, -1), (1, 2 ** 32 + 4), (3, 2 ** 32 + 1), (4, 2 ** 31), (5, 2 ** 40 + 2)):
+        with pytest.raises(ValueError, match="31 bits"):
+            _config(*[n if i == at else v for i, v in enumerate(plain)])
