@@ -48,11 +48,11 @@ def refuse_tangents(what: str, *tensors):
 
 def refuse_gradients(what: str, *tensors):
     """The call has no gradient: an input that records one would lose it without a word."""
-    refuse_tangents(what, *tensors)
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                invalid(what, "has no gradient, and an input requires one: detach it, or call under torch.no_grad()")
+    if forward_ad._current_level >= 0:
+        refuse_tangents(what, *tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            invalid(what, "has no gradient, and an input requires one: detach it, or call under torch.no_grad()")
 
 
 _device = torch._C._cuda_getDevice   # the current device's index, likewise
@@ -60,7 +60,8 @@ _device = torch._C._cuda_getDevice   # the current device's index, likewise
 
 def elsewhere(t) -> bool:
     """Whether the tensor is on another device than the current one, on which a kernel would start."""
-    return t.is_cuda and t.get_device() != _device()
+    index = t.get_device()   # -1: no CUDA tensor
+    return index >= 0 and index != _device()
 
 
 def run_on(stream, fn, first, *args):
