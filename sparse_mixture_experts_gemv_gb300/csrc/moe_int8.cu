@@ -206,27 +206,25 @@ __global__ void __launch_bounds__(kThreads, 3) int8_experts_up_kernel(const Expe
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t a = blockIdx.y; a < (int64_t)p.T * p.k; a += gridDim.y) {
-    const int e = __ldg(p.idx + a);
-    if (e < 0 || e >= p.E) continue;
-    const int64_t row0 = (int64_t)e * 2 * p.I;
-    const int c0 = blockIdx.x * kFeatures;
-    if (threadIdx.x < 2)
-      prefetch_l2_bulk(p.gate_up + (row0 + (threadIdx.x ? p.I : 0) + c0) * p.H, (uint32_t)(min(kFeatures, p.I - c0) * p.H));
-    __syncthreads();
-    quantize_rows_to_smem<DT>(static_cast<const uint16_t*>(p.x) + a / p.k * p.H, p.H, nullptr, 1, p.H, q, s_scale, red);
-    __syncthreads();
-    const int f0 = min(c0 + 2 * warp, p.I - 1), f1 = min(f0 + 1, p.I - 1);   // a warp past the end repeats the last
-    const int8_t* rows[4] = {p.gate_up + (row0 + f0) * p.H, p.gate_up + (row0 + p.I + f0) * p.H,
-                             p.gate_up + (row0 + f1) * p.H, p.gate_up + (row0 + p.I + f1) * p.H};
-    int acc[4][1];
-    dot_rows<1, 4>(rows, q, p.H / 16, lane, acc);
-    if (lane < 2 && c0 + 2 * warp + lane < p.I) {
-      const float* ws = p.gate_up_scale + row0 + f0 + lane;
-      const float g = (float)(lane ? acc[2][0] : acc[0][0]) * s_scale[0] * __ldg(ws);
-      const float u = (float)(lane ? acc[3][0] : acc[1][0]) * s_scale[0] * __ldg(ws + p.I);
-      p.h[a * p.I + f0 + lane] = swiglu(g, u);
-    }
+  const int64_t a = blockIdx.y;
+  const int e = __ldg(p.idx + a);
+  if (e < 0 || e >= p.E) return;
+  const int64_t row0 = (int64_t)e * 2 * p.I;
+  const int c0 = blockIdx.x * kFeatures;
+  if (threadIdx.x < 2)
+    prefetch_l2_bulk(p.gate_up + (row0 + (threadIdx.x ? p.I : 0) + c0) * p.H, (uint32_t)(min(kFeatures, p.I - c0) * p.H));
+  quantize_rows_to_smem<DT>(static_cast<const uint16_t*>(p.x) + a / p.k * p.H, p.H, nullptr, 1, p.H, q, s_scale, red);
+  __syncthreads();
+  const int f0 = min(c0 + 2 * warp, p.I - 1), f1 = min(f0 + 1, p.I - 1);   // a warp past the end repeats the last
+  const int8_t* rows[4] = {p.gate_up + (row0 + f0) * p.H, p.gate_up + (row0 + p.I + f0) * p.H,
+                           p.gate_up + (row0 + f1) * p.H, p.gate_up + (row0 + p.I + f1) * p.H};
+  int acc[4][1];
+  dot_rows<1, 4>(rows, q, p.H / 16, lane, acc);
+  if (lane < 2 && c0 + 2 * warp + lane < p.I) {
+    const float* ws = p.gate_up_scale + row0 + f0 + lane;
+    const float g = (float)(lane ? acc[2][0] : acc[0][0]) * s_scale[0] * __ldg(ws);
+    const float u = (float)(lane ? acc[3][0] : acc[1][0]) * s_scale[0] * __ldg(ws + p.I);
+    p.h[a * p.I + f0 + lane] = swiglu(g, u);
   }
 }
 
@@ -250,87 +248,86 @@ __global__ void __launch_bounds__(kThreads, 3) int8_experts_down_kernel(const Ex
   const int c0 = blockIdx.x * kWarps * CH, ch0 = c0 + warp * CH;
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t t = blockIdx.y; t < p.T; t += gridDim.y) {
-    float sum[CH];
+  const int64_t t = blockIdx.y;
+  float sum[CH];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) sum[i] = 0.f;
-    for (int j0 = 0; j0 < p.k; j0 += held) {
-      const int nj = min(held, p.k - j0);
-      __syncthreads();
-      for (int j = warp; j < nj; j += kWarps) {
-        const int64_t a = t * p.k + j0 + j;
-        int e = __ldg(p.idx + a);
-        if (e < 0 || e >= p.E) e = -1;
-        if (e >= 0) {
-          const float weight = __ldg(p.weights + a);
-          const float* h = p.h + a * p.I;
-          float v[16], u[16];   // the row's first 1024 values stay in registers
-          uint32_t m = 0;
-          if (lane < nch) {
-            load16_cg(h + 16 * lane, v);
-            m = amax_bits(v);
-          }
-          if (lane + 32 < nch) {
-            load16_cg(h + 16 * (lane + 32), u);
-            m = max(m, amax_bits(u));
-          }
-          for (int c = lane + 64; c < nch; c += 32) {
-            float w[16];
-            load16_cg(h + 16 * c, w);
-            m = max(m, amax_bits(w));
-          }
-          const RowScale r = row_scale(__reduce_max_sync(0xFFFFFFFFu, m));
-          if (lane < nch) q[j * nch + lane] = quantize16(v, r);
-          if (lane + 32 < nch) q[j * nch + lane + 32] = quantize16(u, r);
-          for (int c = lane + 64; c < nch; c += 32) {
-            load16_cg(h + 16 * c, v);
-            q[j * nch + c] = quantize16(v, r);
-          }
-          if (lane == 0) s_scale[j] = r.scale * weight;
+  for (int i = 0; i < CH; ++i) sum[i] = 0.f;
+  for (int j0 = 0; j0 < p.k; j0 += held) {
+    const int nj = min(held, p.k - j0);
+    __syncthreads();
+    for (int j = warp; j < nj; j += kWarps) {
+      const int64_t a = t * p.k + j0 + j;
+      int e = __ldg(p.idx + a);
+      if (e < 0 || e >= p.E) e = -1;
+      if (e >= 0) {
+        const float weight = __ldg(p.weights + a);
+        const float* h = p.h + a * p.I;
+        float v[16], u[16];   // the row's first 1024 values stay in registers
+        uint32_t m = 0;
+        if (lane < nch) {
+          load16_cg(h + 16 * lane, v);
+          m = amax_bits(v);
         }
-        if (lane == 0) s_e[j] = e;
+        if (lane + 32 < nch) {
+          load16_cg(h + 16 * (lane + 32), u);
+          m = max(m, amax_bits(u));
+        }
+        for (int c = lane + 64; c < nch; c += 32) {
+          float w[16];
+          load16_cg(h + 16 * c, w);
+          m = max(m, amax_bits(w));
+        }
+        const RowScale r = row_scale(__reduce_max_sync(0xFFFFFFFFu, m));
+        if (lane < nch) q[j * nch + lane] = quantize16(v, r);
+        if (lane + 32 < nch) q[j * nch + lane + 32] = quantize16(u, r);
+        for (int c = lane + 64; c < nch; c += 32) {
+          load16_cg(h + 16 * c, v);
+          q[j * nch + c] = quantize16(v, r);
+        }
+        if (lane == 0) s_scale[j] = r.scale * weight;
       }
-      __syncthreads();
-      if (ch0 < p.H) {
-        float ws[CH];   // lane j: the scales of choice j
-        const int my_e = lane < nj ? s_e[lane] : -1;
+      if (lane == 0) s_e[j] = e;
+    }
+    __syncthreads();
+    if (ch0 < p.H) {
+      float ws[CH];   // lane j: the scales of choice j
+      const int my_e = lane < nj ? s_e[lane] : -1;
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-          ws[i] = my_e >= 0 && ch0 + i < p.H ? s_scale[lane] * __ldg(p.down_scale + (int64_t)my_e * p.H + ch0 + i) : 0.f;
-        int j = 0, c = lane;   // the lane's chunk: c of choice j
-        while (c >= nch) { c -= nch; ++j; }
-        for (int at = 0; at < nj * nch; at += 32 * kAtOnce) {
-          uint4 w[kAtOnce][CH];
-          int from[kAtOnce];
+      for (int i = 0; i < CH; ++i)
+        ws[i] = my_e >= 0 && ch0 + i < p.H ? s_scale[lane] * __ldg(p.down_scale + (int64_t)my_e * p.H + ch0 + i) : 0.f;
+      int j = 0, c = lane;   // the lane's chunk: c of choice j
+      while (c >= nch) { c -= nch; ++j; }
+      for (int at = 0; at < nj * nch; at += 32 * kAtOnce) {
+        uint4 w[kAtOnce][CH];
+        int from[kAtOnce];
 #pragma unroll
-          for (int u = 0; u < kAtOnce; ++u) {
-            const int e = j < nj ? s_e[j] : -1;
-            const int8_t* row = p.down + ((int64_t)max(e, 0) * p.H + ch0) * p.I + 16 * c;
-            from[u] = e >= 0 ? j : -1;
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int e = j < nj ? s_e[j] : -1;
+          const int8_t* row = p.down + ((int64_t)max(e, 0) * p.H + ch0) * p.I + 16 * c;
+          from[u] = e >= 0 ? j : -1;
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-              w[u][i] = e >= 0 && ch0 + i < p.H ? ldg_stream(row + (int64_t)i * p.I) : make_uint4(0, 0, 0, 0);
-            c += 32;
-            while (c >= nch) { c -= nch; ++j; }
-          }
+          for (int i = 0; i < CH; ++i)
+            w[u][i] = e >= 0 && ch0 + i < p.H ? ldg_stream(row + (int64_t)i * p.I) : make_uint4(0, 0, 0, 0);
+          c += 32;
+          while (c >= nch) { c -= nch; ++j; }
+        }
 #pragma unroll
-          for (int u = 0; u < kAtOnce; ++u) {
-            const int chunk = at + 32 * u + lane;
-            const uint4 xv = from[u] >= 0 ? q[chunk] : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int chunk = at + 32 * u + lane;
+          const uint4 xv = from[u] >= 0 ? q[chunk] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const float f = __shfl_sync(0xFFFFFFFFu, ws[i], from[u] & 31);
-              if (from[u] >= 0) sum[i] += (float)dot16(w[u][i], xv, 0) * f;
-            }
+          for (int i = 0; i < CH; ++i) {
+            const float f = __shfl_sync(0xFFFFFFFFu, ws[i], from[u] & 31);
+            if (from[u] >= 0) sum[i] += (float)dot16(w[u][i], xv, 0) * f;
           }
         }
       }
     }
+  }
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const float f = warp_sum(sum[i]);
-      if (lane == i && ch0 + i < p.H) store(p.out, p.out_dtype, t * p.H + ch0 + i, f);
-    }
+  for (int i = 0; i < CH; ++i) {
+    const float f = warp_sum(sum[i]);
+    if (lane == i && ch0 + i < p.H) store(p.out, p.out_dtype, t * p.H + ch0 + i, f);
   }
 }
 
@@ -662,8 +659,7 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int block, size_t smem, cudaStream_t
 }
 
 cudaError_t launch_experts_stream(const ExpertsParams& p, int x_dtype, int num_sms, cudaStream_t s) {
-  const int64_t choices = (int64_t)p.T * p.k;
-  const dim3 up((p.I + kFeatures - 1) / kFeatures, (unsigned)(choices < 65535 ? choices : 65535));
+  const dim3 up((p.I + kFeatures - 1) / kFeatures, (unsigned)(p.T * p.k));
   cudaError_t e = x_dtype == MOE_DTYPE_BF16
                       ? launch_pdl(int8_experts_up_kernel<MOE_DTYPE_BF16>, up, kThreads, (size_t)p.H, s, p)
                       : launch_pdl(int8_experts_up_kernel<MOE_DTYPE_F16>, up, kThreads, (size_t)p.H, s, p);
@@ -673,7 +669,7 @@ cudaError_t launch_experts_stream(const ExpertsParams& p, int x_dtype, int num_s
   // as many channels a warp as leave two CTAs an SM
   const int64_t want = (int64_t)p.T * p.H / (2 * kWarps * num_sms);
   const auto down = [&](int ch) {
-    return dim3((p.H + kWarps * ch - 1) / (kWarps * ch), (unsigned)(p.T < 65535 ? p.T : 65535));
+    return dim3((p.H + kWarps * ch - 1) / (kWarps * ch), (unsigned)p.T);
   };
   const size_t smem = (size_t)held * p.I;
   if (want < 2) return launch_pdl(int8_experts_down_kernel<1>, down(1), kThreads, smem, s, p, held);
