@@ -460,8 +460,11 @@ moe_status_t moe_route_experts_backward(const moe_route_config_t* cfg, const voi
  * row of NaN. w_dev S8 [N, K], w_scale_dev fp32 [N]; out_dev [T, N] BF16, F16 or F32
  * without gaps, rounded once. Rows of x and w start x_stride and w_stride elements
  * apart. K, the strides in bytes and the addresses of x and w are multiples of 16 (K
- * else MOE_ERR_UNSUPPORTED); K <= MOE_INT8_MAX_K. T or N of 0 is a no-op. Integer sums are exact
- * up to 2^24 in magnitude and rounded to 24 bits beyond that.
+ * else MOE_ERR_UNSUPPORTED); 16 <= K <= MOE_INT8_MAX_K. T or N of 0 is a no-op. Few tokens
+ * (see moe_quant_matmul_workspace: 0 bytes) are added up as integers, exactly, and rounded
+ * to fp32 once. Many are added up in fp32 on the tensor cores: exactly while no partial sum
+ * passes 2^24, as for every K up to 1,024; beyond it each of K / 16 additions may round the
+ * sum so far, and the error is at most K / 16 * 2^-23 of sum_k |q[t, k] w[n, k]|.
  * workspace_dev: moe_quant_matmul_workspace() bytes, 256-byte aligned, free for reuse
  * when the call's work on `stream` has finished (NULL where 0 bytes are needed).
  */

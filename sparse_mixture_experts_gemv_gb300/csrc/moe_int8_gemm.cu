@@ -6,7 +6,9 @@
 // The fifth-generation tensor cores have no 8-bit integer kind on this chip, and the
 // older integer instructions run far below the f16 rate. Whole numbers of 8 bits are
 // exact in f16, their products (at most 2^14) and sums (up to 2^24) in the fp32
-// accumulators, so the products run as f16 x f16, and give the integers themselves.
+// accumulators, so the products run as f16 x f16, and give the integers themselves as
+// long as no partial sum passes 2^24: for every K up to 1,024, and for longer ones but
+// where nearly all terms are large and of one sign. There every step rounds.
 //
 // The weights stay bytes in memory: each tile of 128 channels x 128 bytes comes in by
 // TMA, eight converter warps turn it into f16 and write it straight into tensor memory,

@@ -72,3 +72,38 @@ def test_most_rows_of_one_channel():
     assert (ref.abs() * 2 < 2 ** 24).all() and torch.equal(got[some, 0].double(), ref)   # exact below 2^24
     del x, got
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_sums_of_few_tokens_are_exact(T):
+    """Integer sums beyond 2^24, of one sign and cancelling: added as integers and rounded once."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    K, n = 65536, 40
+    w = torch.full((n, K), 127, dtype=torch.int8)
+    w[1] = -128
+    w[2, ::2] = -127
+    w[3, : K // 2] = -127
+    w[4:] = _ints(n - 4, K).cpu()
+    x = torch.full((T, K), 127, dtype=torch.int8)
+    x[T - 1, 1:] = -128
+    got = M.int8_matmul(x.cuda(), w.cuda(), torch.ones(n, device="cuda"), torch.ones(T, device="cuda"),
+                        out_dtype=torch.float32)
+    ref = x.long() @ w.long().T
+    assert ref.abs().max() > 2 ** 29 and torch.equal(got.cpu(), ref.float())
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_sums_that_no_part_of_passes_24_bits_are_exact(T):
+    """K of 1,024 and less: the largest partial sum there can be is 128 * 128 * 1,024 = 2^24."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    K, n = 1024, 2000
+    w = _ints(n, K, lo=100).cpu()
+    w[1], w[2], w[3, : K // 2] = -128, 127, -127
+    w[4:600] = -_ints(596, K, lo=100, seed=1).cpu()
+    x = _ints(T, K, lo=120, seed=2).cpu()
+    x[0] = -128
+    got = M.int8_matmul(x.cuda(), w.cuda(), torch.ones(n, device="cuda"), torch.ones(T, device="cuda"),
+                        out_dtype=torch.float32)
+    ref = (x.double() @ w.double().T).long()
+    assert ref.abs().max() == 2 ** 24 and (T == 1 or (ref % 2 != 0).any())   # the row of -128 alone is even
+    assert torch.equal(got.cpu().long(), ref)
