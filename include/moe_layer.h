@@ -455,9 +455,10 @@ moe_status_t moe_route_experts_backward(const moe_route_config_t* cfg, const voi
  *   out[t, n] = (sum_k q[t, k] * w[n, k]) * x_scale[t] * w_scale[n]
  * x_dev [T, K]: S8 with x_scale_dev fp32 [T], or BF16 / F16 / F32 with x_scale_dev
  * NULL. The latter is quantized by the call: x_scale[t] = amax_k |x[t, k]| times 1/127,
- * both rounded to fp32 (1 for a row of zeros), q = x / x_scale to the nearest whole
- * number, halves to the even one (of the real quotient). A row that holds an infinity or a NaN gives a
- * row of NaN. w_dev S8 [N, K], w_scale_dev fp32 [N]; out_dev [T, N] BF16, F16 or F32
+ * both rounded to fp32 (not the rounded quotient by 127; 1 for a row of zeros),
+ * q = x / x_scale to the nearest whole number, halves to the even one (of the real
+ * quotient). A row that holds an infinity or a NaN gives a row of NaN.
+ * w_dev S8 [N, K], w_scale_dev fp32 [N]; out_dev [T, N] BF16, F16 or F32
  * without gaps, rounded once. Rows of x and w start x_stride and w_stride elements
  * apart. K, the strides in bytes and the addresses of x and w are multiples of 16 (K
  * else MOE_ERR_UNSUPPORTED); 16 <= K <= MOE_INT8_MAX_K. T or N of 0 is a no-op. Few tokens

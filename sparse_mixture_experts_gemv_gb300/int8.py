@@ -42,9 +42,10 @@ def int8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale
     """out[t, n] = (sum_k q[t, k] w[n, k]) x_scale[t] w_scale[n].
 
     w: int8 [N, K], w_scale: fp32 [N]. x [T, K]: int8 with x_scale fp32 [T], or bf16, fp16 or
-    fp32 without: each row is then quantized by the call to its largest magnitude / 127, to
-    the nearest whole number (a row with an infinity or a NaN gives NaN). K is a multiple of
-    16. Rows may be apart (any stride(0)); rows off 16-byte boundaries are copied first.
+    fp32 without: each row is then quantized by the call, its scale being its largest magnitude
+    times fp32(1/127) (what amax / 127 is for a tensor on the GPU; the rounded quotient differs
+    by a step in some rows), to the nearest whole number (a row with an infinity or a NaN gives
+    NaN). K is a multiple of 16. Rows may be apart (any stride(0)); rows off 16-byte boundaries are copied first.
     out_dtype: bf16, fp16 or fp32; by default x's, and bf16 for int8 x. There is no gradient:
     inputs that require one are refused while gradients are recorded.
     """

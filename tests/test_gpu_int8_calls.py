@@ -1,7 +1,7 @@
 """int8_matmul and int8_experts: what they refuse, and the sizes at the ends of their ranges."""
 import pytest
 
-from test_gpu_int8 import _choices, _experts, _ints, _scales, _x
+from test_gpu_int8 import DT, _choices, _experts, _ints, _scales, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,17 @@ def test_sums_that_no_part_of_passes_24_bits_are_exact(T):
     ref = (x.double() @ w.double().T).long()
     assert ref.abs().max() == 2 ** 24 and (T == 1 or (ref % 2 != 0).any())   # the row of -128 alone is even
     assert torch.equal(got.cpu().long(), ref)
+
+
+@pytest.mark.parametrize("T", [2, 500])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_rows_quantized_by_the_caller_are_the_calls(T, dtype):
+    """amax / 127 on the GPU is the scale that the call takes, halves of the largest value among the elements."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    x = _x(T, 272, dtype, seed=T)
+    x[:, 7] = x.abs().amax(1) / 2
+    w, ws = _ints(300, 272), _scales(300)
+    scale = x.float().abs().amax(1) / 127
+    q = (x.double() / scale.double()[:, None]).round().to(torch.int8)
+    assert torch.equal(M.int8_matmul(x, w, ws, out_dtype=torch.float32),
+                       M.int8_matmul(q, w, ws, scale, out_dtype=torch.float32))
