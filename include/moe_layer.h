@@ -511,6 +511,9 @@ moe_status_t moe_quant_experts(const moe_int8_experts_config_t* cfg, const moe_i
  * out (its outputs are undefined then).
  */
 moe_status_t moe_quant_sync_status(void* stream);
+/* Test only: while nonzero, the tensor-core products that the calling thread launches get no tokens, so that their
+ * bounded waits run out (about two seconds each) and moe_quant_sync_status reports it. */
+void moe_quant_test_force_wait_timeout(int32_t on);
 
 /* Name of a status code (static string). */
 const char* moe_status_string(moe_status_t status);

@@ -141,6 +141,7 @@ _SIGNATURES = {
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     "moe_quant_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
+    "moe_quant_test_force_wait_timeout": (None, [ctypes.c_int32]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_cuda_error": (ctypes.c_char_p, []),
 }

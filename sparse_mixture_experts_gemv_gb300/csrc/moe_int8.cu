@@ -994,6 +994,8 @@ moe_status_t moe_quant_experts(const moe_int8_experts_config_t* c, const moe_int
   return e == cudaSuccess ? MOE_OK : moe::record_cuda_failure(e, "moe_quant_experts");
 }
 
+void moe_quant_test_force_wait_timeout(int32_t on) { moe::int8::test_withhold(on != 0); }
+
 moe_status_t moe_quant_sync_status(void* stream) {
   int code = 0;
   const cudaError_t e = moe::int8::gemm_status((cudaStream_t)stream, &code);

@@ -36,6 +36,7 @@ struct GemmArgs {
 };
 int device_sms();   // of the current device
 cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStream_t s);
+void test_withhold(int on);   // test only: products launched by this thread get no tokens
 cudaError_t gemm_status(cudaStream_t s, int* code);   // synchronises; reads and clears the device's error word
 
 }  // namespace int8

@@ -77,6 +77,7 @@ struct Params {
   void* out;
   int out_dtype;
   int wide;                  // dense: 16-bit results whose rows are 16-byte aligned
+  int withhold;              // test only: no tokens come, so that the waits for them run out
 };
 
 // A copy's issue costs about as much as 8 KB, so that every step is one copy of weights (up: two) and one
@@ -298,7 +299,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     // -------------------------------------------------------------- tokens
     uint32_t it = 0;
     int s = 0, ph = 1;
-    bool stop = false;
+    bool stop = p.withhold != 0;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = decode<KIND>(p, tile);
       const CUtensorMap* map = &maps.b[t.n / 16 - 1];
@@ -589,7 +590,11 @@ cudaError_t launch_kind(const Maps& maps, const Params& p, int grid, size_t smem
   return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<KIND>, maps, p);
 }
 
+thread_local int t_withhold = 0;
+
 }  // namespace
+
+void test_withhold(int on) { t_withhold = on; }
 
 cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStream_t s) {
   Maps maps = {};
@@ -622,6 +627,7 @@ cudaError_t launch_gemm(GemmKind kind, const GemmArgs& a, int num_sms, cudaStrea
   p.w_scale = a.w_scale;
   p.out = a.out;
   p.out_dtype = a.out_dtype;
+  p.withhold = t_withhold;
   p.wide = a.out_dtype != MOE_DTYPE_F32 && a.channels % 8 == 0 && !((uintptr_t)a.out & 15);
   const size_t smem = (size_t)p.b_stages * p.b_bytes + (size_t)p.raw_stages * kRawBytes + kFixedSmem;
   const int64_t tiles = (int64_t)p.tiles_m * (kind == kDense ? p.tiles_t : a.max_blocks);

@@ -121,3 +121,28 @@ def test_rows_quantized_by_the_caller_are_the_calls(T, dtype):
     q = (x.double() / scale.double()[:, None]).round().to(torch.int8)
     assert torch.equal(M.int8_matmul(x, w, ws, out_dtype=torch.float32),
                        M.int8_matmul(q, w, ws, scale, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("op", ["matmul", "experts"])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_device_usable(op):
+    """Tokens that never come: every role of the product winds down after its bounded wait, the status says so
+    once, and the next call is right."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    from sparse_mixture_experts_gemv_gb300 import _native as N
+    if op == "matmul":
+        x, w, ws = _x(200, 1040, "bf16"), _ints(3000, 1040), _scales(3000)
+        call = lambda: M.int8_matmul(x, w, ws)  # noqa: E731
+    else:
+        xe, (idx, weights), ex = _x(40, 640, "bf16"), _choices(40, 8, 2), _experts(8, 640, 576)
+        call = lambda: M.int8_experts(xe, idx, weights, *ex)  # noqa: E731
+    want = call()
+    assert M.int8_sync_status() == N.MOE_OK
+    N.load().moe_quant_test_force_wait_timeout(1)
+    try:
+        call()
+    finally:
+        N.load().moe_quant_test_force_wait_timeout(0)
+    assert M.int8_sync_status() == N.MOE_ERR_TIMEOUT
+    assert M.int8_sync_status() == N.MOE_OK
+    assert torch.equal(call(), want)
+    assert M.int8_sync_status() == N.MOE_OK
