@@ -697,9 +697,23 @@ int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 // More tokens than 65,535, the CTAs of a grid's second dimension, always go to the tensor cores: with a long K a
 // CTA of the dot products holds one.
 bool stream_matmul(int64_t T, int64_t N) { return T <= 2 || (T <= 65535 && T * N <= (T <= 4 ? 131072 : 65536)); }
-// Experts (H 2,048, I 512, 8 of 256): 16 tokens 89 / 93, 24 tokens 114 / 113; (2,048, 512, 2 of 16): 23 / 32
-// and 28 / 33, 32 tokens 36 / 33; (1,024, 512, 4 of 64): 27 / 35 and 31 / 36, 32 tokens 43 / 37.
-bool stream_experts(int64_t T) { return T <= 16; }
+// Experts: the dot-product kernels read an expert's rows for every choice of it, the second time from L2 (some 7 TB/s);
+// the tensor cores read them once, and take three launches more, some 20 us. So few tokens stream, unless the choices
+// beyond one an expert have 2^27 bytes and more to read again. GB300, us a call after a flush of L2, streamed / tensor
+// cores, k of E, H x I, and the bytes read again:
+//   8 of 256, 2,048 x 512   T 16  86 / 101 (0)        T 24 111 / 128    T 32 145 / 142
+//   8 of 512, 2,560 x 768   T 16 141 / 159 (0)        T 24 201 / 208    T 32 244 / 243
+//   8 of 128, 2,048 x 768   T 12  86 / 103 (0)        T 16 117 / 114 (0)
+//   2 of  16, 2,048 x 512   T 16  29 /  42 (50 MB)    T 32  43 /  46
+//   8 of  16, 2,048 x 512   T  4  33 /  44 (50 MB)    T  8  41 /  48 (151 MB)   T 16  66 / 50 (352 MB)
+//  32 of  32, 2,048 x 512   T  2  61 /  67 (101 MB)   T  4  86 /  69 (302 MB)   T 16 223 / 93 (1.5 GB)
+//  32 of  64, 1,024 x 256   T  4  45 /  46 (50 MB)    T  8  63 /  52 (151 MB)   T 16  94 / 60 (352 MB)
+//   8 of   8, 1,024 x 512   T  8  35 /  32 (88 MB)    T 12  37 /  34 (138 MB)   T 16  47 / 34 (189 MB)
+//   2 of   8, 4,096 x 2,048 T  4  53 /  79 (0)        T  8  78 /  83 (201 MB)   T 12  98 / 85 (403 MB)
+bool stream_experts(const moe_int8_experts_config_t* c, int64_t T) {
+  const int64_t again = T * c->top_k - c->num_experts;
+  return T <= 16 && again * 3 * c->hidden * c->intermediate < (int64_t(1) << 27);
+}
 
 cudaError_t launch_prepare(const PrepareParams& p, int dtype, int num_sms, cudaStream_t s) {
   const int64_t blocks = ((int64_t)p.rows + kPrepareThreads / 32 - 1) / (kPrepareThreads / 32);
@@ -769,7 +783,7 @@ struct ExpertsWorkspace {
 ExpertsWorkspace experts_workspace(const moe_int8_experts_config_t* c, int64_t T) {
   ExpertsWorkspace w = {};
   const int64_t rows = T * c->top_k, H = c->hidden, I = c->intermediate;
-  if (stream_experts(T)) {
+  if (stream_experts(c, T)) {
     w.bytes = pad256(rows * I * 4);
     return w;
   }
@@ -987,7 +1001,7 @@ moe_status_t moe_quant_experts(const moe_int8_experts_config_t* c, const moe_int
   p.H = c->hidden;
   p.I = c->intermediate;
   p.out_dtype = x_dtype;
-  const cudaError_t e = stream_experts(T)
+  const cudaError_t e = stream_experts(c, T)
                             ? launch_experts_stream(p, x_dtype, device_sms(), (cudaStream_t)stream)
                             : launch_experts_tensor(p, c, x_dtype, (uint8_t*)workspace_dev, device_sms(),
                                                     (cudaStream_t)stream);

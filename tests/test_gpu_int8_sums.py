@@ -57,3 +57,13 @@ def test_a_channel_of_any_scale_leaves_the_others_alone(T, scale):
         assert (got[:, 77].abs() < 1e-37).all()
     elif scale != 3e38:
         assert not torch.isfinite(got[:, 77]).any()
+
+
+@pytest.mark.parametrize("T,k", [(6, 8), (7, 8), (2, 24), (16, 8), (16, 24)])
+def test_few_tokens_that_share_experts(T, k):
+    """On either side of the rule that goes by the bytes read again for choices of the same expert."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    E = 8 if k == 8 else 24
+    x, (idx, w), ex = _x(T, 2048, "bf16", seed=T), _choices(T, E, k, seed=T), _experts(E, 2048, 512)
+    idx[T - 1, 0] = -1
+    _close(x, idx, w, ex, M.int8_experts(x, idx, w, *ex))
