@@ -232,8 +232,8 @@ constexpr int kMaxChoices = MOE_ROUTE_MAX_TOP_K;
 
 // out of one token (blockIdx.y) and CH channels a warp, all its choices. Dynamic shared memory: `held`
 // quantized rows of h; every CTA quantizes all of the token's, which more channels a warp keep from being
-// most of the work. (Ling-shaped, T = 4: of 42 us for both kernels the tokens' quantization here is 5, the
-// rows 13. Requesting the rows into L2 ahead of h, by this kernel or the one before, made it 45 and 46.5.)
+// most of the work. (Ling-shaped, T = 4: of 39 to 42 us for both kernels the tokens' quantization here is 5,
+// the rows 13. Requesting the rows into L2 ahead of h, by this kernel or the one before, made it 3 and 4.5 more.)
 // The chunks of all the held
 // choices are one list: lane l takes chunks l, l + 32, ..., 8 / CH of them and CH channels at once, so that
 // eight loads are in flight and a chunk's place and token values serve CH channels.

@@ -138,8 +138,12 @@ MOE_DEV unsigned long long f64_order_key(double d) {
 // The k choices of one token, lane r's being the r-th, with every key in 64 bits (the logits
 // themselves where nothing else is asked for). keys: E doubles of this warp in shared memory. It
 // serves the rows that the short list does not: too few lanes with an expert on, too many equal
-// keys, groups or (softmax) experts too close to tell apart in 32 bits. Rare, and so fetched cold:
-// rolled loops, as little code as can be (unrolled, its fetch alone took some 50 us of a call).
+// keys, groups or (softmax) experts too close to tell apart in 32 bits. With sigmoid scores, or a
+// bias of distinct values, that is under 1% of rows, and so it is fetched cold: rolled loops, as
+// little code as can be (unrolled, its fetch alone took some 50 us of a call). It is not rare where
+// a softmax has equal keys, as 16-bit logits often are under groups or under one bias for several
+// experts: 6% (fp16) to 50% (bf16) of rows, and 65,536 x 512 take 0.6 to 2.7 ms. Nor where one
+// finite bias is very large (-1e9), by which all rows' keys count as close: 3.3 to 4.6 ms (-inf: 57 us).
 template <int DT>
 __device__ __noinline__ int route_exact(const RouteParams& p, int64_t t, bool keyed, double* keys, int lane) {
   const double kNone = -(double)INFINITY, kOut = __longlong_as_double(0x7FF8000000000000ll);   // off; NaN: out
@@ -321,7 +325,7 @@ MOE_DEV float rcp(float v) {
 // indexes, are ranked by counting; with a bias or groups, keys closer than `near` are ranked again in
 // 64 bits, one evaluation a lane.
 // What bounds it is its instructions, a warp's per row, not what it reads: 65,536 rows of 512 bf16 logits
-// with a bias and groups take 75 us, 909 instructions a row with 69% of the issue slots busy (all keys through k
+// with a bias and groups take 75 us, 910 instructions a row with 68% of the issue slots busy (all keys through k
 // rounds of a warp: 457 us); 4,096 rows of 256 without 6 us.
 template <int DT, int NPL, bool VEC, bool KEYED>
 __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_experts_kernel(const RouteParams p) {

@@ -108,7 +108,7 @@ def route_experts(logits: torch.Tensor, k: int, score: str = "softmax", bias: to
     """Chooses k experts for each row of logits [T, E] (fp32, bf16 or fp16).
 
     score: "softmax" or "sigmoid". bias: fp32 [E], added to the scores for the choice alone
-    (a bias for balance). groups > 1: consecutive experts form groups; the top_groups groups
+    (a bias for balance; it has no gradient). groups > 1: consecutive experts form groups; the top_groups groups
     whose group_top (1 or 2) largest keys add up to most stay. The weights are the scores
     without the bias, divided by their sum if renormalise, times scale. Equal keys go by the
     lower index; a logit of -inf or NaN turns its expert off for the row. A bias of
