@@ -36,13 +36,14 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include "moe_int8.cuh"
 #include "moe_int8.h"
 #include "moe_layer.h"
 #include "moe_sm100.cuh"
+#include "moe_sm100_warp.cuh"
+#include "moe_tensormap.h"
 
 namespace moe {
 namespace int8 {
@@ -139,69 +140,6 @@ MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// One lane of a converged warp, the same one each time. Roles run as whole warps and elect a
-// lane around what it issues: the compiler then keeps addresses and descriptors in uniform
-// registers (four MMAs and a commit of one thread in a divergent branch issue in 275
-// cycles, elected in 165).
-MOE_DEV bool elect() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-  return r != 0;
-}
-// Barriers by their 32-bit shared-memory addresses: the roles' loops are bound by their own
-// instructions, and generic pointers cost several of them each time.
-MOE_DEV bool try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-// Bounded: about two seconds, after which every role winds down and the error word is set.
-__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  const long long t0 = clock64();
-  while (!__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) {
-    if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
-    if (__any_sync(0xFFFFFFFFu, clock64() - t0 > 4000000000LL)) {
-      set_error(&g_gemm_error, kDevTimeout);
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
-// A wait by a whole warp, which goes on or gives up as one.
-MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
-  return slow_wait(bar, parity, abort);
-}
-MOE_DEV void arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-MOE_DEV void expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
-}
-MOE_DEV void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
-}
-MOE_DEV void load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
-}
-MOE_DEV void load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
-}
-
-// After an abort: the copies of a ring's last stages land before the CTA exits.
-MOE_DEV void land(uint64_t* full, int stages, uint32_t issued, volatile int* abort) {
-  if ((threadIdx.x & 31) || !*abort) return;
-  for (uint32_t q = issued > (uint32_t)stages ? issued - stages : 0; q < issued; ++q)
-    mbar_wait(&full[q % stages], (q / stages) & 1, &g_gemm_error, abort, 20000000LL, false);
-}
-
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
 MOE_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -284,7 +222,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       const Tile t = decode<KIND>(p, tile);
       const int r0 = t.e * p.rows_per_group + t.mt * (KIND == kUp ? 64 : kChannels);
       for (int ks = 0; ks < p.steps; ++ks, ++it) {
-        if (!warp_wait(raw_empty0 + 8 * s, ph, abort_flag)) { stop = true; break; }
+        if (!warp_wait(raw_empty0 + 8 * s, ph, &g_gemm_error, abort_flag)) { stop = true; break; }
         if (elect()) {
           const uint32_t bar = raw_full0 + 8 * s, dst = raw0 + s * kRawBytes;
           expect_tx(bar, kRawBytes);
@@ -296,7 +234,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
         if (++s == p.raw_stages) { s = 0; ph ^= 1; }
       }
     }
-    land(raw_full, p.raw_stages, it, abort_flag);
+    land(raw_full, p.raw_stages, it, &g_gemm_error, abort_flag);
   } else if (warp == 2) {
     // -------------------------------------------------------------- tokens
     uint32_t it = 0;
@@ -306,7 +244,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       const Tile t = decode<KIND>(p, tile);
       const CUtensorMap* map = &maps.b[t.n / 16 - 1];
       for (int ks = 0; ks < p.steps; ++ks, ++it) {
-        if (!warp_wait(b_empty0 + 8 * s, ph, abort_flag)) { stop = true; break; }
+        if (!warp_wait(b_empty0 + 8 * s, ph, &g_gemm_error, abort_flag)) { stop = true; break; }
         if (elect()) {
           expect_tx(b_full0 + 8 * s, (uint32_t)(t.n * kStep * 2));
           load_3d(b0 + s * p.b_bytes, map, 0, t.row0, ks * (kStep / 64), b_full0 + 8 * s);
@@ -315,7 +253,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
         if (++s == p.b_stages) { s = 0; ph ^= 1; }
       }
     }
-    land(b_full, p.b_stages, it, abort_flag);
+    land(b_full, p.b_stages, it, &g_gemm_error, abort_flag);
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
     int s = 0, ph = 0;
@@ -328,10 +266,11 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       const uint32_t idesc = (1u << 4) | ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kChannels >> 4) << 24);
       const uint32_t ab = tc & 1, d = tmem + ab * kMaxBlock;
       const uint32_t half = (uint32_t)t.n * 8;   // the second 64 of K lie n x 128 bytes behind the first
-      if (!warp_wait(d_empty0 + 8 * ab, ((tc >> 1) & 1) ^ 1, abort_flag)) break;
+      if (!warp_wait(d_empty0 + 8 * ab, ((tc >> 1) & 1) ^ 1, &g_gemm_error, abort_flag)) break;
       tc_fence_after();
       for (int ks = 0; ks < p.steps; ++ks) {
-        if (!warp_wait(b_full0 + 8 * s, ph, abort_flag) || !warp_wait(a_full0 + 8 * slot, slot_ph, abort_flag)) {
+        if (!warp_wait(b_full0 + 8 * s, ph, &g_gemm_error, abort_flag) ||
+            !warp_wait(a_full0 + 8 * slot, slot_ph, &g_gemm_error, abort_flag)) {
           stop = true;
           break;
         }
@@ -369,7 +308,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     bool stop = false, first = true;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       for (int ks = 0; ks < p.steps; ++ks) {
-        if (!warp_wait(raw_full0 + 8 * s, ph, abort_flag)) { stop = true; break; }
+        if (!warp_wait(raw_full0 + 8 * s, ph, &g_gemm_error, abort_flag)) { stop = true; break; }
         const uint8_t* src = src0 + s * kRawBytes;
         uint32_t r[32];
 #pragma unroll
@@ -385,7 +324,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
         __syncwarp();
         if (lane == 0) arrive(raw_empty0 + 8 * s);
         if (es == 0) first = false;
-        if (!first && !warp_wait(b_empty0 + 8 * es, eph, abort_flag)) { stop = true; break; }
+        if (!first && !warp_wait(b_empty0 + 8 * es, eph, &g_gemm_error, abort_flag)) { stop = true; break; }
         tc_fence_after();
         tmem_st32(to + slot * kSlotCols, r);
         tc_fence_before();
@@ -435,7 +374,7 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
       const int ch = channel(t);
       const bool in = ch < p.channels;
       __syncwarp();
-      if (!warp_wait(smem_u32(&d_full[ab]), (tc >> 1) & 1, abort_flag)) break;
+      if (!warp_wait(smem_u32(&d_full[ab]), (tc >> 1) & 1, &g_gemm_error, abort_flag)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ab * kMaxBlock + ((uint32_t)(quad * 32) << 16);
       for (int c0 = 0; c0 < t.rows; c0 += 32) {
@@ -530,33 +469,11 @@ int8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
 }
 
 // ------------------------------------------------------------------------- host
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 f = nullptr;
-  if (!f) {
-    cudaDriverEntryPointQueryResult q;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      f = (PFN_cuTensorMapEncodeTiled_v12000)fn;
-  }
-  return f;
-}
-
-cudaError_t encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
-                   const cuuint64_t* strides, const cuuint32_t* box) {
-  PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
-  if (!f) return cudaErrorNotSupported;
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = f(m, type, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
 // `box_rows` rows of a step's 128 bytes; zeros past the rows' ends.
 cudaError_t encode_weights(CUtensorMap* m, const GemmArgs& a, uint32_t box_rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.a_rows}, strides[1] = {(cuuint64_t)a.a_stride};
   const cuuint32_t box[2] = {kStep, box_rows};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.a, dims, strides, box);
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.a, dims, strides, box);
 }
 // A step's tokens in one copy: two columns of n rows x 64 values, one behind the other.
 // Rows are padded to 64 values, so that a column never reaches into the next row.
@@ -564,7 +481,7 @@ cudaError_t encode_tokens(CUtensorMap* m, const GemmArgs& a, uint32_t n) {
   const cuuint64_t dims[3] = {64, (cuuint64_t)a.b_rows, (cuuint64_t)(a.b_stride / 64)};
   const cuuint64_t strides[2] = {(cuuint64_t)a.b_stride * 2, 128};
   const cuuint32_t box[3] = {64, n, kStep / 64};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, a.b, dims, strides, box);
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, a.b, dims, strides, box);
 }
 
 template <int KIND>
