@@ -400,7 +400,7 @@ void moe_lmhead_destroy(moe_lmhead_t* head);
  * ones that need scratch say how much. Nothing allocates or synchronises; work is
  * enqueued on `stream`, which belongs to the current device, as every buffer does. (The pages name no such interface; it is this library's own.)
  * ------------------------------------------------------------------------ */
-typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_S8 = 3 } moe_dtype_t;
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_S8 = 3, MOE_DTYPE_E4M3 = 4 } moe_dtype_t;
 
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
@@ -514,6 +514,103 @@ moe_status_t moe_quant_sync_status(void* stream);
 /* Test only: while nonzero, the tensor-core products that the calling thread launches get no tokens, so that their
  * bounded waits run out (about two seconds each) and moe_quant_sync_status reports it. */
 void moe_quant_test_force_wait_timeout(int32_t on);
+
+/* ------------------------------------------------------------------------
+ * Tokens in the order of their experts and back, and products in 8-bit floating point
+ * with a scale for each block of 128. As above: no state, every buffer is the caller's,
+ * nothing allocates or synchronises. (The pages name no such interface; it is this
+ * library's own.)
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Copies each token's row to the places of its k choices, which are sorted by expert,
+ * those of one expert in the order of the choices (t, j):
+ *   rows_dev [T k][row_bytes]   rows[pos[t, j]] = x[t]
+ *   offsets_dev int32 [E + 1]   expert e has the rows offsets[e] .. offsets[e + 1]
+ *   pos_dev int32 [T, k]
+ * A choice outside [0, E) takes a place behind the last expert's rows: that row is zero, and
+ * pos is ~place (below 0). So every row belongs to one choice. Rows of x have row_bytes
+ * bytes and start row_stride bytes apart; any alignment (16 bytes is fastest). With
+ * x_scale_dev fp32 [T, scales] the scales go the same way to row_scale_dev
+ * [T k, scales] (scales 0 and NULL: none). x and rows, idx and pos do not overlap. T == 0
+ * writes offsets of 0. E <= MOE_DISPATCH_MAX_EXPERTS, k <= MOE_ROUTE_MAX_TOP_K,
+ * T * k < 2^30. Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ */
+#define MOE_DISPATCH_MAX_EXPERTS 1024
+moe_status_t moe_dispatch_tokens(const void* x_dev, int64_t row_bytes, int64_t row_stride, const float* x_scale_dev,
+                                 int32_t scales, const int32_t* idx_dev, int32_t T, int32_t k, int32_t E, void* rows_dev,
+                                 float* row_scale_dev, int32_t* offsets_dev, int32_t* pos_dev, void* stream);
+
+/*
+ * out[t] = sum_j weights[t, j] * y[pos[t, j]], added up in fp32 in the order of j and
+ * rounded once; weights_dev fp32 [T, k], NULL: all 1 (which is also the gradient of x
+ * from that of rows in moe_dispatch_tokens). y_dev [T k][H] (row stride y_stride elements)
+ * and out_dev [T, H] (no gaps) are F32, BF16 or F16. A pos below 0, or of no row, adds nothing.
+ * T == 0 is a no-op. Limits and errors as above.
+ */
+moe_status_t moe_combine_tokens(const void* y_dev, int32_t dtype, int64_t y_stride, const int32_t* pos_dev,
+                                const float* weights_dev, int32_t T, int32_t k, int32_t H, void* out_dev, void* stream);
+
+/*
+ * Its gradients from d_out_dev [T, H] (row stride d_stride): d_y_dev [T k][H] without gaps,
+ * d_y[pos[t, j]] = weights[t, j] * d_out[t], zeros in the rows of choices with pos below 0; and
+ * d_weights_dev fp32 [T, k], <d_out[t], y[pos[t, j]]>, 0 for those. Either may be NULL and
+ * is left out then (y_dev too, without d_weights). pos is that of a moe_dispatch_tokens call:
+ * each row of d_y is written by the choice whose place it is.
+ */
+moe_status_t moe_combine_tokens_backward(const void* d_out_dev, int64_t d_stride, const void* y_dev, int32_t dtype,
+                                         int64_t y_stride, const int32_t* pos_dev, const float* weights_dev, int32_t T,
+                                         int32_t k, int32_t H, void* d_y_dev, float* d_weights_dev, void* stream);
+
+/*
+ * Rows to E4M3 (OCP: bias 7, largest finite 448, no infinities) with a scale for each
+ * block of 128 values of a row (the last one may be shorter):
+ *   scale_dev fp32 [T, ceil(K / 128)]   the block's largest magnitude times fp32(1/448), 1 where that is 0
+ *   q_dev E4M3 [T, K], no gaps          v / scale, rounded to fp32 and then to the nearest E4M3 value, halves to
+ *                                       even, held to +-448
+ * v is x, or with swiglu != 0 g / (1 + e^-g) * u of rows [g | u] of 2 K values, computed in
+ * fp32. A block with an infinity or a NaN has the scale NaN. x_dev: F32, BF16 or F16, rows
+ * x_stride elements apart. K is a multiple of 16 and at most MOE_BLOCK_MAX_K (else MOE_ERR_UNSUPPORTED);
+ * x and q 16-byte aligned, x_stride a multiple of 16 bytes; x overlaps neither output. T == 0 is a no-op.
+ */
+#define MOE_BLOCK_MAX_K 65536
+moe_status_t moe_block_quantize(const void* x_dev, int32_t x_dtype, int64_t x_stride, int32_t swiglu, int32_t T, int32_t K,
+                                void* q_dev, float* scale_dev, void* stream);
+
+/*
+ * Product in E4M3 with a scale for each 128 values of a row and each 128 x 128 of weights:
+ *   out[t, n] = sum_b x_scale[t, b] * w_scale[n / 128, b] * (sum over block b of x[t, k] * w[n, k])
+ * x_dev [T, K]: E4M3 with x_scale_dev fp32 [T, ceil(K / 128)], or BF16 / F16 / F32 with
+ * x_scale_dev NULL, which the call quantizes as moe_block_quantize does. w_dev E4M3 [N, K],
+ * w_scale_dev fp32 [ceil(N / 128), ceil(K / 128)]; out_dev [T, N] BF16, F16 or F32 without gaps,
+ * rounded once. Blocks are added up on the tensor cores in fp32, and their sums in fp32.
+ * Rows of x and w start x_stride and w_stride elements apart. K, the strides in bytes and
+ * the addresses of x and w are multiples of 16 (K else MOE_ERR_UNSUPPORTED); K <= MOE_BLOCK_MAX_K.
+ * out overlaps neither x nor w. T or N of 0 is a no-op. workspace_dev: moe_block_matmul_workspace() bytes (0 for E4M3
+ * rows), 256-byte aligned, free for reuse when the call's work on `stream` has finished.
+ */
+moe_status_t moe_block_matmul_workspace(int32_t rows, int32_t K, int32_t x_dtype, int64_t* bytes);
+moe_status_t moe_block_matmul(const void* x_dev, int32_t x_dtype, int64_t x_stride, const float* x_scale_dev,
+                              const void* w_dev, int64_t w_stride, const float* w_scale_dev, void* out_dev,
+                              int32_t out_dtype, int32_t T, int32_t N, int32_t K, void* workspace_dev,
+                              int64_t workspace_bytes, void* stream);
+
+/*
+ * The same for rows in the order of their experts: rows offsets[e] .. offsets[e + 1] of x
+ * (offsets_dev int32 [E + 1] on the device, as moe_dispatch_tokens writes them) are multiplied with
+ * w_dev E4M3 [E, N, K], w_scale_dev fp32 [E, ceil(N / 128), ceil(K / 128)], both without gaps. Rows of x that
+ * belong to no expert give rows of zeros in out_dev [M, N]. (Offsets outside [0, M] or falling are held to
+ * that range and to growing.) E <= MOE_BLOCK_MAX_EXPERTS; the workspace is that of M rows.
+ */
+#define MOE_BLOCK_MAX_EXPERTS 1024
+moe_status_t moe_block_grouped_matmul(const void* x_dev, int32_t x_dtype, int64_t x_stride, const float* x_scale_dev,
+                                      const int32_t* offsets_dev, const void* w_dev, const float* w_scale_dev,
+                                      void* out_dev, int32_t out_dtype, int32_t M, int32_t E, int32_t N, int32_t K,
+                                      void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* As moe_quant_sync_status and moe_quant_test_force_wait_timeout, of these products. */
+moe_status_t moe_block_sync_status(void* stream);
+void moe_block_test_force_wait_timeout(int32_t on);
 
 /* Name of a status code (static string). */
 const char* moe_status_string(moe_status_t status);

@@ -11,3 +11,6 @@ from .layer import MoeLayer, weights_from_raw  # noqa: F401
 from .lmhead import LmHead  # noqa: F401
 from .routing import route_experts, route_experts_backward  # noqa: F401
 from .int8 import int8_experts, int8_matmul, int8_sync_status  # noqa: F401
+from .tokens import (combine_tokens, combine_tokens_backward, dispatch_tokens,  # noqa: F401
+                     dispatch_tokens_backward)
+from .fp8 import fp8_grouped_matmul, fp8_matmul, fp8_quantize, fp8_sync_status  # noqa: F401

@@ -35,6 +35,7 @@ MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
 MOE_DTYPE_F16 = 2
 MOE_DTYPE_S8 = 3
+MOE_DTYPE_E4M3 = 4
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 MOE_ROUTE_MAX_EXPERTS = 512
@@ -42,6 +43,9 @@ MOE_ROUTE_MAX_TOP_K = 32
 MOE_ROUTE_MAX_GROUPS = 32
 MOE_INT8_MAX_K = 65536
 MOE_INT8_MAX_EXPERTS = 1024
+MOE_DISPATCH_MAX_EXPERTS = 1024
+MOE_BLOCK_MAX_K = 65536
+MOE_BLOCK_MAX_EXPERTS = 1024
 
 MOE_PATH_NONE = 0
 MOE_PATH_DECODE_GEMV = 1
@@ -142,6 +146,25 @@ _SIGNATURES = {
                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     "moe_quant_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
     "moe_quant_test_force_wait_timeout": (None, [ctypes.c_int32]),
+    "moe_dispatch_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                           ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 3 +
+                            [ctypes.c_void_p] * 5),
+    "moe_combine_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_void_p] + [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 2),
+    "moe_combine_tokens_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
+                                                   ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p] +
+                                    [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 3),
+    "moe_block_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64] + [ctypes.c_int32] * 3 +
+                           [ctypes.c_void_p] * 3),
+    "moe_block_matmul_workspace": (ctypes.c_int, [ctypes.c_int32] * 3 + [ctypes.POINTER(ctypes.c_int64)]),
+    "moe_block_matmul": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p] +
+                         [ctypes.c_int32] * 4 + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "moe_block_grouped_matmul": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64] +
+                                 [ctypes.c_void_p] * 5 + [ctypes.c_int32] * 5 +
+                                 [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "moe_block_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
+    "moe_block_test_force_wait_timeout": (None, [ctypes.c_int32]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_cuda_error": (ctypes.c_char_p, []),
 }

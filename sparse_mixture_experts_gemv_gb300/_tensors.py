@@ -55,6 +55,41 @@ def refuse_gradients(what: str, *tensors):
             invalid(what, "has no gradient, and an input requires one: detach it, or call under torch.no_grad()")
 
 
+class Gradient(torch.autograd.Function):
+    """A gradient as a step of a recorded graph: it has no derivative of its own, and says so when asked for one."""
+
+    @staticmethod
+    def forward(ctx, what, fn, *args):
+        ctx.what = what
+        return fn(*args)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.what} has no second derivative")
+
+
+def gradient(what: str, fn, tensors, *args):
+    """fn(*tensors, *args), in the recorded graph where one is recorded."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return Gradient.apply(what, fn, *tensors, *args)
+    return fn(*tensors, *args)
+
+
+def rows16(t, K, what, name):
+    """A matrix whose rows the kernels can read in 16-byte pieces (addresses and row strides), its address and row
+    stride; one that is not so is copied."""
+    size, ptr = t.element_size(), t.data_ptr()
+    stride, inner = t.stride()
+    if inner != 1 or stride < K or (ptr | stride * size) & 15:
+        if size == 1 and t.dtype is not torch.int8:   # 8-bit floating point is copied as the bytes it is
+            t = t.view(torch.uint8).clone(memory_format=torch.contiguous_format).view(t.dtype)
+        else:
+            t = t.clone(memory_format=torch.contiguous_format)
+        ptr, stride = t.data_ptr(), K
+        want(K * size % 16 == 0, what, f"the rows of {name} must be a multiple of 16 bytes long")
+    return t, ptr, stride
+
+
 _device = torch._C._cuda_getDevice   # the current device's index, likewise
 
 
