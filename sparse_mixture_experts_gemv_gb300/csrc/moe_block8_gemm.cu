@@ -6,7 +6,7 @@
 // The MMA multiplies E4M3 by E4M3 into fp32 accumulators, but knows nothing of scales that are no
 // powers of two. So each block of 128 of K is a product of its own in tensor memory, and eight
 // epilogue warps add it, times its scale, to sums in registers while the tensor cores work on
-// the next block in the other half of tensor memory. Rows are the lanes of tensor memory and
+// the next blocks in other columns of tensor memory. Rows are the lanes of tensor memory and
 // channels its columns: then a thread's values of a block have one scale, its row's times the
 // 128 channels', and an element costs one FMA. (Channels as lanes would let a tile have fewer rows than
 // 128, but every element would need a scale of its own from shared memory. A tile with few
@@ -14,8 +14,10 @@
 // make 256 operations of a weight byte, and the tensor cores do some 500 in a byte's time.)
 //
 // One persistent CTA an SM, warp-specialised:
-//   warp 0        rows and weights by TMA into a ring, a block of K a stage
+//   warp 0        weights by TMA into a ring, a block of K a stage
 //   warp 1        issues the MMAs
+//   warp 2        rows by TMA into the same ring
+//   warp 3        scales into a ring of their own, four blocks a slot
 //   warps 4-11    epilogue: four warps for each half of the columns
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -36,22 +38,32 @@ namespace {
 using namespace sm100;
 
 constexpr int kRows = 128;                // rows of a tile = lanes of tensor memory
-constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 128 + kEpilogueWarps * 32;
 constexpr int kMaxStages = 16;
-constexpr int kRingBytes = 192 * 1024;
-constexpr int kTurnBytes = 8 * 2048;      // 32 rows x 64 bytes for each epilogue warp
+constexpr int kDone = 16;                 // completions of blocks: no fewer than stages or products
 constexpr int kMaxGroups = MOE_BLOCK_MAX_EXPERTS;
 constexpr int kTableBytes = 2 * (kMaxGroups + 4) * 4;
-constexpr int kFixedSmem = 1024 /*align*/ + kTurnBytes + kTableBytes + 1024 /*barriers*/;
+constexpr int kScaleSlots = 4;            // of four blocks: each row's, and that of the tile's block of 128 channels
+constexpr int kBlockFloats = kRows + 4;
+constexpr int kSlotFloats = 4 * kBlockFloats;
+constexpr int kFixedSmem = 1024 /*align*/ + kTableBytes + kScaleSlots * kSlotFloats * 4 + 512 /*barriers*/;
+// A tile's results in 16 bits, in units of 32 rows x 64 bytes: they leave on their own while the next tile is computed.
+// (Stored by the warps themselves they left all SMs at once, and the next tiles waited for them: 1.8 us a tile of
+// 128 x 256.)
+template <int NT>
+constexpr int kTurnBytes = kRows * NT * 2;
+template <int NT>
+constexpr int kRingBytes = (232448 /*an SM's shared memory*/ - kFixedSmem - kTurnBytes<NT>) / 1024 * 1024;
 // A stage of few rows holds only those; the MMA reads 128 all the same, into what lies behind (their results are not
 // used): the buffers behind the last stage are as long as that.
-static_assert(kTurnBytes >= kRows * kBlock, "the MMA reads past the last stage");
+static_assert(kTurnBytes<64> >= kRows * kBlock, "the MMA reads past the last stage");
 
 __device__ int g_gemm_error;              // MOE_ERR_TIMEOUT once a bounded wait ran out
 
 struct Params {
   const int* offsets;
-  int rows, channels, groups, K;
+  int rows, channels, groups;
   int tiles_n;               // channel tiles of a group
   int blocks;                // of K
   int row_blocks;            // channels' blocks of 128
@@ -61,6 +73,7 @@ struct Params {
   void* out;
   int out_dtype;
   int wide;                  // rows of out are 16-byte aligned
+  int scales_wide;           // and those of x_scale
   int withhold;              // test only: no rows come, so that the waits for them run out
 };
 
@@ -68,6 +81,7 @@ struct Params {
 struct Maps {
   CUtensorMap w;
   CUtensorMap x[4];
+  CUtensorMap out;           // units of results, where rows are 16-byte aligned
 };
 MOE_DEV int box_of(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
 
@@ -110,7 +124,6 @@ MOE_DEV void mma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc
 
 // First rows and first tiles of the groups, by all threads: offsets are held to [0, rows] and to growing, so that
 // whatever they are, tiles lie within the rows and apart.
-template <int NT>
 MOE_DEV void make_tables(const Params& p, int* first, int* row, int* scratch) {
   constexpr int kPer = (kMaxGroups + kThreads) / kThreads;
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
@@ -173,6 +186,113 @@ MOE_DEV void make_tables(const Params& p, int* first, int* row, int* scratch) {
   __syncthreads();
 }
 
+// 32 columns of the lane on their way from tensor memory, and the wait for them: r is used behind it.
+MOE_DEV void tmem_request32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+MOE_DEV void tmem_arrived32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :: "memory");
+}
+// acc[i] += v[i] * scale for 32 values, two an instruction.
+MOE_DEV void add32(float2* acc, const uint32_t* v, float scale) {
+  const float2 s = make_float2(scale, scale);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    acc[i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s, acc[i]);
+}
+
+MOE_DEV float shared_f32(uint32_t a) {
+  float f;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
+  return f;
+}
+// Where an epilogue lane finds its scales: its row's, and that of the tile's block of 128 channels.
+struct Scales {
+  uint32_t full, empty;      // first barriers
+  uint32_t row, channels;    // addresses within a slot
+  int at, ph;
+};
+
+// Four blocks' scales of a row, written by a kernel that this one may overlap; those past the end are not used.
+MOE_DEV float4 four_scales(const Params& p, const float* xs, int b) {
+  if (p.scales_wide) {
+    const uint4 u = ldg_cg(xs + b);
+    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  const int last = p.blocks - 1;
+  return make_float4(ldg_cg_f32(xs + b), ldg_cg_f32(xs + min(b + 1, last)), ldg_cg_f32(xs + min(b + 2, last)),
+                     ldg_cg_f32(xs + min(b + 3, last)));
+}
+
+// Where an epilogue warp is.
+struct Ring {
+  uint32_t done, empty;      // first barriers
+  uint32_t block;
+};
+
+// All blocks of a tile's C chunks of 32 channels (of one block of 128): acc += scale * product, 32 columns on their way
+// while the 32 before them are added. `there` false: no rows or channels, and the products are let go. What is done
+// once a block bounds it, so that all of it is in registers: parameters, behind the barriers' memory clobbers, would
+// be read again every time.
+template <int C, int NT>
+MOE_DEV void add_blocks(float2 (&acc)[16 * C], Scales& scales, Ring& ring, uint32_t taddr, int blocks, bool there,
+                        volatile int* abort_flag) {
+  Scales sc = scales;
+  Ring r = ring;
+  const bool first = (threadIdx.x & 31) == 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < blocks; b0 += 4) {
+    lane_wait(sc.full + 8 * sc.at, sc.ph, &g_gemm_error, abort_flag);
+    uint32_t row = sc.row + sc.at * (kSlotFloats * 4), channels = sc.channels + sc.at * (kSlotFloats * 4);
+    const uint32_t last = row + min(4, blocks - b0) * (kBlockFloats * 4);
+#pragma unroll 1
+    do {
+      const float scale = shared_f32(row) * shared_f32(channels);
+      lane_wait(r.done + 8 * (r.block % kDone), r.block / kDone & 1, &g_gemm_error, abort_flag);
+      tc_fence_after();
+      const uint32_t now = taddr + r.block % (512 / NT) * NT, empty = r.empty + 8 * (r.block % (512 / NT));
+      if (there) {
+        uint32_t v[2][32];
+        tmem_request32(now, v[0]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          tmem_arrived32(v[c & 1]);
+          if (c + 1 < C) {
+            tmem_request32(now + 32 * (c + 1), v[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (first) arrive(empty);
+          }
+          add32(acc + 16 * c, v[c & 1], scale);
+        }
+      } else if (first) {
+        arrive(empty);
+      }
+      ++r.block;
+      row += kBlockFloats * 4;
+      channels += kBlockFloats * 4;
+    } while (row != last);
+    __syncwarp();
+    if (first) arrive(sc.empty + 8 * sc.at);
+    if (++sc.at == kScaleSlots) { sc.at = 0; sc.ph ^= 1; }
+  }
+  scales = sc;
+  ring = r;
+}
+
 template <int OUT>
 MOE_DEV uint32_t pack2(float a, float b) {
   if (OUT == MOE_DTYPE_BF16) {
@@ -183,15 +303,26 @@ MOE_DEV uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 64 bytes of each of the warp's 32 rows, turned in shared memory so that eight rows leave at a time in 16-byte
-// pieces. v: the lane's row, 16 words.
-MOE_DEV void store_rows(uint8_t* turn, const uint32_t (&v)[16], const Params& p, int64_t row0, int rows, int ch0, int size) {
+// A unit of results in shared memory: the lane's row, 16 words. Chunk c of row r lies at c ^ (r / 2 % 4), the 64-byte
+// swizzle.
+MOE_DEV void put_unit(uint8_t* unit, const uint32_t (&v)[16]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int c = 0; c < 4; ++c)   // chunk c of row r lies at c ^ (r / 2 % 4): no bank twice in either direction
-    *reinterpret_cast<uint4*>(turn + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) =
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(unit + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) =
         make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-  __syncwarp();
+}
+MOE_DEV void store_2d(const CUtensorMap* map, int c0, int c1, const void* smem) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+               :: "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(smem)) : "memory");
+}
+MOE_DEV void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+MOE_DEV void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+MOE_DEV void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A unit of fewer rows than 32 (the next ones are another group's), or of rows off 16-byte boundaries, by the warp.
+MOE_DEV void copy_unit(const uint8_t* unit, const Params& p, int64_t row0, int rows, int ch0, int size) {
+  const int lane = threadIdx.x & 31;
   const int64_t ld = (int64_t)p.channels * size;
   uint8_t* out = static_cast<uint8_t*>(p.out) + row0 * ld + (int64_t)ch0 * size;
   const int n = min(64, (p.channels - ch0) * size);   // bytes of a row that there are
@@ -202,59 +333,78 @@ MOE_DEV void store_rows(uint8_t* turn, const uint32_t (&v)[16], const Params& p,
       const int r = 8 * i + (lane >> 2);
       if (r < rows && 16 * c < n)
         *reinterpret_cast<uint4*>(out + r * ld + 16 * c) =
-            *reinterpret_cast<const uint4*>(turn + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+            *reinterpret_cast<const uint4*>(unit + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
     }
   } else if (size == 4) {
-    for (int i = lane >> 4; i < rows; i += 2) {
-      const int b = (lane & 15) * 4;
-      if (b < n)
+    const int b = (lane & 15) * 4;
+    if (b < n)
+      for (int i = lane >> 4; i < rows; i += 2)
         *reinterpret_cast<uint32_t*>(out + i * ld + b) =
-            *reinterpret_cast<const uint32_t*>(turn + i * 64 + (((b >> 4) ^ (i >> 1 & 3)) << 4) + (b & 15));
-    }
+            *reinterpret_cast<const uint32_t*>(unit + i * 64 + (((b >> 4) ^ (i >> 1 & 3)) << 4) + (b & 15));
   } else {
     const int b = lane * 2;
     if (b < n)
       for (int i = 0; i < rows; ++i)
         *reinterpret_cast<uint16_t*>(out + i * ld + b) =
-            *reinterpret_cast<const uint16_t*>(turn + i * 64 + (((b >> 4) ^ (i >> 1 & 3)) << 4) + (b & 15));
+            *reinterpret_cast<const uint16_t*>(unit + i * 64 + (((b >> 4) ^ (i >> 1 & 3)) << 4) + (b & 15));
   }
-  __syncwarp();
 }
 
+// N units of `step` channels from ch0 on leave.
+template <int N>
+MOE_DEV void store_units(uint8_t* turn, const CUtensorMap* map, const Params& p, int64_t row0, int rows, int ch0, int size) {
+  const int step = 64 / size;
+  if (p.wide && rows == 32) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (elect()) {
+      for (int c = 0; c < N; ++c)
+        if (ch0 + c * step < p.channels) store_2d(map, ch0 + c * step, (int)row0, turn + c * 2048);
+      store_commit();
+    }
+  } else {
+    __syncwarp();
+    for (int c = 0; c < N; ++c)
+      if (ch0 + c * step < p.channels) copy_unit(turn + c * 2048, p, row0, rows, ch0 + c * step, size);
+  }
+}
+
+// NT: channels of a tile.
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
-  constexpr int kCols = NT / 2;             // of an epilogue warp
-  constexpr uint32_t kTmem = 2 * NT;        // two products
+  constexpr int kProducts = 512 / NT;       // in tensor memory at once
+  static_assert(kProducts <= kDone, "a completion each");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* s_turn = smem + p.stages * p.stage_bytes;
-  int* first = reinterpret_cast<int*>(s_turn + kTurnBytes);
+  int* first = reinterpret_cast<int*>(s_turn + kTurnBytes<NT>);
   int* row = first + kMaxGroups + 4;
-  uint64_t* full = reinterpret_cast<uint64_t*>(row + kMaxGroups + 4);
-  uint64_t* empty = full + kMaxStages;
-  uint64_t* d_full = empty + kMaxStages;
-  uint64_t* d_empty = d_full + 2;
-  uint64_t* drain = d_empty + 2;
+  float* s_scale = reinterpret_cast<float*>(row + kMaxGroups + 4);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + kScaleSlots * kSlotFloats);
+  uint64_t* done = full + kMaxStages;
+  uint64_t* d_empty = done + kDone;
+  uint64_t* sc_full = d_empty + kProducts;
+  uint64_t* sc_empty = sc_full + kScaleSlots;
+  uint64_t* drain = sc_empty + kScaleSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* scratch = reinterpret_cast<int*>(tmem_slot + 2);   // [kThreads / 32]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 2);
+    for (int a = 0; a < kDone; ++a) mbar_init(&done[a], 1);
+    for (int a = 0; a < kScaleSlots; ++a) {
+      mbar_init(&sc_full[a], 1);
+      mbar_init(&sc_empty[a], kEpilogueWarps);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&d_full[a], 1);
-      mbar_init(&d_empty[a], 8);
-    }
+    for (int a = 0; a < kProducts; ++a) mbar_init(&d_empty[a], kEpilogueWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&maps.w);
   }
-  if (warp == 1) tmem_alloc(tmem_slot, kTmem);
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -263,141 +413,185 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
   pdl_wait();
   asm volatile("fence.proxy.async.global;" ::: "memory");   // rows written by the kernel before, read by TMA here
   pdl_launch_dependents();
-  make_tables<NT>(p, first, row, scratch);
+  make_tables(p, first, row, scratch);
   const int total = first[p.groups];
   Finder finder = {first, row, 0};
 
-  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), ring0 = smem_u32(smem);
-  if (warp == 0) {
-    // ---------------------------------------------------- rows and weights
+  // One completion a block, behind its MMAs: it frees the stage for the copies and hands the product to the epilogue.
+  const uint32_t full0 = smem_u32(full), done0 = smem_u32(done), ring0 = smem_u32(smem);
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------ weights (0), rows (2)
+    const int blocks = p.blocks, stages = p.stages;
+    const uint32_t stage_bytes = p.stage_bytes;
     uint32_t it = 0;
-    int s = 0, ph = 1;
+    int s = 0;
     bool stop = p.withhold != 0;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = finder.find<NT>(p, tile);
       const int box = box_of(t.rows);
-      const CUtensorMap* map = &maps.x[box];
-      const uint32_t bytes = (uint32_t)((16 << box) + NT) * kBlock;
-      for (int b = 0; b < p.blocks; ++b, ++it) {
-        if (!warp_wait(empty0 + 8 * s, ph, &g_gemm_error, abort_flag)) { stop = true; break; }
+      const CUtensorMap* map = warp == 0 ? &maps.w : &maps.x[box];
+      const uint32_t bytes = (uint32_t)(warp == 0 ? NT : 16 << box) * kBlock;
+      const uint32_t to = ring0 + (warp == 0 ? p.a_bytes : 0);
+      const int at = warp == 0 ? t.e * p.channels + t.n0 : t.row0;
+      for (int b = 0; b < blocks; ++b, ++it) {
+        const uint32_t was = it - stages;   // the block whose stage this is
+        if (it >= (uint32_t)stages &&
+            !warp_wait(done0 + 8 * (was % kDone), was / kDone & 1, &g_gemm_error, abort_flag)) {
+          stop = true;
+          break;
+        }
         if (elect()) {
-          const uint32_t bar = full0 + 8 * s, dst = ring0 + s * p.stage_bytes;
-          expect_tx(bar, bytes);
-          load_2d(dst + p.a_bytes, &maps.w, b * kBlock, t.e * p.channels + t.n0, bar);
-          load_2d(dst, map, b * kBlock, t.row0, bar);
+          expect_tx(full0 + 8 * s, bytes);
+          load_2d(to + s * stage_bytes, map, b * kBlock, at, full0 + 8 * s);
         }
         __syncwarp();
-        if (++s == p.stages) { s = 0; ph ^= 1; }
+        if (++s == stages) s = 0;
       }
     }
     land(full, p.stages, it, &g_gemm_error, abort_flag);
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
+    // What is done between two blocks, some 400 cycles, bounds it: so two blocks are issued at once where both are
+    // there, their waits overlap, and one commit a block serves both sides.
     constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-    const uint32_t d_full0 = smem_u32(d_full), d_empty0 = smem_u32(d_empty);
-    int s = 0, ph = 0;
-    uint32_t ab = 0, d_ph = 1;
+    const uint32_t d_empty0 = smem_u32(d_empty);
+    const int blocks = p.blocks, stages = p.stages;
+    const uint32_t stage_bytes = p.stage_bytes, a_bytes = p.a_bytes;
+    int s = 0, ph = 0, ab = 0, d_ph = 1;
+    uint32_t it = 0;
     bool stop = false;
+    const auto issue = [&](int s, int ab, uint32_t it) {
+      const uint32_t at = ring0 + s * stage_bytes, d = tmem + ab * NT;
+      const uint64_t adesc = smem_desc_sw128(at), bdesc = smem_desc_sw128(at + a_bytes);
+#pragma unroll
+      for (int kk = 0; kk < kBlock / 32; ++kk)   // 32 of K: 32 bytes, 2 in the descriptors
+        mma_e4m3(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+      commit(done0 + 8 * (it % kDone));
+    };
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
-      for (int b = 0; b < p.blocks; ++b) {
-        if (!warp_wait(d_empty0 + 8 * ab, d_ph, &g_gemm_error, abort_flag) ||
-            !warp_wait(full0 + 8 * s, ph, &g_gemm_error, abort_flag)) {
+      for (int b = 0; b < blocks;) {
+        int s1 = s + 1, ph1 = ph, ab1 = ab + 1, d_ph1 = d_ph;
+        if (s1 == stages) { s1 = 0; ph1 ^= 1; }
+        if (ab1 == kProducts) { ab1 = 0; d_ph1 ^= 1; }
+        const bool one = try_wait(d_empty0 + 8 * ab, d_ph) & try_wait(full0 + 8 * s, ph);
+        const bool two = (b + 1 < blocks) & test_wait(d_empty0 + 8 * ab1, d_ph1) & test_wait(full0 + 8 * s1, ph1);
+        const bool both = __all_sync(0xFFFFFFFFu, one & two);
+        if (!both && !__all_sync(0xFFFFFFFFu, one) &&
+            (!warp_wait(d_empty0 + 8 * ab, d_ph, &g_gemm_error, abort_flag) ||
+             !warp_wait(full0 + 8 * s, ph, &g_gemm_error, abort_flag))) {
           stop = true;
           break;
         }
         tc_fence_after();
-        const uint32_t at = ring0 + s * p.stage_bytes, d = tmem + ab * NT;
-        const uint64_t adesc = smem_desc_sw128(at), bdesc = smem_desc_sw128(at + p.a_bytes);
         if (elect()) {
-#pragma unroll
-          for (int kk = 0; kk < kBlock / 32; ++kk)   // 32 of K: 32 bytes, 2 in the descriptors
-            mma_e4m3(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0 ? 1u : 0u);
-          commit(empty0 + 8 * s);
-          commit(d_full0 + 8 * ab);
+          issue(s, ab, it);
+          if (both) issue(s1, ab1, it + 1);
         }
         __syncwarp();
-        if (++s == p.stages) { s = 0; ph ^= 1; }
-        ab ^= 1;
-        d_ph ^= ab ^ 1;   // flips when the halves come round
+        s = s1; ph = ph1; ab = ab1; d_ph = d_ph1;
+        ++b;
+        ++it;
+        if (both) {
+          if (++s == stages) { s = 0; ph ^= 1; }
+          if (++ab == kProducts) { ab = 0; d_ph ^= 1; }
+          ++b;
+          ++it;
+        }
       }
     }
     if (elect()) mma_commit(drain);   // all MMAs complete before tensor memory is released
     __syncwarp();
     mbar_wait(drain, 0, &g_gemm_error, abort_flag, 2000000000LL, false);
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3, half = (warp - 4) >> 2;
-    uint8_t* turn = s_turn + (warp - 4) * 2048;
-    const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
-    const uint32_t d_full0 = smem_u32(d_full), d_empty0 = smem_u32(d_empty);
-    uint32_t ab = 0, ph = 0;
+  } else if (warp == 3) {
+    // -------------------------------------------------------------- scales
+    const uint32_t sc_full0 = smem_u32(sc_full), sc_empty0 = smem_u32(sc_empty);
+    int at = 0, ph = 1;
     bool stop = false;
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = finder.find<NT>(p, tile);
+      const float* ws = p.w_scale + ((int64_t)t.e * p.row_blocks + t.n0 / kBlock) * p.blocks;
+      for (int b = 0; b < p.blocks; b += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = four_scales(p, p.x_scale + (int64_t)(t.row0 + min(lane + 32 * i, t.rows - 1)) * p.blocks, b);
+        const float w = __ldg(ws + min(b + (lane & 3), p.blocks - 1));
+        if (!warp_wait(sc_empty0 + 8 * at, ph, &g_gemm_error, abort_flag)) { stop = true; break; }
+        float* slot = s_scale + at * kSlotFloats;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          slot[lane + 32 * i] = x[i].x;
+          slot[kBlockFloats + lane + 32 * i] = x[i].y;
+          slot[2 * kBlockFloats + lane + 32 * i] = x[i].z;
+          slot[3 * kBlockFloats + lane + 32 * i] = x[i].w;
+        }
+        if (lane < 4) slot[lane * kBlockFloats + kRows] = w;
+        __syncwarp();
+        if (lane == 0) arrive(sc_full0 + 8 * at);
+        if (++at == kScaleSlots) { at = 0; ph ^= 1; }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    constexpr int kCols = NT / 2;             // of a warp
+    const int quad = warp & 3, half = (warp - 4) >> 2, blocks = p.blocks;
+    uint8_t* turn = s_turn + (warp - 4) * (kTurnBytes<NT> / kEpilogueWarps);
+    const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
+    Ring ring = {done0, smem_u32(d_empty), 0};
+    Scales sc = {smem_u32(sc_full), smem_u32(sc_empty), smem_u32(s_scale + quad * 32 + lane),
+                 smem_u32(s_scale + kRows), 0, 0};
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      const Tile t = finder.find<NT>(p, tile);
       const int rows = min(32, t.rows - quad * 32);   // of this warp
       const int ch0 = t.n0 + half * kCols;
-      const bool work = rows > 0 && ch0 < p.channels;
-      const float* xs = p.x_scale + (int64_t)(t.row0 + min(quad * 32 + lane, t.rows - 1)) * p.blocks;
-      const float* ws = p.w_scale + ((int64_t)t.e * p.row_blocks + min(ch0, p.channels - 1) / kBlock) * p.blocks;
-      float acc[kCols];
+      const bool there = rows > 0 && ch0 < p.channels;
+      float2 acc[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-      float x_next = ldg_cg_f32(xs), w_next = __ldg(ws);
-      for (int b = 0; b < p.blocks; ++b) {
-        const float scale = x_next * w_next;
-        if (b + 1 < p.blocks) {
-          x_next = ldg_cg_f32(xs + b + 1);
-          w_next = __ldg(ws + b + 1);
-        }
-        if (!warp_wait(d_full0 + 8 * ab, ph, &g_gemm_error, abort_flag)) { stop = true; break; }
-        tc_fence_after();
-        if (work) {
-#pragma unroll
-          for (int c = 0; c < kCols; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(taddr + ab * NT + c, v);
-            if (c + 32 == kCols) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) arrive(d_empty0 + 8 * ab);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), scale, acc[c + i]);
-          }
-        } else if (lane == 0) {
-          arrive(d_empty0 + 8 * ab);
-        }
-        ab ^= 1;
-        ph ^= ab ^ 1;
-      }
-      if (stop || !work) continue;
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      add_blocks<kCols / 32, NT>(acc, sc, ring, taddr, blocks, there, abort_flag);
+      if (!there) continue;
       const int64_t row0 = t.row0 + quad * 32;
-      const int size = p.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
-      if (size == 4) {
+      constexpr int kUnits = kCols / 32;
+      if (p.out_dtype == MOE_DTYPE_F32) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          uint32_t v[16];
+        for (int part = 0; part < 2; ++part) {   // the buffer holds half of them
+          if (elect()) store_wait_read();
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[c + i]);
-          if (ch0 + c < p.channels) store_rows(turn, v, p, row0, rows, ch0 + c, 4);
+          for (int c = 0; c < kUnits; ++c) {
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              v[2 * i] = __float_as_uint(acc[8 * (kUnits * part + c) + i].x);
+              v[2 * i + 1] = __float_as_uint(acc[8 * (kUnits * part + c) + i].y);
+            }
+            put_unit(turn + c * 2048, v);
+          }
+          store_units<kUnits>(turn, &maps.out, p, row0, rows, ch0 + part * kCols / 2, 4);
         }
       } else {
+        if (elect()) store_wait_read();
+        __syncwarp();
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
+        for (int c = 0; c < kUnits; ++c) {
           uint32_t v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            v[i] = p.out_dtype == MOE_DTYPE_BF16 ? pack2<MOE_DTYPE_BF16>(acc[c + 2 * i], acc[c + 2 * i + 1])
-                                                 : pack2<MOE_DTYPE_F16>(acc[c + 2 * i], acc[c + 2 * i + 1]);
-          if (ch0 + c < p.channels) store_rows(turn, v, p, row0, rows, ch0 + c, 2);
+            v[i] = p.out_dtype == MOE_DTYPE_BF16 ? pack2<MOE_DTYPE_BF16>(acc[16 * c + i].x, acc[16 * c + i].y)
+                                                 : pack2<MOE_DTYPE_F16>(acc[16 * c + i].x, acc[16 * c + i].y);
+          put_unit(turn + c * 2048, v);
         }
+        store_units<kUnits>(turn, &maps.out, p, row0, rows, ch0, 2);
       }
     }
+    if (elect()) store_wait();
+    __syncwarp();
     // rows before the first group and behind the last one are zeros
     const int64_t ld = (int64_t)p.channels * (p.out_dtype == MOE_DTYPE_F32 ? 4 : 2) / 2;   // in 16-bit words
     const int64_t head = row[0] * ld, tail = row[p.groups] * ld, end = p.rows * ld;
     uint16_t* out = static_cast<uint16_t*>(p.out);
-    const int64_t step = (int64_t)gridDim.x * 256, i0 = (int64_t)blockIdx.x * 256 + threadIdx.x - 128;
+    constexpr int kLanes = kEpilogueWarps * 32;
+    const int64_t step = (int64_t)gridDim.x * kLanes, i0 = (int64_t)blockIdx.x * kLanes + threadIdx.x - 128;
     for (int64_t i = i0; i < head; i += step) out[i] = 0;
     for (int64_t i = tail + i0; i < end; i += step) out[i] = 0;
   }
@@ -406,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmem);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -415,6 +609,15 @@ cudaError_t encode(CUtensorMap* m, const void* base, int64_t rows, int K, int64_
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
   const cuuint32_t box[2] = {kBlock, box_rows};
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box);
+}
+
+cudaError_t encode_out(CUtensorMap* m, const GemmArgs& a, int size) {
+  const CUtensorMapDataType type = a.out_dtype == MOE_DTYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : a.out_dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.channels, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.channels * size};
+  const cuuint32_t box[2] = {(cuuint32_t)(64 / size), 32};
+  return encode_tensor_map(m, type, 2, a.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 thread_local int t_withhold = 0;
@@ -428,27 +631,30 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
     if (a.rows <= 16 << i) break;
   }
   if (e != cudaSuccess) return e;
+  const int size = a.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
   Params p = {};
+  p.wide = !(((uintptr_t)a.out | (uint64_t)a.channels * size) & 15);
+  if (p.wide) e = encode_out(&maps.out, a, size);
+  if (e != cudaSuccess) return e;
   p.offsets = a.offsets;
   p.rows = a.rows;
   p.channels = a.channels;
   p.groups = a.groups;
-  p.K = a.K;
   p.tiles_n = (a.channels + NT - 1) / NT;
   p.blocks = (a.K + kBlock - 1) / kBlock;
   p.row_blocks = (a.channels + kBlock - 1) / kBlock;
   const int box = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 ? 64 : kRows;
   p.a_bytes = box * kBlock;
   p.stage_bytes = p.a_bytes + NT * kBlock;
-  p.stages = kRingBytes / p.stage_bytes;
+  p.stages = kRingBytes<NT> / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.x_scale = a.x_scale;
   p.w_scale = a.w_scale;
   p.out = a.out;
   p.out_dtype = a.out_dtype;
-  p.wide = !(((uintptr_t)a.out | (uint64_t)a.channels * (a.out_dtype == MOE_DTYPE_F32 ? 4 : 2)) & 15);
+  p.scales_wide = !((uintptr_t)a.x_scale & 15) && p.blocks % 4 == 0;
   p.withhold = t_withhold;
-  const size_t smem = (size_t)p.stages * p.stage_bytes + kFixedSmem;
+  const size_t smem = (size_t)p.stages * p.stage_bytes + kTurnBytes<NT> + kFixedSmem;
   // at most one tile a group more than the rows fill
   int64_t tiles = (a.rows + kRows - 1) / kRows;
   if (a.offsets) tiles += a.groups < a.rows ? a.groups : a.rows;
@@ -460,7 +666,8 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !allowed[dev]) {
-    e = cudaFuncSetAttribute(block8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + kFixedSmem);
+    e = cudaFuncSetAttribute(block8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kRingBytes<NT> + kTurnBytes<NT> + kFixedSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed[dev] = true;
   }
@@ -482,12 +689,14 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
 void test_withhold(int on) { t_withhold = on; }
 
 cudaError_t launch_gemm(const GemmArgs& a, int num_sms, cudaStream_t s) {
-  // the widest tile that still gives every SM one
+  // Narrow tiles while each has an SM of its own, wide ones beyond. A block of K takes a CTA some 290 ns with 128 channels
+  // and 215 with 64; rows fetched for 64 channels are fetched twice as often. GB300, us, 128 / 64: 333 x 2,560 x 1,537
+  // 10.3 / 8.1; 32 rows of 512 experts, 2,560 x 1,536 27 / 32; 1 x 2,560 x 157,184 68 / 85; 4,096 x 2,048 x 4,096
+  // 40 / 57; 32,768 rows of 256 experts, 2,048 x 1,024 115 / 158. (256 channels: 16, 33, 76, 41, 118: two warps a
+  // scheduler with 128 sums a lane have no registers left to keep loads from tensor memory on their way.)
   const int64_t groups = a.offsets ? (a.rows < a.groups ? a.rows : a.groups) : 1;
   const int64_t tm = a.offsets ? (a.rows / kRows > groups ? a.rows / kRows : groups) : (a.rows + kRows - 1) / kRows;
-  if (tm * ((a.channels + 255) / 256) >= num_sms) return launch_tile<256>(a, num_sms, s);
-  if (tm * ((a.channels + 127) / 128) >= num_sms) return launch_tile<128>(a, num_sms, s);
-  return launch_tile<64>(a, num_sms, s);
+  return tm * ((a.channels + 63) / 64) <= num_sms ? launch_tile<64>(a, num_sms, s) : launch_tile<128>(a, num_sms, s);
 }
 
 cudaError_t gemm_status(cudaStream_t s, int* code) {

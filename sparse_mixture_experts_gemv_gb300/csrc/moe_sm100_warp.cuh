@@ -25,10 +25,27 @@ MOE_DEV bool try_wait(uint32_t bar, uint32_t parity) {
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
+// Whether the phase is complete, without any waiting.
+MOE_DEV bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// try_wait for one that will wait: asleep until the phase completes or some 20 us have passed, instead of taking turns
+// from the warps that work.
+MOE_DEV bool try_wait_asleep(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity), "r"(20000u) : "memory");
+  return ok != 0;
+}
 // Bounded: about two seconds, after which every role winds down and the error word is set.
 static __device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
   const long long t0 = clock64();
-  while (!__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) {
+  while (!__all_sync(0xFFFFFFFFu, try_wait_asleep(bar, parity))) {
     if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
     if (__any_sync(0xFFFFFFFFu, clock64() - t0 > 4000000000LL)) {
       set_error(err, kDevTimeout);
@@ -37,6 +54,21 @@ static __device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, int
     }
   }
   return true;
+}
+// The same for a role that has no registers left for a call, nor time for a vote: each lane waits by itself. Lanes may
+// give up apart, so that nobody stops here: a role goes on to its end with whatever there is, and after the first wait
+// that ran out (or an abort elsewhere) no other one waits.
+MOE_DEV void lane_wait(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+  if (!try_wait(bar, parity)) {
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!try_wait_asleep(bar, parity) && !*abort)
+      if (clock64() - t0 > 4000000000LL) {
+        set_error(err, kDevTimeout);
+        *abort = 1;
+      }
+  }
+  __syncwarp();
 }
 // A wait by a whole warp, which goes on or gives up as one.
 MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {

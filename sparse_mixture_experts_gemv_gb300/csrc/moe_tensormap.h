@@ -1,4 +1,4 @@
-// Tensor maps of row-major operands with the 128-byte swizzle, zeros outside.
+// Tensor maps of row-major operands, zeros outside.
 #pragma once
 
 #include <cuda.h>
@@ -21,12 +21,13 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 inline cudaError_t encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
-                                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+                                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   PFN_cuTensorMapEncodeTiled_v12000 f = tensor_map_encoder();
   if (!f) return cudaErrorNotSupported;
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = f(m, type, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

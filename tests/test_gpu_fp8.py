@@ -227,7 +227,8 @@ def _offsets(counts):
 # counts of rows by expert, K, N: empty experts at the ends and between, tiles that end anywhere, one expert, many
 GROUPS = [([1], 16, 8), ([8, 0, 0, 3], 128, 64), ([0, 0, 5, 0], 144, 72), ([128, 129, 0, 1, 300, 127], 272, 200),
           ([1] * 40, 256, 136), ([0] * 100 + [7] + [0] * 155, 512, 24), ([2000, 3], 128, 520), ([3] * 1024, 32, 16),
-          ([40, 60, 16, 33, 64, 65], 640, 1000), ([0, 700, 0, 0, 900], 400, 128)]
+          ([40, 60, 16, 33, 64, 65], 640, 1000), ([0, 700, 0, 0, 900], 400, 128),
+          ([(37 * i) % 301 for i in range(120)], 272, 200), ([17, 0, 33] * 30, 1168, 130)]
 
 
 @pytest.mark.parametrize("out", list(DT))
