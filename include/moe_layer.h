@@ -534,12 +534,16 @@ void moe_quant_test_force_wait_timeout(int32_t on);
  * x_scale_dev fp32 [T, scales] the scales go the same way to row_scale_dev
  * [T k, scales] (scales 0 and NULL: none). x and rows, idx and pos do not overlap. T == 0
  * writes offsets of 0. E <= MOE_DISPATCH_MAX_EXPERTS, k <= MOE_ROUTE_MAX_TOP_K,
- * T * k < 2^30. Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ * T * k < 2^30. workspace_dev: moe_dispatch_tokens_workspace() bytes (0 for few choices; it goes by the current
+ * device's SMs), 256-byte aligned, free for reuse when the call's work on `stream` has finished. Errors:
+ * MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
  */
 #define MOE_DISPATCH_MAX_EXPERTS 1024
+moe_status_t moe_dispatch_tokens_workspace(int32_t T, int32_t k, int32_t E, int64_t* bytes);
 moe_status_t moe_dispatch_tokens(const void* x_dev, int64_t row_bytes, int64_t row_stride, const float* x_scale_dev,
                                  int32_t scales, const int32_t* idx_dev, int32_t T, int32_t k, int32_t E, void* rows_dev,
-                                 float* row_scale_dev, int32_t* offsets_dev, int32_t* pos_dev, void* stream);
+                                 float* row_scale_dev, int32_t* offsets_dev, int32_t* pos_dev, void* workspace_dev,
+                                 int64_t workspace_bytes, void* stream);
 
 /*
  * out[t] = sum_j weights[t, j] * y[pos[t, j]], added up in fp32 in the order of j and

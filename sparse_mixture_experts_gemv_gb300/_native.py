@@ -148,7 +148,8 @@ _SIGNATURES = {
     "moe_quant_test_force_wait_timeout": (None, [ctypes.c_int32]),
     "moe_dispatch_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                            ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 3 +
-                            [ctypes.c_void_p] * 5),
+                            [ctypes.c_void_p] * 5 + [ctypes.c_int64, ctypes.c_void_p]),
+    "moe_dispatch_tokens_workspace": (ctypes.c_int, [ctypes.c_int32] * 3 + [ctypes.POINTER(ctypes.c_int64)]),
     "moe_combine_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
                                           ctypes.c_void_p] + [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 2),
     "moe_combine_tokens_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,

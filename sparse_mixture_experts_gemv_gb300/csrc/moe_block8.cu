@@ -28,6 +28,48 @@ struct QuantizeParams {
 
 constexpr int kThreads = 256;
 
+// g / (1 + e^-g) * u. The quotient is the product with the approximate reciprocal, corrected once by the remainder (one
+// step of Newton's): off by little more than its rounding. Below -80, where the reciprocal leaves the normal
+// range, it is the division.
+MOE_DEV void silu_mul(float (&g)[16], const float (&u)[16]) {
+  float least = g[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) least = fminf(least, g[i]);
+  if (least >= -80.f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float d = 1.f + expf(-g[i]);
+      float y;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+      const float q = g[i] * y;
+      g[i] = fmaf(fmaf(-q, d, g[i]), y, q) * u[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = g[i] / (1.f + expf(-g[i])) * u[i];
+  }
+}
+
+// The quotients of 16 values of a block by its scale, rounded to the nearest fp32 each: the product with the correctly
+// rounded reciprocal is off by two steps at most, one correction by its exact remainder by less than one, and from
+// there a second one is the rounded quotient (Markstein, IBM Journal of Research and Development 34, 1990). Remainders
+// are exact while nothing leaves the normal range: scales beyond 2^+-90 (or NaN) take the division. Values below 2^-10
+// of the scale, whose remainder may, are 0 in E4M3 either way.
+MOE_DEV void divide(float (&v)[16], float scale) {
+  if (scale >= 0x1p-90f && scale <= 0x1p90f) {
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float q = v[i] * inv;
+      q = fmaf(fmaf(-q, scale, v[i]), inv, q);
+      v[i] = fmaf(fmaf(-q, scale, v[i]), inv, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], scale);
+  }
+}
+
 // Sixteen values a thread, eight threads a block of 128: its largest value comes from three exchanges, so that the
 // rows are read once. The scale is a product with the rounded 1/448, and the quotient is rounded to fp32
 // before E4M3: what elementary operations on tensors give, bit for bit. A block with an infinity or a NaN
@@ -39,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) block8_quantize_kernel(const Quantiz
   const int64_t per_row = (int64_t)p.blocks * 8, n = p.T * per_row;
   // whole warps take part in the exchanges: their last lanes may lie behind the end
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i - (threadIdx.x & 31) < n; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t t = i / per_row;
+    const int64_t t = n >> 32 ? i / per_row : (uint32_t)i / (uint32_t)per_row;   // a 64-bit division takes 100 instructions
     const int c = (int)(i - t * per_row) * 16;
     const bool in = i < n && c < p.K;
     float v[16] = {};
@@ -48,8 +90,7 @@ __global__ void __launch_bounds__(kThreads) block8_quantize_kernel(const Quantiz
       if (SWIGLU) {
         float u[16];
         int8::load16<DT>(p.x, t * p.stride + p.K + c, u);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = swiglu(v[j], u[j]);
+        silu_mul(v, u);
       }
     }
     uint32_t top = int8::amax_bits(v);
@@ -59,14 +100,12 @@ __global__ void __launch_bounds__(kThreads) block8_quantize_kernel(const Quantiz
     float scale = __uint_as_float(top) * (1.f / 448.f);
     if (top >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);
     else if (scale == 0.f) scale = 1.f;
+    divide(v, scale);
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float f[4];
-#pragma unroll
-      for (int l = 0; l < 4; ++l) f[l] = __fdiv_rn(v[4 * j + l], scale);
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j], v[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j + 2], v[4 * j + 3]), __NV_SATFINITE, __NV_E4M3);
       w[j] = lo | hi << 16;
     }
     *reinterpret_cast<uint4*>(p.q + t * p.K + c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -155,6 +194,7 @@ moe_status_t product(const void* x, int x_dtype, int64_t x_stride, const float* 
     q.q = (uint8_t*)workspace;
     q.scale = (float*)((uint8_t*)workspace + pad256((int64_t)g.rows * g.K));
     e = launch_quantize(q, x_dtype, false, s);
+    g.early = 1;
     g.x = q.q;
     g.x_stride = g.K;
     g.x_scale = q.scale;

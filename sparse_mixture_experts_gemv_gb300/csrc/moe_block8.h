@@ -22,6 +22,7 @@ struct GemmArgs {
   int out_dtype;
   int rows, K, channels, groups;
   const int* offsets;        // [groups + 1] on the device, or NULL: one group of all rows
+  int early;                 // the kernel before wrote x and x_scale, had waited for those before it, and nothing else
 };
 cudaError_t launch_gemm(const GemmArgs& a, int num_sms, cudaStream_t s);
 void test_withhold(int on);   // test only: products launched by this thread get no rows

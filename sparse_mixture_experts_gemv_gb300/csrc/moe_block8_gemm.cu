@@ -74,6 +74,7 @@ struct Params {
   int out_dtype;
   int wide;                  // rows of out are 16-byte aligned
   int scales_wide;           // and those of x_scale
+  int early;                 // see GemmArgs
   int withhold;              // test only: no rows come, so that the waits for them run out
 };
 
@@ -410,7 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  pdl_wait();
+  // Behind the call's own quantization only rows and scales wait for it: what came before it is complete when it lets
+  // this kernel start, so that weights are on their way meanwhile.
+  if (!p.early) pdl_wait();
   asm volatile("fence.proxy.async.global;" ::: "memory");   // rows written by the kernel before, read by TMA here
   pdl_launch_dependents();
   make_tables(p, first, row, scratch);
@@ -421,6 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
   const uint32_t full0 = smem_u32(full), done0 = smem_u32(done), ring0 = smem_u32(smem);
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------ weights (0), rows (2)
+    if (p.early && warp == 2) {
+      pdl_wait();
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+    }
     const int blocks = p.blocks, stages = p.stages;
     const uint32_t stage_bytes = p.stage_bytes;
     uint32_t it = 0;
@@ -504,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
     mbar_wait(drain, 0, &g_gemm_error, abort_flag, 2000000000LL, false);
   } else if (warp == 3) {
     // -------------------------------------------------------------- scales
+    if (p.early) pdl_wait();
     const uint32_t sc_full0 = smem_u32(sc_full), sc_empty0 = smem_u32(sc_empty);
     int at = 0, ph = 1;
     bool stop = false;
@@ -626,9 +634,10 @@ template <int NT>
 cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   Maps maps = {};
   cudaError_t e = encode(&maps.w, a.w, (int64_t)a.groups * a.channels, a.K, a.w_stride, NT);
+  const int tail = (a.rows - 1) % kRows + 1;   // dense: rows of the last tile
   for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
-    e = encode(&maps.x[i], a.x, a.rows, a.K, a.x_stride, 16u << i);
-    if (a.rows <= 16 << i) break;
+    const bool used = a.offsets ? i == 0 || a.rows > 8 << i : (i == 3 && a.rows > 64) || (tail <= 16 << i && (i == 0 || tail > 8 << i));
+    if (used) e = encode(&maps.x[i], a.x, a.rows, a.K, a.x_stride, 16u << i);
   }
   if (e != cudaSuccess) return e;
   const int size = a.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
@@ -653,6 +662,7 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   p.out = a.out;
   p.out_dtype = a.out_dtype;
   p.scales_wide = !((uintptr_t)a.x_scale & 15) && p.blocks % 4 == 0;
+  p.early = a.early;
   p.withhold = t_withhold;
   const size_t smem = (size_t)p.stages * p.stage_bytes + kTurnBytes<NT> + kFixedSmem;
   // at most one tile a group more than the rows fill

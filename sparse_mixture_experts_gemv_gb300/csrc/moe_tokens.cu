@@ -24,69 +24,37 @@ namespace tokens {
 namespace {
 
 // ------------------------------------------------------------------------------- places
-constexpr int kPlanThreads = 512;              // = choices of a segment
-constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanCtas = 8;                   // of the cluster that places many choices
 constexpr int kBuckets = MOE_DISPATCH_MAX_EXPERTS + 1;   // the last one: no expert
+constexpr int kFusedThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kFusedChoices = 2048;            // so many are placed by every CTA for itself
 
+template <int THREADS>
 struct PlanShared {
-  int hist[kBuckets];                          // choices of this CTA's part by expert
-  int cursor[kBuckets];                        // the expert's next row
-  uint8_t count[kPlanWarps][kBuckets + 3];     // a segment's choices by warp and expert
-  int sums[kPlanWarps];
-  int pos[kFusedChoices];
+  int hist[kBuckets + 7];                      // choices by expert
+  int cursor[kBuckets + 7];                    // before: of the chunks before this one; then the expert's next row
+  alignas(16) uint8_t count[kBuckets][THREADS / 32];   // a segment's choices by expert and warp
+  int sums[THREADS / 32];
 };
 
 MOE_DEV int bucket_of(int e, int E) { return e >= 0 && e < E ? e : E; }
 
-MOE_DEV uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-MOE_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
-// The int at the same place of another CTA's shared memory.
-MOE_DEV int remote(const int* p, uint32_t rank) {
-  uint32_t a, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return (int)v;
-}
-
-// The rows of choices [a0, a1), which are this CTA's part of n: put(choice, row). Counts by expert, their sums over
-// the parts and experts before, and then 512 choices at a time: a choice's rank is that within its warp (the lanes
-// of the same expert below) plus the counts of the warps before it, a byte each, which keeps the order of the
-// choices without a sort. CLUSTER: the parts are those of a cluster's CTAs.
-template <bool CLUSTER, class Put>
-MOE_DEV void place(PlanShared& s, const int* idx, int a0, int a1, int E, int* offsets, Put put) {
+// The rows of choices [a0, a1): put(choice, row). s.hist holds all choices by expert and s.cursor those before a0 (what
+// is written before is seen behind a barrier in here). Experts follow each other, and within a segment of as many
+// choices as threads a choice's rank is that within its warp (the lanes of the same expert below) plus the counts of
+// the warps before it, a byte each and added up four an instruction: the order of the choices, without a sort.
+template <int THREADS, class Put>
+MOE_DEV void place(PlanShared<THREADS>& s, const int* idx, int64_t a0, int64_t a1, int E, int* offsets, Put put) {
+  constexpr int kWarps = THREADS / 32, kPer = (kBuckets + THREADS - 1) / THREADS;
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
-  for (int e = i; e <= E; e += kPlanThreads) s.hist[e] = 0;
-  for (int c = i; c < (int)sizeof(s.count) / 4; c += kPlanThreads) reinterpret_cast<int*>(s.count)[c] = 0;
+  int next = a0 + i < a1 ? __ldg(idx + a0 + i) : 0;
+  for (int c = i; c < (E + 1) * kWarps / 4; c += THREADS) reinterpret_cast<int*>(s.count)[c] = 0;
   __syncthreads();
-#pragma unroll 8
-  for (int a = a0 + i; a < a1; a += kPlanThreads) atomicAdd(&s.hist[bucket_of(__ldg(idx + a), E)], 1);
-  if (CLUSTER) cluster_sync();
-  else __syncthreads();
-  // three consecutive experts a thread at most
-  const int per = (E + kPlanThreads) / kPlanThreads, e0 = i * per;
-  int total[3] = {}, before[3] = {}, sum = 0;
+  int total[kPer], sum = 0;
+  const int e0 = i * kPer;                     // consecutive experts a thread
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    if (q >= per || e0 + q > E) continue;
-    if constexpr (CLUSTER) {
-      const uint32_t rank = cluster_rank();
-#pragma unroll
-      for (uint32_t r = 0; r < kPlanCtas; ++r) {
-        const int v = remote(&s.hist[e0 + q], r);
-        total[q] += v;
-        before[q] += r < rank ? v : 0;
-      }
-    } else {
-      total[q] = s.hist[e0 + q];
-    }
+  for (int q = 0; q < kPer; ++q) {
+    total[q] = e0 + q <= E ? s.hist[e0 + q] : 0;
     sum += total[q];
   }
   int upto = sum;
@@ -97,35 +65,56 @@ MOE_DEV void place(PlanShared& s, const int* idx, int a0, int a1, int E, int* of
   }
   if (lane == 31) s.sums[warp] = upto;
   __syncthreads();
-  int base = upto - sum;
-  for (int w = 0; w < warp; ++w) base += s.sums[w];
+  // the sums of the warps before, by one exchange among the lanes
+  int base = lane < warp ? s.sums[lane] : 0;
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    if (q >= per || e0 + q > E) continue;
-    s.cursor[e0 + q] = base + before[q];
+  for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xFFFFFFFFu, base, o);
+  base += upto - sum;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    if (e0 + q > E) continue;
+    s.cursor[e0 + q] += base;
     if (offsets) offsets[e0 + q] = base;       // offsets[E]: where the choices of no expert begin
     base += total[q];
   }
-  if (CLUSTER) cluster_sync();                 // no CTA leaves while its counts are read
-  else __syncthreads();
-  for (int a = a0; a < a1; a += kPlanThreads) {
-    const int at = a + i;
-    const int e = at < a1 ? bucket_of(__ldg(idx + at), E) : -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    const bool first = e >= 0 && (same & ((1u << lane) - 1)) == 0;
-    if (first) s.count[warp][e] = (uint8_t)__popc(same);
+  const uint32_t below = (1u << lane) - 1;
+  const int bits = 32 - __clz(E + 1);
+  for (int64_t a = a0; a < a1; a += THREADS) {
+    const int64_t at = a + i;
+    const int e = at < a1 ? bucket_of(next, E) : E + 1;   // E + 1: behind the end
+    if (at + THREADS < a1) next = __ldg(idx + at + THREADS);
+    // the lanes of the same expert, a vote a bit (one match of all values takes some 2,000 cycles a segment)
+    uint32_t same = 0xFFFFFFFFu;
+    for (int b = 0; b < bits; ++b) {
+      const uint32_t set = __ballot_sync(0xFFFFFFFFu, e >> b & 1);
+      same &= e >> b & 1 ? set : ~set;
+    }
+    const bool first = e <= E && (same & below) == 0;
+    if (first) s.count[e][warp] = (uint8_t)__popc(same);
     __syncthreads();
-    if (e >= 0) {
-      int row = s.cursor[e] + __popc(same & ((1u << lane) - 1));
-      for (int w = 0; w < warp; ++w) row += s.count[w][e];
-      put(at, e < E ? row : ~row);
+    if (e <= E) {
+      uint32_t row = s.cursor[e] + __popc(same & below);
+      const uint4* c = reinterpret_cast<const uint4*>(s.count[e]);
+#pragma unroll
+      for (int w = 0; w < kWarps; w += 16) {
+        const uint4 u = c[w / 16];
+        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+          const int n = warp - w - 4 * l;      // of these four warps, those before this one
+          row = __dp4a(v[l], n >= 4 ? 0x01010101u : n <= 0 ? 0u : 0x01010101u >> (32 - 8 * n), row);
+        }
+      }
+      put(at, e < E ? (int)row : ~(int)row);
     }
     __syncthreads();
-    if (first) {
-      atomicAdd(&s.cursor[e], __popc(same));
-      s.count[warp][e] = 0;
+    if (a + THREADS < a1) {
+      if (first) {
+        atomicAdd(&s.cursor[e], __popc(same));
+        s.count[e][warp] = 0;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -140,18 +129,25 @@ struct DispatchParams {
   float* row_scale;
   int* offsets;
   int* pos;
+  uint16_t* counts;          // [chunks][stride]: choices by chunk and expert
+  int chunk, chunks, stride;
 };
 
-// A vector of a row to its k places. `at`: the place of choice `lane`, ~place where there is no expert.
+// A piece of a row (16-byte vectors: 1 KB) to its k places, and the row's scales with the first. `at`: the place of
+// choice `lane`, ~place where there is no expert.
+template <class V>
+constexpr int kVectors = sizeof(V) == 16 ? 2 : 8;   // of a lane
 template <class V>
 MOE_DEV void copy_piece(const DispatchParams& p, int64_t t, int64_t piece, int at, int lane) {
-  constexpr int kU = sizeof(V) == 16 ? 4 : 8;
+  constexpr int kU = kVectors<V>;
   const int64_t n = p.row / (int64_t)sizeof(V), v0 = piece * 32 * kU + lane;
   const V* src = reinterpret_cast<const V*>(p.x + t * p.x_stride);
   V v[kU];
 #pragma unroll
   for (int u = 0; u < kU; ++u)
     if (v0 + 32 * u < n) v[u] = __ldg(src + v0 + 32 * u);
+  const bool scales = piece == 0 && p.x_scale;
+  float f = scales && lane < p.scales ? __ldg(p.x_scale + t * p.scales + lane) : 0.f;
   for (int j = 0; j < p.k; ++j) {
     const int r = __shfl_sync(0xFFFFFFFFu, at, j);
     V* dst = reinterpret_cast<V*>(p.rows + (int64_t)(r >= 0 ? r : ~r) * p.row);
@@ -159,65 +155,101 @@ MOE_DEV void copy_piece(const DispatchParams& p, int64_t t, int64_t piece, int a
     for (int u = 0; u < kU; ++u)
       if (v0 + 32 * u < n) dst[v0 + 32 * u] = r >= 0 ? v[u] : V{};
   }
-  if (piece == 0 && p.x_scale)
-    for (int c = lane; c - lane < p.scales; c += 32) {
-      const float f = c < p.scales ? __ldg(p.x_scale + t * p.scales + c) : 0.f;
-      for (int j = 0; j < p.k; ++j) {
-        const int r = __shfl_sync(0xFFFFFFFFu, at, j);
-        if (c < p.scales) p.row_scale[(int64_t)(r >= 0 ? r : ~r) * p.scales + c] = r >= 0 ? f : 0.f;
-      }
+  if (!scales) return;
+  for (int c = lane; c - lane < p.scales; c += 32) {
+    if (c >= 32) f = c < p.scales ? __ldg(p.x_scale + t * p.scales + c) : 0.f;
+    for (int j = 0; j < p.k; ++j) {
+      const int r = __shfl_sync(0xFFFFFFFFu, at, j);
+      if (c < p.scales) p.row_scale[(int64_t)(r >= 0 ? r : ~r) * p.scales + c] = r >= 0 ? f : 0.f;
     }
+  }
 }
 template <class V>
 __host__ __device__ int64_t pieces_of(int64_t row) {
-  const int64_t v = 32 * (sizeof(V) == 16 ? 4 : 8) * (int64_t)sizeof(V);
+  const int64_t v = 32 * kVectors<V> * (int64_t)sizeof(V);
   return row > v ? (row + v - 1) / v : 1;
 }
 
-// Few choices: every CTA places all of them and copies its share of the rows.
+template <class V, class Pos>
+MOE_DEV void copy_tokens(const DispatchParams& p, int64_t t0, int64_t t1, int part, int parts, Pos pos) {
+  const int lane = threadIdx.x & 31;
+  const int64_t pieces = pieces_of<V>(p.row), units = (t1 - t0) * pieces;
+  for (int64_t u = part; u < units; u += parts) {
+    const int64_t t = t0 + u / pieces;
+    copy_piece<V>(p, t, u % pieces, lane < p.k ? pos(t * p.k + lane) : 0, lane);
+  }
+}
+
+// Few choices: every CTA counts and places all of them, and copies its share of the rows.
 template <class V>
-__global__ void __launch_bounds__(kPlanThreads) dispatch_fused_kernel(const DispatchParams p) {
-  __shared__ PlanShared s;
+__global__ void __launch_bounds__(kFusedThreads) dispatch_fused_kernel(const DispatchParams p) {
+  __shared__ PlanShared<kFusedThreads> s;
+  __shared__ int s_pos[kFusedChoices];
+  for (int e = threadIdx.x; e <= p.E; e += kFusedThreads) s.hist[e] = s.cursor[e] = 0;
   pdl_wait();
   pdl_launch_dependents();
+  __syncthreads();
+  const int n = p.T * p.k;
+#pragma unroll 4
+  for (int a = threadIdx.x; a < n; a += kFusedThreads) atomicAdd(&s.hist[bucket_of(__ldg(p.idx + a), p.E)], 1);
   const bool tells = blockIdx.x == 0;
-  place<false>(s, p.idx, 0, p.T * p.k, p.E, tells ? p.offsets : nullptr, [&](int a, int row) {
-    s.pos[a] = row;
+  place(s, p.idx, 0, n, p.E, tells ? p.offsets : nullptr, [&](int64_t a, int row) {
+    s_pos[a] = row;
     if (tells) p.pos[a] = row;
   });
+  constexpr int kW = kFusedThreads / 32;
+  copy_tokens<V>(p, 0, p.T, blockIdx.x * kW + (threadIdx.x >> 5), gridDim.x * kW, [&](int64_t a) { return s_pos[a]; });
+}
+
+// Many choices: their numbers by expert in each chunk of tokens first.
+__global__ void __launch_bounds__(kThreads) dispatch_count_kernel(const DispatchParams p) {
+  __shared__ int hist[kBuckets + 7];
+  for (int e = threadIdx.x; e < p.stride; e += kThreads) hist[e] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const int64_t pieces = pieces_of<V>(p.row), units = p.T * pieces;
-  for (int64_t u = (int64_t)blockIdx.x * kPlanWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kPlanWarps) {
-    const int64_t t = u / pieces;
-    copy_piece<V>(p, t, u - t * pieces, lane < p.k ? s.pos[t * p.k + lane] : 0, lane);
-  }
+  const int64_t a0 = (int64_t)blockIdx.x * p.chunk * p.k, a1 = min(a0 + (int64_t)p.chunk * p.k, (int64_t)p.T * p.k);
+#pragma unroll 4
+  for (int64_t a = a0 + threadIdx.x; a < a1; a += kThreads) atomicAdd(&hist[bucket_of(__ldg(p.idx + a), p.E)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.stride; e += kThreads)
+    p.counts[(int64_t)blockIdx.x * p.stride + e] = (uint16_t)hist[e];
 }
 
-// Many choices: one cluster places them, each CTA an eighth.
-__global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kPlanCtas, 1, 1) dispatch_plan_kernel(const DispatchParams p) {
-  __shared__ PlanShared s;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int n = p.T * p.k, part = (n + kPlanCtas - 1) / kPlanCtas;
-  const int a0 = min(n, (int)blockIdx.x * part), a1 = min(n, a0 + part);
-  place<true>(s, p.idx, a0, a1, p.E, blockIdx.x == 0 ? p.offsets : nullptr, [&](int a, int row) { p.pos[a] = row; });
-}
-
-constexpr int kCopyThreads = 256;
-
-// The rows, each token's read once.
+// Then every CTA adds up all chunks' numbers and those before its own, eight experts a load, places its chunk and copies
+// its rows. 4,096 tokens of 2,048 bytes, k = 8: 20 us with the counts; 8,191 of 5,120 bytes, k = 8: 68 us, 5.6 TB/s.
 template <class V>
-__global__ void __launch_bounds__(kCopyThreads) dispatch_copy_kernel(const DispatchParams p) {
+__global__ void __launch_bounds__(kThreads, 1) dispatch_chunk_kernel(const DispatchParams p) {
+  __shared__ PlanShared<kThreads> s;
+  for (int e = threadIdx.x; e < p.stride; e += kThreads) s.hist[e] = s.cursor[e] = 0;
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t pieces = pieces_of<V>(p.row), units = p.T * pieces;
-  constexpr int kW = kCopyThreads / 32;
-  for (int64_t u = (int64_t)blockIdx.x * kW + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kW) {
-    const int64_t t = u / pieces;
-    copy_piece<V>(p, t, u - t * pieces, lane < p.k ? ldg_cg_s32(p.pos + t * p.k + lane) : 0, lane);
+  __syncthreads();
+  const int groups = p.stride / 8, parts = kThreads / groups, part = threadIdx.x / groups, g = threadIdx.x % groups;
+  if (part < parts) {
+    int all[8] = {}, before[8] = {};
+#pragma unroll 4
+    for (int c = part; c < p.chunks; c += parts) {
+      const uint4 u = ldg_cg(p.counts + (int64_t)c * p.stride + 8 * g);
+      const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+      const bool own = c < (int)blockIdx.x;
+#pragma unroll
+      for (int l = 0; l < 8; ++l) {
+        const int n = l & 1 ? v[l / 2] >> 16 : v[l / 2] & 0xFFFF;
+        all[l] += n;
+        before[l] += own ? n : 0;
+      }
+    }
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+      atomicAdd(&s.hist[8 * g + l], all[l]);
+      atomicAdd(&s.cursor[8 * g + l], before[l]);
+    }
   }
+  const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, (int64_t)p.T);
+  place(s, p.idx, t0 * p.k, t1 * p.k, p.E, blockIdx.x == 0 ? p.offsets : nullptr,
+        [&](int64_t a, int row) { p.pos[a] = row; });
+  copy_tokens<V>(p, t0, t1, threadIdx.x >> 5, kThreads / 32, [&](int64_t a) { return ldg_cg_s32(p.pos + a); });
 }
 
 // ------------------------------------------------------------------------ sums and gradients
@@ -252,15 +284,18 @@ struct Pack {
     if constexpr (DT == MOE_DTYPE_F32) {
 #pragma unroll
       for (int i = 0; i < N; ++i) w[i] = __float_as_uint(f[i]);
-    } else {
-      uint16_t h[N];
+    } else if constexpr (N == 1) {
+      w[0] = DT == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f[0])) : __half_as_ushort(__float2half_rn(f[0]));
+    } else {   // in pairs: single conversions are an eighth as fast
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        h[i] = DT == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f[i])) : __half_as_ushort(__float2half_rn(f[i]));
-      if constexpr (N == 1) w[0] = h[0];
-      else {
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) w[i] = h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
+      for (int i = 0; i < N / 2; ++i) {
+        if constexpr (DT == MOE_DTYPE_BF16) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
       }
     }
   }
@@ -282,64 +317,82 @@ struct CombineParams {
 constexpr int kMaxThreads = 256;
 constexpr int kTogether = 8;   // choices whose rows are on their way at once
 
-// out[t] = sum_j w y[pos], in 32 bits and in the order of the choices. One CTA a token.
+// A token's places and weights, in shared memory by turns: the next token's are on their way while one is worked on.
+struct Choices {
+  int at[2][MOE_ROUTE_MAX_TOP_K];
+  float w[2][MOE_ROUTE_MAX_TOP_K];
+};
+// Place and weight of choice threadIdx.x of token t; INT32_MAX: no row of y at all.
+MOE_DEV void fetch(const CombineParams& p, int64_t t, int& at, float& w) {
+  if (t < p.T && threadIdx.x < p.k) {
+    at = ldg_cg_s32(p.pos + t * p.k + threadIdx.x);
+    w = p.weights ? ldg_cg_f32(p.weights + t * p.k + threadIdx.x) : 1.f;
+  }
+}
+MOE_DEV void keep(Choices& s, int turn, const CombineParams& p, int at, float w) {
+  const int64_t rows = (int64_t)p.T * p.k;
+  if (threadIdx.x < p.k) {
+    s.at[turn][threadIdx.x] = at < rows && ~at < rows ? at : INT32_MAX;
+    s.w[turn][threadIdx.x] = w;
+  }
+}
+
+// out[t] = sum_j w y[pos], in 32 bits and in the order of the choices. One CTA a token, one barrier a token. 8,191 tokens
+// of 2,048 bf16, k = 8: see the table of cases.
 template <int DT, int N>
 __global__ void __launch_bounds__(kMaxThreads) combine_kernel(const CombineParams p) {
-  __shared__ int s_at[MOE_ROUTE_MAX_TOP_K];
-  __shared__ float s_w[MOE_ROUTE_MAX_TOP_K];
+  __shared__ Choices s;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t rows = (int64_t)p.T * p.k;
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    __syncthreads();
-    for (int j = threadIdx.x; j < p.k; j += blockDim.x) {
-      const int at = ldg_cg_s32(p.pos + t * p.k + j);
-      s_at[j] = at < rows ? at : -1;
-      s_w[j] = p.weights ? ldg_cg_f32(p.weights + t * p.k + j) : 1.f;
-    }
-    __syncthreads();
+  int at = 0, turn = 0;
+  float w = 0.f;
+  fetch(p, blockIdx.x, at, w);
+  keep(s, 0, p, at, w);
+  __syncthreads();
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+    fetch(p, t + gridDim.x, at, w);
     for (int c = threadIdx.x * N; c < p.H; c += blockDim.x * N) {
       float acc[N] = {};
       for (int j0 = 0; j0 < p.k; j0 += kTogether) {
         Pack<DT, N> v[kTogether];
 #pragma unroll
         for (int q = 0; q < kTogether; ++q)
-          if (j0 + q < p.k && s_at[j0 + q] >= 0) v[q].load(p.y, s_at[j0 + q] * p.y_stride + c);
+          if (j0 + q < p.k && (unsigned)s.at[turn][j0 + q] < (unsigned)INT32_MAX)
+            v[q].load(p.y, s.at[turn][j0 + q] * p.y_stride + c);
 #pragma unroll
         for (int q = 0; q < kTogether; ++q)
-          if (j0 + q < p.k && s_at[j0 + q] >= 0) {
-            const float w = s_w[j0 + q];
+          if (j0 + q < p.k && (unsigned)s.at[turn][j0 + q] < (unsigned)INT32_MAX) {
+            const float f = s.w[turn][j0 + q];
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(w, v[q].get(i), acc[i]);
+            for (int i = 0; i < N; ++i) acc[i] = fmaf(f, v[q].get(i), acc[i]);
           }
       }
       Pack<DT, N> o;
       o.set(acc);
       o.store(p.out, t * p.H + c);
     }
+    keep(s, turn ^ 1, p, at, w);
+    __syncthreads();
   }
 }
 
 // d_y[pos] = w d_out[t] and d_w = <d_out[t], y[pos]>, eight choices at a time: each thread adds up its columns, then
 // the CTA adds the threads' sums, in a fixed order.
 template <int DT, int N>
-__global__ void __launch_bounds__(kMaxThreads) combine_backward_kernel(const CombineParams p) {
-  __shared__ int s_at[MOE_ROUTE_MAX_TOP_K];
-  __shared__ float s_w[MOE_ROUTE_MAX_TOP_K];
-  __shared__ float s_sum[kMaxThreads / 32][kTogether];
+__global__ void __launch_bounds__(kMaxThreads, 4) combine_backward_kernel(const CombineParams p) {
+  __shared__ Choices s;
+  __shared__ float s_sum[2][kMaxThreads / 32][kTogether];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t rows = (int64_t)p.T * p.k;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    __syncthreads();
-    for (int j = threadIdx.x; j < p.k; j += blockDim.x) {
-      const int at = ldg_cg_s32(p.pos + t * p.k + j);
-      s_at[j] = at < rows && ~at < rows ? at : INT32_MAX;   // INT32_MAX: no row of y at all
-      s_w[j] = p.weights ? ldg_cg_f32(p.weights + t * p.k + j) : 1.f;
-    }
-    __syncthreads();
-    for (int j0 = 0; j0 < p.k; j0 += kTogether) {
+  int next_at = 0, turn = 0, side = 0;
+  float next_w = 0.f;
+  fetch(p, blockIdx.x, next_at, next_w);
+  keep(s, 0, p, next_at, next_w);
+  __syncthreads();
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+    fetch(p, t + gridDim.x, next_at, next_w);
+    for (int j0 = 0; j0 < p.k; j0 += kTogether, side ^= 1) {
       float dot[kTogether] = {};
       for (int c = threadIdx.x * N; c < p.H; c += blockDim.x * N) {
         Pack<DT, N> d, v[kTogether];
@@ -347,19 +400,20 @@ __global__ void __launch_bounds__(kMaxThreads) combine_backward_kernel(const Com
         if (p.d_weights) {
 #pragma unroll
           for (int q = 0; q < kTogether; ++q)
-            if (j0 + q < p.k && (unsigned)s_at[j0 + q] < (unsigned)INT32_MAX) v[q].load(p.y, s_at[j0 + q] * p.y_stride + c);
+            if (j0 + q < p.k && (unsigned)s.at[turn][j0 + q] < (unsigned)INT32_MAX)
+              v[q].load(p.y, s.at[turn][j0 + q] * p.y_stride + c);
         }
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) {
           if (j0 + q >= p.k) break;
-          const int at = s_at[j0 + q];
+          const int at = s.at[turn][j0 + q];
           if (at == INT32_MAX) continue;
           if (p.d_weights && at >= 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) dot[q] = fmaf(d.get(i), v[q].get(i), dot[q]);
           }
           if (p.d_y) {
-            const float w = s_w[j0 + q];
+            const float w = s.w[turn][j0 + q];
             float f[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) f[i] = at >= 0 ? w * d.get(i) : 0.f;
@@ -369,19 +423,20 @@ __global__ void __launch_bounds__(kMaxThreads) combine_backward_kernel(const Com
           }
         }
       }
-      if (!p.d_weights) continue;
+      if (p.d_weights) {
 #pragma unroll
-      for (int q = 0; q < kTogether; ++q) {
-        const float sum = warp_sum(dot[q]);
-        if (lane == 0) s_sum[warp][q] = sum;
+        for (int q = 0; q < kTogether; ++q) {
+          const float sum = warp_sum(dot[q]);
+          if (lane == 0) s_sum[side][warp][q] = sum;
+        }
       }
+      if (j0 + kTogether >= p.k) keep(s, turn ^ 1, p, next_at, next_w);
       __syncthreads();
-      if (threadIdx.x < kTogether && j0 + threadIdx.x < p.k) {
+      if (p.d_weights && threadIdx.x < kTogether && j0 + threadIdx.x < p.k) {   // the other side is written meanwhile
         float sum = 0.f;
-        for (int w = 0; w < (int)blockDim.x / 32; ++w) sum += s_sum[w][threadIdx.x];
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) sum += s_sum[side][w][threadIdx.x];
         p.d_weights[t * p.k + j0 + threadIdx.x] = sum;
       }
-      __syncthreads();
     }
   }
 }
@@ -401,25 +456,40 @@ cudaError_t launch(K kernel, int64_t grid, int block, cudaStream_t s, const P& p
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Chunks of many choices: one an SM, but none of more choices than 16 bits count.
+struct Chunks {
+  int chunk, chunks, stride;
+  int64_t bytes;
+};
+Chunks chunks_of(int64_t T, int64_t k, int64_t E) {
+  Chunks c = {};
+  if (T * k <= kFusedChoices) return c;
+  const int sms = int8::device_sms();
+  const int64_t most = 65535 / k, each = (T + sms - 1) / sms;
+  c.chunk = (int)(each < most ? each : most);
+  c.chunks = (int)((T + c.chunk - 1) / c.chunk);
+  c.stride = (int)((E + 1 + 7) / 8 * 8);
+  c.bytes = ((int64_t)c.chunks * c.stride * 2 + 255) / 256 * 256;
+  return c;
+}
+
 template <class V>
 cudaError_t launch_dispatch(const DispatchParams& p, int sms, cudaStream_t s) {
-  const int64_t units = p.T * pieces_of<V>(p.row);
-  if ((int64_t)p.T * p.k <= kFusedChoices) {
-    int64_t grid = (units + kPlanWarps - 1) / kPlanWarps;
+  if (!p.chunks) {
+    constexpr int kW = kFusedThreads / 32;
+    int64_t grid = (p.T * pieces_of<V>(p.row) + kW - 1) / kW;
     if (grid > 2 * sms) grid = 2 * sms;
-    return launch(dispatch_fused_kernel<V>, grid < 1 ? 1 : grid, kPlanThreads, s, p);
+    return launch(dispatch_fused_kernel<V>, grid < 1 ? 1 : grid, kFusedThreads, s, p);
   }
-  cudaError_t e = launch(dispatch_plan_kernel, kPlanCtas, kPlanThreads, s, p);
-  if (e != cudaSuccess) return e;
-  constexpr int kW = kCopyThreads / 32;
-  const int64_t want = (units + kW - 1) / kW, most = 8 * (int64_t)sms;
-  return launch(dispatch_copy_kernel<V>, want < most ? want : most, kCopyThreads, s, p);
+  const cudaError_t e = launch(dispatch_count_kernel, p.chunks, kThreads, s, p);
+  return e != cudaSuccess ? e : launch(dispatch_chunk_kernel<V>, p.chunks, kThreads, s, p);
 }
 
 template <int DT, int N>
 cudaError_t launch_combine(const CombineParams& p, bool backward, int sms, cudaStream_t s) {
-  int threads = (int)((p.H + 32 * N - 1) / (32 * N)) * 32;
-  if (threads > kMaxThreads) threads = kMaxThreads;
+  // as many rounds as kMaxThreads take, each with the same threads
+  const int vectors = (p.H + N - 1) / N, rounds = (vectors + kMaxThreads - 1) / kMaxThreads;
+  const int threads = ((vectors + rounds - 1) / rounds + 31) / 32 * 32;
   const int64_t most = (int64_t)sms * 2048 / threads, grid = p.T < most ? p.T : most;
   return backward ? launch(combine_backward_kernel<DT, N>, grid, threads, s, p)
                   : launch(combine_kernel<DT, N>, grid, threads, s, p);
@@ -455,9 +525,20 @@ bool in_range(int32_t T, int32_t k, int64_t row, moe_status_t* st) {
 
 extern "C" {
 
+moe_status_t moe_dispatch_tokens_workspace(int32_t T, int32_t k, int32_t E, int64_t* bytes) {
+  using namespace moe::tokens;
+  moe_status_t st;
+  if (!bytes || E < 1) return MOE_ERR_INVALID_ARG;
+  if (!in_range(T, k, 1, &st)) return st;
+  if (E > MOE_DISPATCH_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+  *bytes = chunks_of(T, k, E).bytes;
+  return MOE_OK;
+}
+
 moe_status_t moe_dispatch_tokens(const void* x_dev, int64_t row_bytes, int64_t row_stride, const float* x_scale_dev,
                                  int32_t scales, const int32_t* idx_dev, int32_t T, int32_t k, int32_t E, void* rows_dev,
-                                 float* row_scale_dev, int32_t* offsets_dev, int32_t* pos_dev, void* stream) {
+                                 float* row_scale_dev, int32_t* offsets_dev, int32_t* pos_dev, void* workspace_dev,
+                                 int64_t workspace_bytes, void* stream) {
   using namespace moe::tokens;
   moe_status_t st;
   if (!in_range(T, k, row_bytes, &st)) return st;
@@ -470,8 +551,11 @@ moe_status_t moe_dispatch_tokens(const void* x_dev, int64_t row_bytes, int64_t r
   const int64_t n = (int64_t)T * k;
   if (T && (overlap(x_dev, (T - 1) * row_stride + row_bytes, rows_dev, n * row_bytes) || overlap(idx_dev, n * 4, pos_dev, n * 4)))
     return MOE_ERR_INVALID_ARG;
+  const Chunks c = chunks_of(T, k, E);
+  if (c.bytes && (!workspace_dev || workspace_bytes < c.bytes || (uintptr_t)workspace_dev & 255)) return MOE_ERR_INVALID_ARG;
   const DispatchParams p = {(const uint8_t*)x_dev, row_stride, row_bytes, x_scale_dev, scales, idx_dev, T, k, E,
-                            (uint8_t*)rows_dev, row_scale_dev, offsets_dev, pos_dev};
+                            (uint8_t*)rows_dev, row_scale_dev, offsets_dev, pos_dev, (uint16_t*)workspace_dev, c.chunk,
+                            c.chunks, c.stride};
   // the widest vector that every row starts and ends on
   const uint64_t a = (uintptr_t)x_dev | (uintptr_t)rows_dev | (uint64_t)row_bytes | (T > 1 ? (uint64_t)row_stride : 0);
   const int sms = moe::int8::device_sms();

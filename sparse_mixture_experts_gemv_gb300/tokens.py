@@ -3,6 +3,9 @@ moe_combine_tokens in the C ABI), and the gradients of both. Argument checks and
 marshalling only."""
 from __future__ import annotations
 
+import ctypes
+import functools
+
 import torch
 
 from . import _native as N
@@ -44,6 +47,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace(device, T, k, E):
+    b = ctypes.c_int64()
+    check(N.load().moe_dispatch_tokens_workspace(T, k, E, ctypes.byref(b)), "moe_dispatch_tokens")
+    return b.value
+
+
 def _dispatch(x, idx, num_experts, x_scale):
     what = "dispatch_tokens"
     if x.dtype not in ROW_TYPES or not x.is_cuda or x.dim() != 2 or x.shape[1] == 0:
@@ -70,9 +80,11 @@ def _dispatch(x, idx, num_experts, x_scale):
     row_scale = torch.empty((T * k, scales), dtype=torch.float32, device=dev) if scales else None
     offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
     pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    need = _workspace(dev.index, T, k, num_experts)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     status = N.load().moe_dispatch_tokens(x.data_ptr(), H * size, (stride if T > 1 else H) * size, _ptr(x_scale), scales,
                                           idx.data_ptr(), T, k, num_experts, rows.data_ptr(), _ptr(row_scale),
-                                          offsets.data_ptr(), pos.data_ptr(), current_stream(dev))
+                                          offsets.data_ptr(), pos.data_ptr(), _ptr(ws), need, current_stream(dev))
     if status:
         check(status, "moe_dispatch_tokens")
     return (rows, offsets, pos) if row_scale is None else (rows, row_scale, offsets, pos)
