@@ -243,13 +243,34 @@ struct Ring {
   uint32_t block;
 };
 
-// All blocks of a tile's C chunks of 32 channels (of one block of 128): acc += scale * product, 32 columns on their way
-// while the 32 before them are added. `there` false: no rows or channels, and the products are let go. What is done
-// once a block bounds it, so that all of it is in registers: parameters, behind the barriers' memory clobbers, would
-// be read again every time.
+// One block of a warp's C chunks of 32 columns: acc += scale * product, 32 columns on their way while the 32 before them
+// are added; the product is let go as soon as it has been read.
+template <int C>
+MOE_DEV void add_block(float2 (&acc)[16 * C], uint32_t taddr, uint32_t empty, bool first, float scale) {
+  uint32_t v[2][32];
+  tmem_request32(taddr, v[0]);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    tmem_arrived32(v[c & 1]);
+    if (c + 1 < C) {
+      tmem_request32(taddr + 32 * (c + 1), v[(c + 1) & 1]);
+    } else {
+      tc_fence_before();
+      __syncwarp();
+      if (first) arrive(empty);
+    }
+    add32(acc + 16 * c, v[c & 1], scale);
+  }
+}
+
+// All blocks of a tile. Instructions other than the sums bound it, some 80 a block and warp where places are counted
+// block by block: parameters are held in registers (behind the barriers' memory clobbers they would be read again every
+// time), and where the blocks come in fours (K a multiple of 512) four are unrolled, whose barriers, scales and products
+// follow each other. `there` false: no rows or channels, and the products are let go.
 template <int C, int NT>
 MOE_DEV void add_blocks(float2 (&acc)[16 * C], Scales& scales, Ring& ring, uint32_t taddr, int blocks, bool there,
                         volatile int* abort_flag) {
+  constexpr uint32_t kProducts = 512 / NT;
   Scales sc = scales;
   Ring r = ring;
   const bool first = (threadIdx.x & 31) == 0;
@@ -257,35 +278,32 @@ MOE_DEV void add_blocks(float2 (&acc)[16 * C], Scales& scales, Ring& ring, uint3
   for (int b0 = 0; b0 < blocks; b0 += 4) {
     lane_wait(sc.full + 8 * sc.at, sc.ph, &g_gemm_error, abort_flag);
     uint32_t row = sc.row + sc.at * (kSlotFloats * 4), channels = sc.channels + sc.at * (kSlotFloats * 4);
-    const uint32_t last = row + min(4, blocks - b0) * (kBlockFloats * 4);
-#pragma unroll 1
-    do {
-      const float scale = shared_f32(row) * shared_f32(channels);
-      lane_wait(r.done + 8 * (r.block % kDone), r.block / kDone & 1, &g_gemm_error, abort_flag);
-      tc_fence_after();
-      const uint32_t now = taddr + r.block % (512 / NT) * NT, empty = r.empty + 8 * (r.block % (512 / NT));
-      if (there) {
-        uint32_t v[2][32];
-        tmem_request32(now, v[0]);
+    if (there && blocks % 4 == 0) {
+      const uint32_t done = r.done + 8 * (r.block % kDone), ph = r.block / kDone & 1, product = r.block % kProducts;
+      const uint32_t to = taddr + product * NT, empty = r.empty + 8 * product;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          tmem_arrived32(v[c & 1]);
-          if (c + 1 < C) {
-            tmem_request32(now + 32 * (c + 1), v[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (first) arrive(empty);
-          }
-          add32(acc + 16 * c, v[c & 1], scale);
-        }
-      } else if (first) {
-        arrive(empty);
+      for (int q = 0; q < 4; ++q) {
+        const float scale = shared_f32(row + q * (kBlockFloats * 4)) * shared_f32(channels + q * (kBlockFloats * 4));
+        lane_wait(done + 8 * q, ph, &g_gemm_error, abort_flag);
+        tc_fence_after();
+        add_block<C>(acc, to + q * NT, empty + 8 * q, first, scale);
       }
-      ++r.block;
-      row += kBlockFloats * 4;
-      channels += kBlockFloats * 4;
-    } while (row != last);
+      r.block += 4;
+    } else {
+      const uint32_t last = row + min(4, blocks - b0) * (kBlockFloats * 4);
+#pragma unroll 1
+      do {
+        const float scale = shared_f32(row) * shared_f32(channels);
+        lane_wait(r.done + 8 * (r.block % kDone), r.block / kDone & 1, &g_gemm_error, abort_flag);
+        tc_fence_after();
+        const uint32_t product = r.block % kProducts;
+        if (there) add_block<C>(acc, taddr + product * NT, r.empty + 8 * product, first, scale);
+        else if (first) arrive(r.empty + 8 * product);
+        ++r.block;
+        row += kBlockFloats * 4;
+        channels += kBlockFloats * 4;
+      } while (row != last);
+    }
     __syncwarp();
     if (first) arrive(sc.empty + 8 * sc.at);
     if (++sc.at == kScaleSlots) { sc.at = 0; sc.ph ^= 1; }
@@ -699,11 +717,11 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
 void test_withhold(int on) { t_withhold = on; }
 
 cudaError_t launch_gemm(const GemmArgs& a, int num_sms, cudaStream_t s) {
-  // Narrow tiles while each has an SM of its own, wide ones beyond. A block of K takes a CTA some 290 ns with 128 channels
-  // and 215 with 64; rows fetched for 64 channels are fetched twice as often. GB300, us, 128 / 64: 333 x 2,560 x 1,537
-  // 10.3 / 8.1; 32 rows of 512 experts, 2,560 x 1,536 27 / 32; 1 x 2,560 x 157,184 68 / 85; 4,096 x 2,048 x 4,096
-  // 40 / 57; 32,768 rows of 256 experts, 2,048 x 1,024 115 / 158. (256 channels: 16, 33, 76, 41, 118: two warps a
-  // scheduler with 128 sums a lane have no registers left to keep loads from tensor memory on their way.)
+  // Narrow tiles while each has an SM of its own, wide ones beyond: a block of K takes a CTA some 290 ns with 128 channels
+  // and 190 with 64, and rows fetched for 64 channels are fetched twice as often. GB300, us, 128 / 64: 333 x 2,560 x 1,537
+  // 10.5 / 8.0; 32 rows of 512 experts, 2,560 x 1,536 27.4 / 27.7; 1 x 2,560 x 157,184 66 / 70; 4,096 x 2,048 x 4,096
+  // 41 / 49; 32,768 rows of 256 experts, 2,048 x 1,024 116 / 137. (256 channels: 16, 33, 76, 41, 118: with 128 sums a lane
+  // the registers are full, and loads from tensor memory wait for the sums of those before.)
   const int64_t groups = a.offsets ? (a.rows < a.groups ? a.rows : a.groups) : 1;
   const int64_t tm = a.offsets ? (a.rows / kRows > groups ? a.rows / kRows : groups) : (a.rows + kRows - 1) / kRows;
   return tm * ((a.channels + 63) / 64) <= num_sms ? launch_tile<64>(a, num_sms, s) : launch_tile<128>(a, num_sms, s);
