@@ -174,16 +174,15 @@ def dispatch_tokens(x: torch.Tensor, idx: torch.Tensor, num_experts: int, x_scal
     and pos is ~row, below 0. With x_scale (fp32 [T, n], the scales of quantized rows) the
     result is (rows, row_scale [T k, n], offsets, pos).
 
-    rows are differentiable with respect to x (without x_scale), once; idx has no gradient.
+    rows of fp32, bf16 or fp16 (without x_scale) are differentiable with respect to x, once; idx has no gradient.
     """
     if stream is not None or elsewhere(x):
         return run_on(stream, dispatch_tokens, x, idx, num_experts, x_scale)
     refuse_tangents("dispatch_tokens", x, x_scale)
-    if x_scale is None:
-        if x.requires_grad and torch.is_grad_enabled():
-            return _Dispatch.apply(x, idx, num_experts)
-    else:
-        refuse_gradients("dispatch_tokens with x_scale", x, x_scale)
+    if x_scale is not None or x.dtype not in FLOAT_CODES:
+        refuse_gradients("dispatch_tokens of quantized rows", x, x_scale)
+    elif x.requires_grad and torch.is_grad_enabled():
+        return _Dispatch.apply(x, idx, num_experts)
     return _dispatch(x, idx, num_experts, x_scale)
 
 

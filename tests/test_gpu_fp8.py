@@ -133,7 +133,7 @@ def test_quantize_rows_apart_and_none():
 # ---------------------------------------------------------------------------------------- products
 SHAPES = [(1, 16, 1), (1, 128, 8), (1, 2048, 1024), (2, 144, 129), (17, 272, 77), (33, 128, 64), (65, 1040, 200),
           (127, 384, 256), (128, 256, 128), (129, 512, 257), (300, 2560, 1537), (1000, 128, 16), (40, 65536, 24),
-          (1500, 400, 4104)]
+          (1500, 400, 4104), (1300, 1024, 2056), (200, 512, 9000)]
 
 
 @pytest.mark.parametrize("out", list(DT))
@@ -228,7 +228,8 @@ def _offsets(counts):
 GROUPS = [([1], 16, 8), ([8, 0, 0, 3], 128, 64), ([0, 0, 5, 0], 144, 72), ([128, 129, 0, 1, 300, 127], 272, 200),
           ([1] * 40, 256, 136), ([0] * 100 + [7] + [0] * 155, 512, 24), ([2000, 3], 128, 520), ([3] * 1024, 32, 16),
           ([40, 60, 16, 33, 64, 65], 640, 1000), ([0, 700, 0, 0, 900], 400, 128),
-          ([(37 * i) % 301 for i in range(120)], 272, 200), ([17, 0, 33] * 30, 1168, 130)]
+          ([(37 * i) % 301 for i in range(120)], 272, 200), ([17, 0, 33] * 30, 1168, 130),
+          ([(53 * i) % 280 for i in range(120)], 512, 200)]
 
 
 @pytest.mark.parametrize("out", list(DT))

@@ -215,7 +215,8 @@ def test_inputs_that_would_lose_a_gradient_or_a_tangent_are_refused():
     for call in (lambda: M.fp8_quantize(leaf), lambda: M.fp8_matmul(leaf, x, x), lambda: M.fp8_matmul(x, x, leaf),
                  lambda: M.fp8_matmul(x, x, x, leaf), lambda: M.fp8_grouped_matmul(leaf, idx, x, x),
                  lambda: M.fp8_grouped_matmul(x, idx, x, leaf), lambda: M.dispatch_tokens(leaf, idx, 4, x),
-                 lambda: M.dispatch_tokens(x, idx, 4, leaf)):
+                 lambda: M.dispatch_tokens(x, idx, 4, leaf),
+                 lambda: M.dispatch_tokens(x.to(torch.float8_e4m3fn).requires_grad_(), idx, 4)):
         with pytest.raises(ValueError, match="gradient"):
             call()
     with forward_ad.dual_level():
