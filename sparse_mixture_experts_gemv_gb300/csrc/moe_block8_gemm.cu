@@ -25,6 +25,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_block8.h"
 #include "moe_internal.h"
 #include "moe_sm100.cuh"
@@ -263,10 +265,107 @@ MOE_DEV void add_block(float2 (&acc)[16 * C], uint32_t taddr, uint32_t empty, bo
   }
 }
 
-// All blocks of a tile. Instructions other than the sums bound it, some 80 a block and warp where places are counted
-// block by block: parameters are held in registers (behind the barriers' memory clobbers they would be read again every
-// time), and where the blocks come in fours (K a multiple of 512) four are unrolled, whose barriers, scales and products
-// follow each other. `there` false: no rows or channels, and the products are let go.
+// At constant distances from an address: in unrolled code sums of addresses are made ahead of their use, and their
+// registers are missing then.
+template <int AT>
+MOE_DEV float shared_f32_at(uint32_t a) {
+  float f;
+  asm volatile("ld.shared.f32 %0, [%1+%2];" : "=f"(f) : "r"(a), "n"(AT) : "memory");
+  return f;
+}
+template <int AT>
+MOE_DEV void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0+%1];" :: "r"(bar), "n"(AT) : "memory");
+}
+template <int AT>
+MOE_DEV void lane_wait_at(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1+%3], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity), "n"(AT) : "memory");
+  if (!ok) lane_wait(bar + AT, parity, err, abort);
+  __syncwarp();
+}
+template <int AT>
+MOE_DEV void tmem_request32_at(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32+%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr), "n"(AT));
+}
+
+// All blocks of a tile, which come in fours: four are unrolled, whose barriers, scales and products follow each other.
+// With two chunks a block (C = 2) the next block's first is on its way while this one's last is added (the request behind
+// the last block is not used; one under a condition would cost copies of its registers): 4,096 x 2,048 x 4,096 40 -> 38 us.
+// With one it only waits for a product that is not there yet.
+template <int C, int NT>
+MOE_DEV void add_fours(float2 (&acc)[16 * C], Scales& scales, Ring& ring, uint32_t taddr, int blocks,
+                       volatile int* abort_flag) {
+  constexpr uint32_t kProducts = 512 / NT;
+  Scales sc = scales;
+  uint32_t block = ring.block;
+  const bool first = (threadIdx.x & 31) == 0;
+  uint32_t v[2][32];
+  if constexpr (C == 2) {
+    lane_wait(ring.done + 8 * (block % kDone), block / kDone & 1, &g_gemm_error, abort_flag);
+    tc_fence_after();
+    tmem_request32(taddr + block % kProducts * NT, v[0]);
+  }
+#pragma unroll 1
+  for (int b0 = 0; b0 < blocks; b0 += 4) {
+    lane_wait(sc.full + 8 * sc.at, sc.ph, &g_gemm_error, abort_flag);
+    const uint32_t row = sc.row + sc.at * (kSlotFloats * 4), channels = sc.channels + sc.at * (kSlotFloats * 4);
+    const uint32_t done = ring.done + 8 * (block % kDone), ph = block / kDone & 1, product = block % kProducts;
+    const uint32_t to = taddr + product * NT, empty = ring.empty + 8 * product;
+    block += 4;
+    const auto one = [&](auto index) {
+      constexpr int q = decltype(index)::value;
+      const float scale = shared_f32_at<q * kBlockFloats * 4>(row) * shared_f32_at<q * kBlockFloats * 4>(channels);
+      if constexpr (C == 2) {
+        tmem_arrived32(v[0]);
+        tmem_request32_at<q * NT + 32>(to, v[1]);
+        add32(acc, v[0], scale);
+      } else {
+        lane_wait_at<8 * q>(done, ph, &g_gemm_error, abort_flag);
+        tc_fence_after();
+        tmem_request32_at<q * NT>(to, v[1]);
+      }
+      tmem_arrived32(v[1]);
+      tc_fence_before();
+      __syncwarp();
+      if (first) arrive_at<8 * q>(empty);
+      if constexpr (C == 2) {
+        if constexpr (q < 3) {
+          lane_wait_at<8 * (q + 1)>(done, ph, &g_gemm_error, abort_flag);
+          tc_fence_after();
+          tmem_request32_at<(q + 1) * NT>(to, v[0]);
+        } else {
+          if (b0 + 4 < blocks) lane_wait(ring.done + 8 * (block % kDone), block / kDone & 1, &g_gemm_error, abort_flag);
+          tc_fence_after();
+          tmem_request32(taddr + block % kProducts * NT, v[0]);
+        }
+      }
+      add32(acc + 16 * (C - 1), v[1], scale);
+    };
+    one(std::integral_constant<int, 0>());
+    one(std::integral_constant<int, 1>());
+    one(std::integral_constant<int, 2>());
+    one(std::integral_constant<int, 3>());
+    __syncwarp();
+    if (first) arrive(sc.empty + 8 * sc.at);
+    if (++sc.at == kScaleSlots) { sc.at = 0; sc.ph ^= 1; }
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");   // the last request's registers are others' next
+  scales = sc;
+  ring.block = block;
+}
+
+// All blocks of any tile. `there` false: no rows or channels, and the products are let go. (Parameters are held in
+// registers: behind the barriers' memory clobbers they would be read again every time.)
 template <int C, int NT>
 MOE_DEV void add_blocks(float2 (&acc)[16 * C], Scales& scales, Ring& ring, uint32_t taddr, int blocks, bool there,
                         volatile int* abort_flag) {
@@ -278,32 +377,19 @@ MOE_DEV void add_blocks(float2 (&acc)[16 * C], Scales& scales, Ring& ring, uint3
   for (int b0 = 0; b0 < blocks; b0 += 4) {
     lane_wait(sc.full + 8 * sc.at, sc.ph, &g_gemm_error, abort_flag);
     uint32_t row = sc.row + sc.at * (kSlotFloats * 4), channels = sc.channels + sc.at * (kSlotFloats * 4);
-    if (there && blocks % 4 == 0) {
-      const uint32_t done = r.done + 8 * (r.block % kDone), ph = r.block / kDone & 1, product = r.block % kProducts;
-      const uint32_t to = taddr + product * NT, empty = r.empty + 8 * product;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float scale = shared_f32(row + q * (kBlockFloats * 4)) * shared_f32(channels + q * (kBlockFloats * 4));
-        lane_wait(done + 8 * q, ph, &g_gemm_error, abort_flag);
-        tc_fence_after();
-        add_block<C>(acc, to + q * NT, empty + 8 * q, first, scale);
-      }
-      r.block += 4;
-    } else {
-      const uint32_t last = row + min(4, blocks - b0) * (kBlockFloats * 4);
+    const uint32_t last = row + min(4, blocks - b0) * (kBlockFloats * 4);
 #pragma unroll 1
-      do {
-        const float scale = shared_f32(row) * shared_f32(channels);
-        lane_wait(r.done + 8 * (r.block % kDone), r.block / kDone & 1, &g_gemm_error, abort_flag);
-        tc_fence_after();
-        const uint32_t product = r.block % kProducts;
-        if (there) add_block<C>(acc, taddr + product * NT, r.empty + 8 * product, first, scale);
-        else if (first) arrive(r.empty + 8 * product);
-        ++r.block;
-        row += kBlockFloats * 4;
-        channels += kBlockFloats * 4;
-      } while (row != last);
-    }
+    do {
+      const float scale = shared_f32(row) * shared_f32(channels);
+      lane_wait(r.done + 8 * (r.block % kDone), r.block / kDone & 1, &g_gemm_error, abort_flag);
+      tc_fence_after();
+      const uint32_t product = r.block % kProducts;
+      if (there) add_block<C>(acc, taddr + product * NT, r.empty + 8 * product, first, scale);
+      else if (first) arrive(r.empty + 8 * product);
+      ++r.block;
+      row += kBlockFloats * 4;
+      channels += kBlockFloats * 4;
+    } while (row != last);
     __syncwarp();
     if (first) arrive(sc.empty + 8 * sc.at);
     if (++sc.at == kScaleSlots) { sc.at = 0; sc.ph ^= 1; }
@@ -574,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
       float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      add_blocks<kCols / 32, NT>(acc, sc, ring, taddr, blocks, there, abort_flag);
+      if (there && blocks % 4 == 0) add_fours<kCols / 32, NT>(acc, sc, ring, taddr, blocks, abort_flag);
+      else add_blocks<kCols / 32, NT>(acc, sc, ring, taddr, blocks, there, abort_flag);
       if (!there) continue;
       const int64_t row0 = t.row0 + quad * 32;
       constexpr int kUnits = kCols / 32;
@@ -717,11 +804,11 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
 void test_withhold(int on) { t_withhold = on; }
 
 cudaError_t launch_gemm(const GemmArgs& a, int num_sms, cudaStream_t s) {
-  // Narrow tiles while each has an SM of its own, wide ones beyond: a block of K takes a CTA some 290 ns with 128 channels
+  // Narrow tiles while each has an SM of its own, wide ones beyond: a block of K takes a CTA some 270 ns with 128 channels
   // and 190 with 64, and rows fetched for 64 channels are fetched twice as often. GB300, us, 128 / 64: 333 x 2,560 x 1,537
-  // 10.5 / 8.0; 32 rows of 512 experts, 2,560 x 1,536 27.4 / 27.7; 1 x 2,560 x 157,184 66 / 70; 4,096 x 2,048 x 4,096
-  // 41 / 49; 32,768 rows of 256 experts, 2,048 x 1,024 116 / 137. (256 channels: 16, 33, 76, 41, 118: with 128 sums a lane
-  // the registers are full, and loads from tensor memory wait for the sums of those before.)
+  // 9.8 / 8.1; 32 rows of 512 experts, 2,560 x 1,536 25.8 / 27.5; 1 x 2,560 x 157,184 65 / 70; 4,096 x 2,048 x 4,096
+  // 36 / 49; 32,768 rows of 256 experts, 2,048 x 1,024 113 / 138. (256 channels, before the epilogue's last steps: 16, 33,
+  // 76, 41, 118: with 128 sums a lane the registers are full, and loads from tensor memory wait for the sums before.)
   const int64_t groups = a.offsets ? (a.rows < a.groups ? a.rows : a.groups) : 1;
   const int64_t tm = a.offsets ? (a.rows / kRows > groups ? a.rows / kRows : groups) : (a.rows + kRows - 1) / kRows;
   return tm * ((a.channels + 63) / 64) <= num_sms ? launch_tile<64>(a, num_sms, s) : launch_tile<128>(a, num_sms, s);
