@@ -70,6 +70,13 @@ MOE_DEV void divide(float (&v)[16], float scale) {
   }
 }
 
+// The larger of two magnitudes; NaN if one of them is.
+MOE_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Sixteen values a thread, eight threads a block of 128: its largest value comes from three exchanges, so that the
 // rows are read once. The scale is a product with the rounded 1/448, and the quotient is rounded to fp32
 // before E4M3: what elementary operations on tensors give, bit for bit. A block with an infinity or a NaN
@@ -93,12 +100,14 @@ __global__ void __launch_bounds__(kThreads) block8_quantize_kernel(const Quantiz
         silu_mul(v, u);
       }
     }
-    uint32_t top = int8::amax_bits(v);
+    float top = fabsf(v[0]);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    for (int j = 1; j < 16; ++j) top = max_nan(top, fabsf(v[j]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     if (!in) continue;
-    float scale = __uint_as_float(top) * (1.f / 448.f);
-    if (top >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);
+    float scale = top * (1.f / 448.f);
+    if (!(top <= 3.402823466e38f)) scale = __uint_as_float(0x7FC00000u);
     else if (scale == 0.f) scale = 1.f;
     divide(v, scale);
     uint32_t w[4];

@@ -28,6 +28,7 @@ constexpr int kBuckets = MOE_DISPATCH_MAX_EXPERTS + 1;   // the last one: no exp
 constexpr int kFusedThreads = 512;
 constexpr int kThreads = 1024;
 constexpr int kFusedChoices = 2048;            // so many are placed by every CTA for itself
+constexpr int kCountedChoices = 32768;         // and so many counted
 
 template <int THREADS>
 struct PlanShared {
@@ -217,7 +218,8 @@ __global__ void __launch_bounds__(kThreads) dispatch_count_kernel(const Dispatch
 }
 
 // Then every CTA adds up all chunks' numbers and those before its own, eight experts a load, places its chunk and copies
-// its rows. 4,096 tokens of 2,048 bytes, k = 8: 20 us with the counts; 8,191 of 5,120 bytes, k = 8: 68 us, 5.6 TB/s.
+// its rows. Up to kCountedChoices it counts them all for itself, four a load, which takes it some 3 us, a launch of the
+// counts 5. 4,096 tokens of 2,048 bytes, k = 8: 20 us; 8,191 of 5,120 bytes, k = 8: 69 us with the counts before it, 5.5 TB/s.
 template <class V>
 __global__ void __launch_bounds__(kThreads, 1) dispatch_chunk_kernel(const DispatchParams p) {
   __shared__ PlanShared<kThreads> s;
@@ -225,8 +227,25 @@ __global__ void __launch_bounds__(kThreads, 1) dispatch_chunk_kernel(const Dispa
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, (int64_t)p.T);
   const int groups = p.stride / 8, parts = kThreads / groups, part = threadIdx.x / groups, g = threadIdx.x % groups;
-  if (part < parts) {
+  if (!p.counts) {
+    // the choices before the chunk into the one, the others into the other
+    const int n = p.T * p.k, own = (int)t0 * p.k, fours = (uintptr_t)p.idx & 15 ? 0 : n / 4;
+    const auto count = [&](int a, int e) { atomicAdd(a < own ? &s.cursor[bucket_of(e, p.E)] : &s.hist[bucket_of(e, p.E)], 1); };
+#pragma unroll 4
+    for (int f = threadIdx.x; f < fours; f += kThreads) {
+      const int4 e = __ldg(reinterpret_cast<const int4*>(p.idx) + f);
+      count(4 * f, e.x);
+      count(4 * f + 1, e.y);
+      count(4 * f + 2, e.z);
+      count(4 * f + 3, e.w);
+    }
+#pragma unroll 4
+    for (int a = 4 * fours + threadIdx.x; a < n; a += kThreads) count(a, __ldg(p.idx + a));
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) s.hist[e] += s.cursor[e];
+  } else if (part < parts) {
     int all[8] = {}, before[8] = {};
 #pragma unroll 4
     for (int c = part; c < p.chunks; c += parts) {
@@ -246,7 +265,6 @@ __global__ void __launch_bounds__(kThreads, 1) dispatch_chunk_kernel(const Dispa
       atomicAdd(&s.cursor[8 * g + l], before[l]);
     }
   }
-  const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, (int64_t)p.T);
   place(s, p.idx, t0 * p.k, t1 * p.k, p.E, blockIdx.x == 0 ? p.offsets : nullptr,
         [&](int64_t a, int row) { p.pos[a] = row; });
   copy_tokens<V>(p, t0, t1, threadIdx.x >> 5, kThreads / 32, [&](int64_t a) { return ldg_cg_s32(p.pos + a); });
@@ -469,7 +487,7 @@ Chunks chunks_of(int64_t T, int64_t k, int64_t E) {
   c.chunk = (int)(each < most ? each : most);
   c.chunks = (int)((T + c.chunk - 1) / c.chunk);
   c.stride = (int)((E + 1 + 7) / 8 * 8);
-  c.bytes = ((int64_t)c.chunks * c.stride * 2 + 255) / 256 * 256;
+  c.bytes = T * k <= kCountedChoices ? 0 : ((int64_t)c.chunks * c.stride * 2 + 255) / 256 * 256;
   return c;
 }
 
@@ -481,7 +499,7 @@ cudaError_t launch_dispatch(const DispatchParams& p, int sms, cudaStream_t s) {
     if (grid > 2 * sms) grid = 2 * sms;
     return launch(dispatch_fused_kernel<V>, grid < 1 ? 1 : grid, kFusedThreads, s, p);
   }
-  const cudaError_t e = launch(dispatch_count_kernel, p.chunks, kThreads, s, p);
+  const cudaError_t e = p.counts ? launch(dispatch_count_kernel, p.chunks, kThreads, s, p) : cudaSuccess;
   return e != cudaSuccess ? e : launch(dispatch_chunk_kernel<V>, p.chunks, kThreads, s, p);
 }
 
@@ -554,7 +572,7 @@ moe_status_t moe_dispatch_tokens(const void* x_dev, int64_t row_bytes, int64_t r
   const Chunks c = chunks_of(T, k, E);
   if (c.bytes && (!workspace_dev || workspace_bytes < c.bytes || (uintptr_t)workspace_dev & 255)) return MOE_ERR_INVALID_ARG;
   const DispatchParams p = {(const uint8_t*)x_dev, row_stride, row_bytes, x_scale_dev, scales, idx_dev, T, k, E,
-                            (uint8_t*)rows_dev, row_scale_dev, offsets_dev, pos_dev, (uint16_t*)workspace_dev, c.chunk,
+                            (uint8_t*)rows_dev, row_scale_dev, offsets_dev, pos_dev, c.bytes ? (uint16_t*)workspace_dev : nullptr, c.chunk,
                             c.chunks, c.stride};
   // the widest vector that every row starts and ends on
   const uint64_t a = (uintptr_t)x_dev | (uintptr_t)rows_dev | (uint64_t)row_bytes | (T > 1 ? (uint64_t)row_stride : 0);

@@ -44,9 +44,11 @@ def _check_dispatch(x, idx, E, got):
     np.testing.assert_array_equal(_bytes(rows), o.dispatch(_bytes(x), want_pos))
 
 
-# (T, k, E, H): one launch up to 2,048 choices, with one segment of 512 and several; two launches beyond
+# (T, k, E, H): up to 2,048 choices every CTA places all, in one segment of 512 and in several; up to 32,768 it counts
+# all and places its chunk; beyond, a launch counts. Chunks of more than 1,024 choices have several segments.
 SHAPES = [(1, 8, 256, 2048), (1, 1, 1, 1), (3, 2, 5, 7), (64, 8, 16, 33), (65, 8, 1024, 130), (256, 8, 64, 24),
-          (257, 8, 64, 24), (2049, 1, 1, 5), (70, 32, 3, 260), (1000, 7, 1023, 96), (5000, 3, 511, 9)]
+          (257, 8, 64, 24), (2049, 1, 1, 5), (70, 32, 3, 260), (1000, 7, 1023, 96), (5000, 3, 511, 9),
+          (4096, 8, 256, 16), (4097, 8, 256, 16), (9000, 32, 1024, 4), (6007, 31, 40, 3)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -97,6 +99,16 @@ def test_dispatch_of_rows_apart_and_off_their_boundaries():
     _check_dispatch(wide, turned, 6, M.dispatch_tokens(wide, turned, 6))
     b = wide.view(torch.uint8)[:, 3:200]
     _check_dispatch(b, idx, 6, M.dispatch_tokens(b, idx, 6))
+
+
+@pytest.mark.parametrize("T", [100, 3000, 20000])
+def test_choices_off_their_boundaries(T):
+    """A view whose first choice lies off a 16-byte boundary."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    x = torch.randn(T, 12, generator=_gen(1), device="cuda")
+    idx = _idx(T + 1, 3, 40)[1:]
+    assert idx.is_contiguous() and idx.data_ptr() % 16
+    _check_dispatch(x, idx, 40, M.dispatch_tokens(x, idx, 40))
 
 
 def test_dispatch_of_no_tokens():

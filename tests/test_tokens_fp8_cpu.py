@@ -76,8 +76,8 @@ def test_the_c_calls_refuse_bad_arguments_before_touching_the_device():
     assert [dispatch(T=-1), dispatch(k=0), dispatch(E=0), dispatch(row=0), dispatch(stride=63), dispatch(x=None),
             dispatch(idx=None), dispatch(rows=None), dispatch(offsets=None), dispatch(pos=None), dispatch(idx=far[1] + 2),
             dispatch(xs=far[5]), dispatch(scales=3), dispatch(xs=far[5], scales=3), dispatch(rows=far[0] + 16),
-            dispatch(pos=far[1] + 4), dispatch(T=2000), dispatch(T=2000, ws=far[6], nb=100),
-            dispatch(T=2000, ws=far[6] + 16, nb=1 << 20)] == [bad] * 19
+            dispatch(pos=far[1] + 4), dispatch(T=20000), dispatch(T=20000, ws=far[6], nb=100),
+            dispatch(T=20000, ws=far[6] + 16, nb=1 << 20)] == [bad] * 19
     assert [dispatch(k=33), dispatch(E=1025), dispatch(T=1 << 29, k=4)] == [out] * 3
 
     def combine(y=far[0], dtype=1, stride=64, pos=far[1], w=far[2], T=4, k=2, H=64, out_=far[3]):
