@@ -355,8 +355,8 @@ MOE_DEV void keep(Choices& s, int turn, const CombineParams& p, int at, float w)
   }
 }
 
-// out[t] = sum_j w y[pos], in 32 bits and in the order of the choices. One CTA a token, one barrier a token. 8,191 tokens
-// of 2,048 bf16, k = 8: see the table of cases.
+// out[t] = sum_j w y[pos], in 32 bits and in the order of the choices. One CTA a token, one barrier a token. Memory
+// bounds it: 8,191 tokens of 2,048 bf16, k = 8: 48 us, 6.0 TB/s.
 template <int DT, int N>
 __global__ void __launch_bounds__(kMaxThreads) combine_kernel(const CombineParams p) {
   __shared__ Choices s;
@@ -395,7 +395,8 @@ __global__ void __launch_bounds__(kMaxThreads) combine_kernel(const CombineParam
 }
 
 // d_y[pos] = w d_out[t] and d_w = <d_out[t], y[pos]>, eight choices at a time: each thread adds up its columns, then
-// the CTA adds the threads' sums, in a fixed order.
+// the CTA adds the threads' sums, in a fixed order. 8,191 tokens of 2,048 bf16, k = 8: 87 us, 6.4 TB/s (80 registers a
+// thread instead of 64, three CTAs an SM: 97).
 template <int DT, int N>
 __global__ void __launch_bounds__(kMaxThreads, 4) combine_backward_kernel(const CombineParams p) {
   __shared__ Choices s;
