@@ -5,12 +5,11 @@
 //   q = E4M3(fp32(v / scale)),   v = x, or g / (1 + e^-g) u of the row's halves g and u
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "moe_block8.cuh"
 #include "moe_block8.h"
-#include "moe_int8.cuh"
 #include "moe_int8.h"
 #include "moe_internal.h"
 
@@ -50,33 +49,6 @@ MOE_DEV void silu_mul(float (&g)[16], const float (&u)[16]) {
   }
 }
 
-// The quotients of 16 values of a block by its scale, rounded to the nearest fp32 each: the product with the correctly
-// rounded reciprocal is off by two steps at most, one correction by its exact remainder by less than one, and from
-// there a second one is the rounded quotient (Markstein, IBM Journal of Research and Development 34, 1990). Remainders
-// are exact while nothing leaves the normal range: scales beyond 2^+-90 (or NaN) take the division. Values below 2^-10
-// of the scale, whose remainder may, are 0 in E4M3 either way.
-MOE_DEV void divide(float (&v)[16], float scale) {
-  if (scale >= 0x1p-90f && scale <= 0x1p90f) {
-    const float inv = 1.f / scale;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float q = v[i] * inv;
-      q = fmaf(fmaf(-q, scale, v[i]), inv, q);
-      v[i] = fmaf(fmaf(-q, scale, v[i]), inv, q);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], scale);
-  }
-}
-
-// The larger of two magnitudes; NaN if one of them is.
-MOE_DEV float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Sixteen values a thread, eight threads a block of 128: its largest value comes from three exchanges, so that the
 // rows are read once. The scale is a product with the rounded 1/448, and the quotient is rounded to fp32
 // before E4M3: what elementary operations on tensors give, bit for bit. A block with an infinity or a NaN
@@ -101,24 +73,9 @@ __global__ void __launch_bounds__(kThreads) block8_quantize_kernel(const Quantiz
         silu_mul(v, u);
       }
     }
-    float top = fabsf(v[0]);
-#pragma unroll
-    for (int j = 1; j < 16; ++j) top = max_nan(top, fabsf(v[j]));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float scale = block_scale(v);
     if (!in) continue;
-    float scale = top * (1.f / 448.f);
-    if (!(top <= 3.402823466e38f)) scale = __uint_as_float(0x7FC00000u);
-    else if (scale == 0.f) scale = 1.f;
-    divide(v, scale);
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j], v[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j + 2], v[4 * j + 3]), __NV_SATFINITE, __NV_E4M3);
-      w[j] = lo | hi << 16;
-    }
-    *reinterpret_cast<uint4*>(p.q + t * p.K + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p.q + t * p.K + c) = to_e4m3(v, scale);
     if (c % kBlock == 0) p.scale[t * p.blocks + c / kBlock] = scale;
   }
 }
@@ -162,9 +119,9 @@ int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 bool is_float(int dtype) { return dtype >= MOE_DTYPE_F32 && dtype <= MOE_DTYPE_F16; }
 
-// Rows that come in another type are quantized to scratch: values, then scales.
+// Rows that come in another type are quantized to scratch: values, then scales. Few rows are quantized inside the product.
 int64_t scratch(int64_t rows, int64_t K, int dtype) {
-  return dtype == MOE_DTYPE_E4M3 ? 0 : pad256(rows * K) + pad256(rows * blocks_of((int)K) * 4);
+  return dtype == MOE_DTYPE_E4M3 || quantized_inside(rows, K) ? 0 : pad256(rows * K) + pad256(rows * blocks_of((int)K) * 4);
 }
 
 // rows, K and N in range, and whether there is anything to do (*st MOE_OK if it returns false)
@@ -205,11 +162,13 @@ moe_status_t product(const void* x, int x_dtype, int64_t x_stride, const float* 
     q.scale = (float*)((uint8_t*)workspace + pad256((int64_t)g.rows * g.K));
     e = launch_quantize(q, x_dtype, false, s);
     g.early = 1;
+    g.x_dtype = MOE_DTYPE_E4M3;
     g.x = q.q;
     g.x_stride = g.K;
     g.x_scale = q.scale;
   } else {
     g.x = x;
+    g.x_dtype = x_dtype;
     g.x_stride = x_stride;
     g.x_scale = x_scale;
   }

@@ -16,7 +16,8 @@
 // One persistent CTA an SM, warp-specialised:
 //   warp 0        weights by TMA into a ring, a block of K a stage
 //   warp 1        issues the MMAs
-//   warp 2        rows by TMA into the same ring
+//   warp 2        rows by TMA into the same ring (or, few rows of another type: they are quantized once, by warps 2-11,
+//                 into an operand that stays in shared memory, and the ring holds weights alone)
 //   warp 3        scales into a ring of their own, four blocks a slot
 //   warps 4-11    epilogue: four warps for each half of the columns
 //
@@ -31,6 +32,7 @@
 
 #include <type_traits>
 
+#include "moe_block8.cuh"
 #include "moe_block8.h"
 #include "moe_internal.h"
 #include "moe_sm100.cuh"
@@ -74,6 +76,9 @@ struct Params {
   int blocks;                // of K
   int row_blocks;            // channels' blocks of 128
   int stages, stage_bytes, a_bytes;
+  const void* x;             // RAW: rows of x_dtype, x_stride elements apart
+  int x_dtype, K, raw_bytes; // raw_bytes: the operand of 16 rows and their scales in shared memory
+  int64_t x_stride;
   const float* x_scale;
   const float* w_scale;
   void* out;
@@ -429,8 +434,9 @@ MOE_DEV void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "me
 MOE_DEV void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 MOE_DEV void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// A unit of fewer rows than 32 (the next ones are another group's), or of rows off 16-byte boundaries, by the warp.
-MOE_DEV void copy_unit(const uint8_t* unit, const Params& p, int64_t row0, int rows, int ch0, int size) {
+// A unit of fewer rows than 32 (the others are another group's), or of rows off 16-byte boundaries, by the warp: rows
+// from .. rows.
+MOE_DEV void copy_unit(const uint8_t* unit, const Params& p, int64_t row0, int from, int rows, int ch0, int size) {
   const int lane = threadIdx.x & 31;
   const int64_t ld = (int64_t)p.channels * size;
   uint8_t* out = static_cast<uint8_t*>(p.out) + row0 * ld + (int64_t)ch0 * size;
@@ -440,20 +446,20 @@ MOE_DEV void copy_unit(const uint8_t* unit, const Params& p, int64_t row0, int r
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 8 * i + (lane >> 2);
-      if (r < rows && 16 * c < n)
+      if (r >= from && r < rows && 16 * c < n)
         *reinterpret_cast<uint4*>(out + r * ld + 16 * c) =
             *reinterpret_cast<const uint4*>(unit + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
     }
   } else if (size == 4) {
     const int b = (lane & 15) * 4;
     if (b < n)
-      for (int i = lane >> 4; i < rows; i += 2)
+      for (int i = from + (lane >> 4); i < rows; i += 2)
         *reinterpret_cast<uint32_t*>(out + i * ld + b) =
             *reinterpret_cast<const uint32_t*>(unit + i * 64 + (((b >> 4) ^ (i >> 1 & 3)) << 4) + (b & 15));
   } else {
     const int b = lane * 2;
     if (b < n)
-      for (int i = 0; i < rows; ++i)
+      for (int i = from; i < rows; ++i)
         *reinterpret_cast<uint16_t*>(out + i * ld + b) =
             *reinterpret_cast<const uint16_t*>(unit + i * 64 + (((b >> 4) ^ (i >> 1 & 3)) << 4) + (b & 15));
   }
@@ -461,9 +467,10 @@ MOE_DEV void copy_unit(const uint8_t* unit, const Params& p, int64_t row0, int r
 
 // N units of `step` channels from ch0 on leave.
 template <int N>
-MOE_DEV void store_units(uint8_t* turn, const CUtensorMap* map, const Params& p, int64_t row0, int rows, int ch0, int size) {
+MOE_DEV void store_units(uint8_t* turn, const CUtensorMap* map, const Params& p, int64_t row0, int from, int rows, int ch0,
+                         int size) {
   const int step = 64 / size;
-  if (p.wide && rows == 32) {
+  if (p.wide && rows - from == 32) {
     fence_proxy_async_smem();
     __syncwarp();
     if (elect()) {
@@ -474,18 +481,38 @@ MOE_DEV void store_units(uint8_t* turn, const CUtensorMap* map, const Params& p,
   } else {
     __syncwarp();
     for (int c = 0; c < N; ++c)
-      if (ch0 + c * step < p.channels) copy_unit(turn + c * 2048, p, row0, rows, ch0 + c * step, size);
+      if (ch0 + c * step < p.channels) copy_unit(turn + c * 2048, p, row0, from, rows, ch0 + c * step, size);
   }
 }
 
-// NT: channels of a tile.
-template <int NT>
+// Few rows of another type to the operand of 16 rows, blocks of 128 behind each other in the 128-byte swizzle, and their
+// scales [block][16] behind that. Rows that there are not stay as they are: results go by rows.
+template <int DT>
+MOE_DEV void quantize_rows(const Params& p, uint8_t* operand, float* scales, int thread, int threads) {
+  const int per_row = p.blocks * 8, n = p.rows * per_row;
+  for (int i = thread; i - (thread & 31) < n; i += threads) {
+    const int t = i / per_row, c = i % per_row, b = c >> 3;
+    const bool in = i < n && c * 16 < p.K;
+    float v[16] = {};
+    if (in) int8::load16<DT>(p.x, t * p.x_stride + 16 * c, v);
+    const float scale = block_scale(v);
+    if (i >= n) continue;
+    const uint4 q = in ? to_e4m3(v, scale) : make_uint4(0, 0, 0, 0);   // zeros behind K
+    *reinterpret_cast<uint4*>(operand + b * 2048 + t * kBlock + (((c & 7) ^ (t & 7)) << 4)) = q;
+    if ((c & 7) == 0) scales[b * 16 + t] = scale;
+  }
+}
+
+// NT: channels of a tile. RAW: quantized_inside().
+template <int NT, bool RAW>
 __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr int kProducts = 512 / NT;       // in tensor memory at once
   static_assert(kProducts <= kDone, "a completion each");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* s_turn = smem + p.stages * p.stage_bytes;
+  const int raw_bytes = RAW ? p.raw_bytes : 0;
+  uint8_t* s_turn = smem + raw_bytes + p.stages * p.stage_bytes;
+  float* s_raw_scale = reinterpret_cast<float*>(smem + p.blocks * 2048);
   int* first = reinterpret_cast<int*>(s_turn + kTurnBytes<NT>);
   int* row = first + kMaxGroups + 4;
   float* s_scale = reinterpret_cast<float*>(row + kMaxGroups + 4);
@@ -494,20 +521,22 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
   uint64_t* d_empty = done + kDone;
   uint64_t* sc_full = d_empty + kProducts;
   uint64_t* sc_empty = sc_full + kScaleSlots;
-  uint64_t* drain = sc_empty + kScaleSlots;
+  uint64_t* raw_ready = sc_empty + kScaleSlots;
+  uint64_t* drain = raw_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* scratch = reinterpret_cast<int*>(tmem_slot + 2);   // [kThreads / 32]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 2);
+    for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], RAW ? 1 : 2);
     for (int a = 0; a < kDone; ++a) mbar_init(&done[a], 1);
     for (int a = 0; a < kScaleSlots; ++a) {
       mbar_init(&sc_full[a], 1);
       mbar_init(&sc_empty[a], kEpilogueWarps);
     }
     for (int a = 0; a < kProducts; ++a) mbar_init(&d_empty[a], kEpilogueWarps);
+    mbar_init(raw_ready, kThreads / 32 - 2);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -529,8 +558,18 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
   Finder finder = {first, row, 0};
 
   // One completion a block, behind its MMAs: it frees the stage for the copies and hands the product to the epilogue.
-  const uint32_t full0 = smem_u32(full), done0 = smem_u32(done), ring0 = smem_u32(smem);
-  if (warp == 0 || warp == 2) {
+  const uint32_t full0 = smem_u32(full), done0 = smem_u32(done), ring0 = smem_u32(smem) + raw_bytes;
+  if (RAW && warp >= 2) {
+    float* scales = s_raw_scale;
+    const int thread = threadIdx.x - 64, threads = kThreads - 64;
+    if (p.x_dtype == MOE_DTYPE_BF16) quantize_rows<MOE_DTYPE_BF16>(p, smem, scales, thread, threads);
+    else if (p.x_dtype == MOE_DTYPE_F16) quantize_rows<MOE_DTYPE_F16>(p, smem, scales, thread, threads);
+    else quantize_rows<MOE_DTYPE_F32>(p, smem, scales, thread, threads);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(raw_ready);
+  }
+  if (warp == 0 || (!RAW && warp == 2)) {
     // ------------------------------------------------ weights (0), rows (2)
     if (p.early && warp == 2) {
       pdl_wait();
@@ -574,10 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
     const uint32_t stage_bytes = p.stage_bytes, a_bytes = p.a_bytes;
     int s = 0, ph = 0, ab = 0, d_ph = 1;
     uint32_t it = 0;
-    bool stop = false;
-    const auto issue = [&](int s, int ab, uint32_t it) {
+    bool stop = RAW && !warp_wait(smem_u32(raw_ready), 0, &g_gemm_error, abort_flag);
+    const auto issue = [&](int s, int ab, uint32_t it, int b) {
       const uint32_t at = ring0 + s * stage_bytes, d = tmem + ab * NT;
-      const uint64_t adesc = smem_desc_sw128(at), bdesc = smem_desc_sw128(at + a_bytes);
+      const uint64_t adesc = smem_desc_sw128(RAW ? smem_u32(smem) + b * 2048 : at), bdesc = smem_desc_sw128(at + a_bytes);
 #pragma unroll
       for (int kk = 0; kk < kBlock / 32; ++kk)   // 32 of K: 32 bytes, 2 in the descriptors
         mma_e4m3(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0 ? 1u : 0u);
@@ -599,8 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
         }
         tc_fence_after();
         if (elect()) {
-          issue(s, ab, it);
-          if (both) issue(s1, ab1, it + 1);
+          issue(s, ab, it, b);
+          if (both) issue(s1, ab1, it + 1, b + 1);
         }
         __syncwarp();
         s = s1; ph = ph1; ab = ab1; d_ph = d_ph1;
@@ -622,20 +661,24 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
     if (p.early) pdl_wait();
     const uint32_t sc_full0 = smem_u32(sc_full), sc_empty0 = smem_u32(sc_empty);
     int at = 0, ph = 1;
-    bool stop = false;
+    bool stop = RAW && !warp_wait(smem_u32(raw_ready), 0, &g_gemm_error, abort_flag);
     for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
       const Tile t = finder.find<NT>(p, tile);
       const float* ws = p.w_scale + ((int64_t)t.e * p.row_blocks + t.n0 / kBlock) * p.blocks;
       for (int b = 0; b < p.blocks; b += 4) {
         float4 x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < (RAW ? 0 : 4); ++i)
           x[i] = four_scales(p, p.x_scale + (int64_t)(t.row0 + min(lane + 32 * i, t.rows - 1)) * p.blocks, b);
         const float w = __ldg(ws + min(b + (lane & 3), p.blocks - 1));
         if (!warp_wait(sc_empty0 + 8 * at, ph, &g_gemm_error, abort_flag)) { stop = true; break; }
         float* slot = s_scale + at * kSlotFloats;
+        if (RAW) {
+          for (int q = lane >> 4; q < 4 && b + q < p.blocks; q += 2)
+            slot[q * kBlockFloats + (lane & 15)] = s_raw_scale[(b + q) * 16 + (lane & 15)];
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < (RAW ? 0 : 4); ++i) {
           slot[lane + 32 * i] = x[i].x;
           slot[kBlockFloats + lane + 32 * i] = x[i].y;
           slot[2 * kBlockFloats + lane + 32 * i] = x[i].z;
@@ -647,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
         if (++at == kScaleSlots) { at = 0; ph ^= 1; }
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     constexpr int kCols = NT / 2;             // of a warp
     const int quad = warp & 3, half = (warp - 4) >> 2, blocks = p.blocks;
@@ -658,7 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
                  smem_u32(s_scale + kRows), 0, 0};
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const Tile t = finder.find<NT>(p, tile);
-      const int rows = min(32, t.rows - quad * 32);   // of this warp
+      // this warp's rows, from .. rows of row0 on (RAW: lanes are rows of x, whatever tile they belong to)
+      const int from = RAW ? t.row0 : 0, rows = RAW ? (quad ? 0 : t.row0 + t.rows) : min(32, t.rows - quad * 32);
       const int ch0 = t.n0 + half * kCols;
       const bool there = rows > 0 && ch0 < p.channels;
       float2 acc[kCols / 2];
@@ -667,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
       if (there && blocks % 4 == 0) add_fours<kCols / 32, NT>(acc, sc, ring, taddr, blocks, abort_flag);
       else add_blocks<kCols / 32, NT>(acc, sc, ring, taddr, blocks, there, abort_flag);
       if (!there) continue;
-      const int64_t row0 = t.row0 + quad * 32;
+      const int64_t row0 = RAW ? 0 : t.row0 + quad * 32;
       constexpr int kUnits = kCols / 32;
       if (p.out_dtype == MOE_DTYPE_F32) {
 #pragma unroll
@@ -684,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
             }
             put_unit(turn + c * 2048, v);
           }
-          store_units<kUnits>(turn, &maps.out, p, row0, rows, ch0 + part * kCols / 2, 4);
+          store_units<kUnits>(turn, &maps.out, p, row0, from, rows, ch0 + part * kCols / 2, 4);
         }
       } else {
         if (elect()) store_wait_read();
@@ -698,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) block8_gemm_kernel(const __grid_c
                                                  : pack2<MOE_DTYPE_F16>(acc[16 * c + i].x, acc[16 * c + i].y);
           put_unit(turn + c * 2048, v);
         }
-        store_units<kUnits>(turn, &maps.out, p, row0, rows, ch0, 2);
+        store_units<kUnits>(turn, &maps.out, p, row0, from, rows, ch0, 2);
       }
     }
     if (elect()) store_wait();
@@ -739,12 +783,12 @@ cudaError_t encode_out(CUtensorMap* m, const GemmArgs& a, int size) {
 
 thread_local int t_withhold = 0;
 
-template <int NT>
+template <int NT, bool RAW>
 cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   Maps maps = {};
   cudaError_t e = encode(&maps.w, a.w, (int64_t)a.groups * a.channels, a.K, a.w_stride, NT);
   const int tail = (a.rows - 1) % kRows + 1;   // dense: rows of the last tile
-  for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+  for (int i = 0; i < 4 && e == cudaSuccess && !RAW; ++i) {
     const bool used = a.offsets ? i == 0 || a.rows > 8 << i : (i == 3 && a.rows > 64) || (tail <= 16 << i && (i == 0 || tail > 8 << i));
     if (used) e = encode(&maps.x[i], a.x, a.rows, a.K, a.x_stride, 16u << i);
   }
@@ -762,9 +806,14 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   p.blocks = (a.K + kBlock - 1) / kBlock;
   p.row_blocks = (a.channels + kBlock - 1) / kBlock;
   const int box = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 ? 64 : kRows;
-  p.a_bytes = box * kBlock;
+  p.a_bytes = RAW ? 0 : box * kBlock;
+  p.x = a.x;
+  p.x_dtype = a.x_dtype;
+  p.x_stride = a.x_stride;
+  p.K = a.K;
+  p.raw_bytes = RAW ? (p.blocks * (2048 + 64) + 1023) / 1024 * 1024 : 0;
   p.stage_bytes = p.a_bytes + NT * kBlock;
-  p.stages = kRingBytes<NT> / p.stage_bytes;
+  p.stages = (kRingBytes<NT> - p.raw_bytes) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.x_scale = a.x_scale;
   p.w_scale = a.w_scale;
@@ -773,7 +822,7 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   p.scales_wide = !((uintptr_t)a.x_scale & 15) && p.blocks % 4 == 0;
   p.early = a.early;
   p.withhold = t_withhold;
-  const size_t smem = (size_t)p.stages * p.stage_bytes + kTurnBytes<NT> + kFixedSmem;
+  const size_t smem = p.raw_bytes + (size_t)p.stages * p.stage_bytes + kTurnBytes<NT> + kFixedSmem;
   // at most one tile a group more than the rows fill
   int64_t tiles = (a.rows + kRows - 1) / kRows;
   if (a.offsets) tiles += a.groups < a.rows ? a.groups : a.rows;
@@ -785,7 +834,7 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !allowed[dev]) {
-    e = cudaFuncSetAttribute(block8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(block8_gemm_kernel<NT, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kRingBytes<NT> + kTurnBytes<NT> + kFixedSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed[dev] = true;
@@ -800,7 +849,7 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block8_gemm_kernel<NT>, maps, p);
+  return cudaLaunchKernelEx(&cfg, block8_gemm_kernel<NT, RAW>, maps, p);
 }
 
 }  // namespace
@@ -815,7 +864,9 @@ cudaError_t launch_gemm(const GemmArgs& a, int num_sms, cudaStream_t s) {
   // 76, 41, 118: with 128 sums a lane the registers are full, and loads from tensor memory wait for the sums before.)
   const int64_t groups = a.offsets ? (a.rows < a.groups ? a.rows : a.groups) : 1;
   const int64_t tm = a.offsets ? (a.rows / kRows > groups ? a.rows / kRows : groups) : (a.rows + kRows - 1) / kRows;
-  return tm * ((a.channels + 63) / 64) <= num_sms ? launch_tile<64>(a, num_sms, s) : launch_tile<128>(a, num_sms, s);
+  const bool narrow = tm * ((a.channels + 63) / 64) <= num_sms;
+  if (a.x_dtype != MOE_DTYPE_E4M3) return narrow ? launch_tile<64, true>(a, num_sms, s) : launch_tile<128, true>(a, num_sms, s);
+  return narrow ? launch_tile<64, false>(a, num_sms, s) : launch_tile<128, false>(a, num_sms, s);
 }
 
 cudaError_t gemm_status(cudaStream_t s, int* code) {

@@ -92,7 +92,8 @@ def _product(what, x, offsets, w, w_scale, x_scale, out_dtype):
     if K % 16 or K == 0:
         invalid(what, "K must be a multiple of 16")
     x, x_ptr, x_stride = rows16(x, K, what, "x")
-    need = 0 if quantized else _pad256(M * K) + _pad256(M * _blocks(K) * 4)
+    # few values are quantized inside the product
+    need = 0 if quantized or (M <= 16 and K <= 4096 and M * K <= 20480) else _pad256(M * K) + _pad256(M * _blocks(K) * 4)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     ws_ptr = None if ws is None else ws.data_ptr()
     scale_ptr = None if x_scale is None else x_scale.data_ptr()

@@ -258,6 +258,33 @@ def test_grouped_matmul_quantizes_other_rows(dtype):
     assert got.dtype is DT[dtype] and torch.equal(got, M.fp8_grouped_matmul(q, off, w, ws, s, DT[dtype]))
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("T,K,N", [(1, 16, 1), (1, 4096, 130), (2, 272, 77), (9, 144, 64), (15, 1040, 2000), (16, 1280, 260),
+                                   (5, 4096, 96), (16, 1296, 40), (1, 4112, 24), (17, 128, 96), (3, 512, 20000)])
+def test_few_rows_are_quantized_inside_the_product_to_the_same_bits(T, K, N, dtype):
+    import sparse_mixture_experts_gemv_gb300 as M
+    x, (w, ws) = _x(T, K + 8, dtype)[:, 8:], _w(N, K)
+    q, s = M.fp8_quantize(x)
+    for out in DT.values():
+        assert torch.equal(M.fp8_matmul(x, w, ws, out_dtype=out), M.fp8_matmul(q, w, ws, s, out))
+    want, mag = o.matmul(_np(q), _np(s), _np(w), _np(ws))
+    _near(M.fp8_matmul(x, w, ws, out_dtype=torch.float32), want, mag, K, "fp32")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("off", [[0, 3, 3, 8, 16], [2, 2, 5, 11, 12], [0, 16, 16, 16, 16], [0, 0, 0, 0, 1], [0, 0, 0, 0, 0], [7, 9, 3, 40, 12]])
+@pytest.mark.parametrize("K,N", [(272, 77), (512, 200)])
+def test_few_grouped_rows_likewise(off, K, N, dtype):
+    import sparse_mixture_experts_gemv_gb300 as M
+    x, (w, ws) = _x(16, K, dtype), _w(4, N, K)
+    x[1, 3] = float("inf")   # stays in its row, and out of the result where the row has no expert
+    q, s = M.fp8_quantize(x)
+    off = torch.tensor(off, dtype=torch.int32, device="cuda")
+    for out in DT.values():
+        a, b = M.fp8_grouped_matmul(x, off, w, ws, out_dtype=out), M.fp8_grouped_matmul(q, off, w, ws, s, out)
+        assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(0), b.nan_to_num(0))
+
+
 @pytest.mark.parametrize("N", [64, 77])
 def test_rows_of_no_expert_are_zeros(N):
     import sparse_mixture_experts_gemv_gb300 as M

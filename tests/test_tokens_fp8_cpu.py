@@ -105,8 +105,9 @@ def test_the_c_calls_refuse_bad_arguments_before_touching_the_device():
         return L.moe_block_matmul(x, dtype, xst, xs, w, wst, ws, y, od, T, n, K, sc, nb, None)
     assert [matmul(x=None), matmul(w=None), matmul(ws=None), matmul(y=None), matmul(xs=None), matmul(dtype=1),
             matmul(dtype=3), matmul(od=4), matmul(xst=48), matmul(wst=48), matmul(xst=72), matmul(x=far[0] + 8),
-            matmul(y=far[4] + 1), matmul(y=far[0]), matmul(y=far[2]), matmul(dtype=1, xs=None),
-            matmul(dtype=1, xs=None, sc=far[5], nb=511), matmul(dtype=1, xs=None, sc=far[5] + 16, nb=4096)] == [bad] * 18
+            matmul(y=far[4] + 1), matmul(y=far[0]), matmul(y=far[2]), matmul(T=20, dtype=1, xs=None),
+            matmul(T=20, dtype=1, xs=None, sc=far[5], nb=511),
+            matmul(T=20, dtype=1, xs=None, sc=far[5] + 16, nb=4096)] == [bad] * 18
     assert matmul(K=40) == out and matmul(T=0, x=None) == N.MOE_OK and matmul(n=0, x=None) == N.MOE_OK
 
     def grouped(off=far[5], E=4, M=4, n=8, K=64, y=far[4]):
@@ -116,7 +117,10 @@ def test_the_c_calls_refuse_bad_arguments_before_touching_the_device():
 
     b = ctypes.c_int64(7)
     assert L.moe_block_matmul_workspace(3, 144, 4, ctypes.byref(b)) == N.MOE_OK and b.value == 0
-    assert L.moe_block_matmul_workspace(3, 144, 1, ctypes.byref(b)) == N.MOE_OK and b.value == 512 + 256
+    assert L.moe_block_matmul_workspace(17, 144, 1, ctypes.byref(b)) == N.MOE_OK and b.value == 2560 + 256
+    assert L.moe_block_matmul_workspace(5, 4096, 1, ctypes.byref(b)) == N.MOE_OK and b.value == 0
+    assert L.moe_block_matmul_workspace(16, 1296, 1, ctypes.byref(b)) == N.MOE_OK and b.value == 20736 + 768
+    assert L.moe_block_matmul_workspace(1, 4112, 1, ctypes.byref(b)) == N.MOE_OK and b.value == 4352 + 256
     assert L.moe_block_matmul_workspace(3, 144, 3, ctypes.byref(b)) == bad
     assert L.moe_block_matmul_workspace(3, 144, 1, None) == bad
 
@@ -125,10 +129,11 @@ def test_the_python_calls_scratch_is_the_librarys():
     import ctypes
     from sparse_mixture_experts_gemv_gb300 import _native as N, fp8
     b = ctypes.c_int64()
-    for rows, K in ((1, 16), (3, 144), (333, 2560), (65536, 4096), (7, 65536)):
+    for rows, K in ((1, 16), (3, 144), (5, 4096), (6, 4096), (16, 1280), (17, 64), (1, 4112), (333, 2560), (65536, 4096), (7, 65536)):
         for code in (0, 1, 2):
             assert N.load().moe_block_matmul_workspace(rows, K, code, ctypes.byref(b)) == N.MOE_OK
-            assert b.value == fp8._pad256(rows * K) + fp8._pad256(rows * fp8._blocks(K) * 4)
+            inside = rows <= 16 and K <= 4096 and rows * K <= 20480
+            assert b.value == (0 if inside else fp8._pad256(rows * K) + fp8._pad256(rows * fp8._blocks(K) * 4))
 
 
 class Stand:
