@@ -590,8 +590,9 @@ moe_status_t moe_block_quantize(const void* x_dev, int32_t x_dtype, int64_t x_st
  * rounded once. Blocks are added up on the tensor cores in fp32, and their sums in fp32.
  * Rows of x and w start x_stride and w_stride elements apart. K, the strides in bytes and
  * the addresses of x and w are multiples of 16 (K else MOE_ERR_UNSUPPORTED); K <= MOE_BLOCK_MAX_K.
- * out overlaps neither x nor w. T or N of 0 is a no-op. workspace_dev: moe_block_matmul_workspace() bytes (0 for E4M3
- * rows, and for a few of other types, which the product quantizes itself), 256-byte aligned, free for reuse when the call's work on `stream` has finished.
+ * out overlaps neither x nor w. T or N of 0 is a no-op. workspace_dev: moe_block_matmul_workspace() bytes, 256-byte
+ * aligned, free for reuse when the call's work on `stream` has finished (0 bytes for E4M3 rows, and for a few rows of
+ * the other types, which the product quantizes itself).
  */
 moe_status_t moe_block_matmul_workspace(int32_t rows, int32_t K, int32_t x_dtype, int64_t* bytes);
 moe_status_t moe_block_matmul(const void* x_dev, int32_t x_dtype, int64_t x_stride, const float* x_scale_dev,
