@@ -19,6 +19,13 @@ def want(cond: bool, what: str, why: str):
         invalid(what, why)
 
 
+def counts32(what: str, *counts: int):
+    """Sizes that the C entry points take as 32-bit integers: a larger one would arrive as another number, and the
+    call would work on a part of its tensors without a word."""
+    if max(counts) >= 2 ** 31:
+        invalid(what, f"each size must be below 2^31, not {max(counts)}")
+
+
 def check(status: int, what: str):
     if status != N.MOE_OK:
         raise N.MoeError(status, what)

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _native as N
-from ._tensors import check, current_stream, elsewhere, invalid, refuse_gradients, rows16, run_on
+from ._tensors import check, counts32, current_stream, elsewhere, invalid, refuse_gradients, rows16, run_on
 
 FLOAT_CODES = {torch.float32: N.MOE_DTYPE_F32, torch.bfloat16: N.MOE_DTYPE_BF16, torch.float16: N.MOE_DTYPE_F16}
 ROW_CODES = {**FLOAT_CODES, torch.float8_e4m3fn: N.MOE_DTYPE_E4M3}
@@ -45,6 +45,7 @@ def fp8_quantize(x: torch.Tensor, swiglu: bool = False, stream: torch.cuda.Strea
         invalid(what, "x must be a CUDA tensor [T, K] (swiglu: [T, 2K]) of fp32, bf16 or fp16")
     T, width = x.shape
     K = width // 2 if swiglu else width
+    counts32(what, T, K)
     q = torch.empty((T, K), dtype=torch.float8_e4m3fn, device=x.device)
     scale = torch.empty((T, _blocks(K)), dtype=torch.float32, device=x.device)
     x, ptr, stride = rows16(x, width, what, "x")
@@ -66,6 +67,7 @@ def _product(what, x, offsets, w, w_scale, x_scale, out_dtype):
     if w.dtype is not torch.float8_e4m3fn or w.dim() != (2 if offsets is None else 3) or w.shape[-1] != K or w.device != dev:
         invalid(what, f"w must be float8_e4m3fn [{'N' if offsets is None else 'E, N'}, {K}] on {dev}")
     n = w.shape[-2]
+    counts32(what, M, n, K, *lead)
     if w_scale.shape != (*lead, _blocks(n), _blocks(K)) or w_scale.dtype is not torch.float32 or w_scale.device != dev:
         invalid(what, f"w_scale must be fp32 {[*lead, _blocks(n), _blocks(K)]} on {dev}")
     w_scale = w_scale.contiguous()

@@ -9,7 +9,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import check, current_stream, elsewhere, gradient, invalid, refuse_gradients, refuse_tangents, run_on
+from ._tensors import check, counts32, current_stream, elsewhere, gradient, invalid, refuse_gradients, refuse_tangents, run_on
 
 FLOAT_CODES = {torch.float32: N.MOE_DTYPE_F32, torch.bfloat16: N.MOE_DTYPE_BF16, torch.float16: N.MOE_DTYPE_F16}
 ROW_TYPES = {torch.float32, torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.int8, torch.uint8}
@@ -75,12 +75,13 @@ def _dispatch(x, idx, num_experts, x_scale):
         x_scale, scales = x_scale.contiguous(), x_scale.shape[1]
         if scales == 0:
             invalid(what, "x_scale must have a scale for each row")
+    counts32(what, T, k, scales)
+    need = _workspace(dev.index, T, k, num_experts)
     idx = idx.contiguous()
     rows = torch.empty((T * k, H), dtype=x.dtype, device=dev)
     row_scale = torch.empty((T * k, scales), dtype=torch.float32, device=dev) if scales else None
     offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
     pos = torch.empty((T, k), dtype=torch.int32, device=dev)
-    need = _workspace(dev.index, T, k, num_experts)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     status = N.load().moe_dispatch_tokens(x.data_ptr(), H * size, (stride if T > 1 else H) * size, _ptr(x_scale), scales,
                                           idx.data_ptr(), T, k, num_experts, rows.data_ptr(), _ptr(row_scale),
@@ -96,6 +97,7 @@ def _sum(y, pos, weights, what):
     weights = _weights(weights, pos, what)
     T, k = pos.shape
     H = y.shape[1]
+    counts32(what, T, k, H)
     out = torch.empty((T, H), dtype=y.dtype, device=y.device)
     if T == 0:
         return out
@@ -121,6 +123,7 @@ def _combine_gradients(d_out, y, weights, pos, want_y, want_weights):
     weights = _weights(weights, pos, what)
     T, k = pos.shape
     H, dev = y.shape[1], y.device
+    counts32(what, T, k, H)
     if d_out.shape != (T, H) or d_out.dtype is not y.dtype or d_out.device != dev:
         invalid(what, f"d_out must be {y.dtype} [{T}, {H}] on {dev}")
     d_out, _, d_stride = _matrix(d_out, what, "d_out")
