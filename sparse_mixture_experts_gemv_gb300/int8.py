@@ -8,7 +8,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import DTYPE_CODES, check, current_stream, elsewhere, invalid, refuse_gradients, run_on, vector, want
+from ._tensors import DTYPE_CODES, check, counts32, current_stream, elsewhere, invalid, refuse_gradients, run_on, vector, want
 
 
 @functools.lru_cache(maxsize=256)
@@ -61,6 +61,7 @@ def int8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale
     if w.dtype is not torch.int8 or w.dim() != 2 or w.shape[1] != K or w.device != dev:
         invalid(what, f"w must be int8 [N, {K}] on {dev}")
     n = w.shape[0]
+    counts32(what, T, n, K)
     w_scale = vector(w_scale, "w_scale", n, what, dev)
     quantized = code == N.MOE_DTYPE_S8
     if quantized != (x_scale is not None):
@@ -118,6 +119,7 @@ def int8_experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, gate
     E, I = gate_up.shape[0], gate_up.shape[1] // 2
     if E == 0 or I == 0:
         invalid(what, "there must be an expert and an intermediate feature")
+    counts32(what, T, k, E, H, I)
     if down.shape != (E, H, I) or down.dtype is not torch.int8:
         invalid(what, f"down must be int8 [{E}, {H}, {I}]")
     if gate_up_scale.shape != (E, 2 * I) or gate_up_scale.dtype is not torch.float32:

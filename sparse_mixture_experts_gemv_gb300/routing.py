@@ -9,7 +9,7 @@ import functools
 import torch
 
 from . import _native as N
-from ._tensors import DTYPE_CODES, check, current_stream, elsewhere, invalid, refuse_tangents, run_on, vector, want
+from ._tensors import DTYPE_CODES, check, counts32, current_stream, elsewhere, invalid, refuse_tangents, run_on, vector, want
 
 LOGIT_CODES = {t: c for t, c in DTYPE_CODES.items() if t is not torch.int8}
 SCORES = {"softmax": N.MOE_SCORE_SOFTMAX, "sigmoid": N.MOE_SCORE_SIGMOID}
@@ -35,6 +35,7 @@ def _logits(what, logits):
     if code is None or not logits.is_cuda or logits.dim() != 2:
         invalid(what, "logits must be a CUDA tensor [T, E] of fp32, bf16 or fp16")
     T, E = logits.shape
+    counts32(what, T, E)
     stride, inner = logits.stride()
     if inner != 1 or stride < E:
         logits, stride = logits.contiguous(), E

@@ -95,3 +95,26 @@ def test_numbers_of_choices_that_are_not_supported_are_refused_before_the_rows_a
     for T, k in ((2 ** 30, 1), (3, 33)):
         with pytest.raises(M.MoeError):
             _dispatch(M, T, k)
+
+
+def _int8_matmul(M, T, K, N):
+    return M.int8_matmul(Sized((T, K), torch.int8), Sized((N, K), torch.int8), Sized((N,)), Sized((T,)))
+
+
+def _int8_experts(M, T, k, E, H, I):
+    return M.int8_experts(Sized((T, H), torch.bfloat16), Sized((T, k), I32), Sized((T, k)), Sized((E, 2 * I, H), torch.int8),
+                          Sized((E, 2 * I)), Sized((E, H, I), torch.int8), Sized((E, H)))
+
+
+EARLIER = [lambda M: _int8_matmul(M, FAR, 16, 1), lambda M: _int8_matmul(M, 1, 2 ** 32 + 16, 1), lambda M: _int8_matmul(M, 1, 16, FAR),
+           lambda M: _int8_experts(M, FAR, 1, 2, 16, 16), lambda M: _int8_experts(M, 1, FAR, 2, 16, 16),
+           lambda M: _int8_experts(M, 1, 1, FAR, 16, 16), lambda M: _int8_experts(M, 1, 1, 2, 2 ** 32 + 16, 16),
+           lambda M: _int8_experts(M, 1, 1, 2, 16, 2 ** 32 + 16),
+           lambda M: M.route_experts(Sized((FAR, 2)), 1), lambda M: M.route_experts(Sized((1, FAR)), 1),
+           lambda M: M.route_experts_backward(Sized((FAR, 1)), Sized((FAR, 2)), Sized((FAR, 1), I32)),
+           lambda M: M.route_experts_backward(Sized((1, 1)), Sized((1, FAR)), Sized((1, 1), I32))]
+
+
+@pytest.mark.parametrize("call", EARLIER)
+def test_sizes_past_32_bits_are_refused_by_the_other_tensor_calls(call, monkeypatch):
+    test_sizes_past_32_bits_are_refused(call, monkeypatch)
