@@ -57,7 +57,7 @@ def fp8_quantize(x: torch.Tensor, swiglu: bool = False, stream: torch.cuda.Strea
 
 
 def _product(what, x, offsets, w, w_scale, x_scale, out_dtype):
-    refuse_gradients(what, x, w_scale, x_scale)
+    refuse_gradients(what, x, w, w_scale, x_scale)
     code = ROW_CODES.get(x.dtype)
     if code is None or not x.is_cuda or x.dim() != 2:
         invalid(what, "x must be a CUDA tensor [rows, K] of float8_e4m3fn, bf16, fp16 or fp32")

@@ -243,3 +243,23 @@ def test_tensors_of_the_host_are_refused():
                  lambda: M.fp8_grouped_matmul(x, None, x, x)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_weights_that_would_lose_a_gradient_or_a_tangent_are_refused():
+    """A parameter of float8_e4m3fn requires a gradient unless it is told not to."""
+    import sparse_mixture_experts_gemv_gb300 as M
+    from torch.autograd import forward_ad
+    x, idx = torch.ones(2, 16), torch.zeros(2, 1, dtype=torch.int32)
+    w = torch.nn.Parameter(torch.ones(2, 16).to(torch.float8_e4m3fn))
+    assert w.requires_grad
+    calls = (lambda w: M.fp8_matmul(x, w, x), lambda w: M.fp8_matmul(x, w, x, x), lambda w: M.fp8_grouped_matmul(x, idx, w, x))
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call(w)
+        with torch.no_grad(), pytest.raises(ValueError, match="must be"):   # goes on to the other checks
+            call(w)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(w.detach(), w.detach())
+        for call in calls:
+            with pytest.raises(ValueError, match="tangent"):
+                call(dual)
