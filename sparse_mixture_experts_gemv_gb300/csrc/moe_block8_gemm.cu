@@ -440,7 +440,7 @@ MOE_DEV void copy_unit(const uint8_t* unit, const Params& p, int64_t row0, int f
   const int lane = threadIdx.x & 31;
   const int64_t ld = (int64_t)p.channels * size;
   uint8_t* out = static_cast<uint8_t*>(p.out) + row0 * ld + (int64_t)ch0 * size;
-  const int n = min(64, (p.channels - ch0) * size);   // bytes of a row that there are
+  const int n = min(64 / size, p.channels - ch0) * size;   // bytes of a row that there are (all channels' pass 31 bits)
   if (p.wide) {
     const int c = lane & 3;
 #pragma unroll
