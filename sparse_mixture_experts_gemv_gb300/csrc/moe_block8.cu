@@ -28,8 +28,8 @@ struct QuantizeParams {
 constexpr int kThreads = 256;
 
 // g / (1 + e^-g) * u. The quotient is the product with the approximate reciprocal, corrected once by the remainder (one
-// step of Newton's): off by little more than its rounding. Below -80, where the reciprocal leaves the normal
-// range, it is the division.
+// step of Newton's; its sign as in divide(), for gates of -0): off by little more than its rounding. Below -80, where the
+// reciprocal leaves the normal range, it is the division.
 MOE_DEV void silu_mul(float (&g)[16], const float (&u)[16]) {
   float least = g[0];
 #pragma unroll
@@ -41,7 +41,7 @@ MOE_DEV void silu_mul(float (&g)[16], const float (&u)[16]) {
       float y;
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
       const float q = g[i] * y;
-      g[i] = fmaf(fmaf(-q, d, g[i]), y, q) * u[i];
+      g[i] = fmaf(-fmaf(q, d, -g[i]), y, q) * u[i];
     }
   } else {
 #pragma unroll

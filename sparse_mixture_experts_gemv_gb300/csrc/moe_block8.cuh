@@ -15,15 +15,16 @@ namespace block8 {
 // rounded reciprocal is off by two steps at most, one correction by its exact remainder by less than one, and from
 // there a second one is the rounded quotient (Markstein, IBM Journal of Research and Development 34, 1990). Remainders
 // are exact while nothing leaves the normal range: scales beyond 2^+-90 (or NaN) take the division. Values below 2^-10
-// of the scale, whose remainder may, are 0 in E4M3 either way.
+// of the scale, whose remainder may, are 0 in E4M3 either way. The remainder is q scale - v, and its
+// correction taken off: where it is 0, that adds -0, and a quotient of -0 stays one.
 MOE_DEV void divide(float (&v)[16], float scale) {
   if (scale >= 0x1p-90f && scale <= 0x1p90f) {
     const float inv = 1.f / scale;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float q = v[i] * inv;
-      q = fmaf(fmaf(-q, scale, v[i]), inv, q);
-      v[i] = fmaf(fmaf(-q, scale, v[i]), inv, q);
+      q = fmaf(-fmaf(q, scale, -v[i]), inv, q);
+      v[i] = fmaf(-fmaf(q, scale, -v[i]), inv, q);
     }
   } else {
 #pragma unroll
