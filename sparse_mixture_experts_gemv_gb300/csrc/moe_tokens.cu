@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kMaxThreads) combine_kernel(const CombineParam
   __syncthreads();
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
     fetch(p, t + gridDim.x, at, w);
-    for (int c = threadIdx.x * N; c < p.H; c += blockDim.x * N) {
+    for (uint32_t c = threadIdx.x * N; c < (uint32_t)p.H; c += blockDim.x * N) {   // past 2^31 behind the last
       float acc[N] = {};
       for (int j0 = 0; j0 < p.k; j0 += kTogether) {
         Pack<DT, N> v[kTogether];
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) combine_backward_kernel(const 
     fetch(p, t + gridDim.x, next_at, next_w);
     for (int j0 = 0; j0 < p.k; j0 += kTogether, side ^= 1) {
       float dot[kTogether] = {};
-      for (int c = threadIdx.x * N; c < p.H; c += blockDim.x * N) {
+      for (uint32_t c = threadIdx.x * N; c < (uint32_t)p.H; c += blockDim.x * N) {   // past 2^31 behind the last
         Pack<DT, N> d, v[kTogether];
         d.load(p.d_out, t * p.d_stride + c);
         if (p.d_weights) {
@@ -507,8 +507,8 @@ cudaError_t launch_dispatch(const DispatchParams& p, int sms, cudaStream_t s) {
 template <int DT, int N>
 cudaError_t launch_combine(const CombineParams& p, bool backward, int sms, cudaStream_t s) {
   // as many rounds as kMaxThreads take, each with the same threads
-  const int vectors = (p.H + N - 1) / N, rounds = (vectors + kMaxThreads - 1) / kMaxThreads;
-  const int threads = ((vectors + rounds - 1) / rounds + 31) / 32 * 32;
+  const int64_t vectors = ((int64_t)p.H + N - 1) / N, rounds = (vectors + kMaxThreads - 1) / kMaxThreads;
+  const int threads = (int)((vectors + rounds - 1) / rounds + 31) / 32 * 32;
   const int64_t most = (int64_t)sms * 2048 / threads, grid = p.T < most ? p.T : most;
   return backward ? launch(combine_backward_kernel<DT, N>, grid, threads, s, p)
                   : launch(combine_kernel<DT, N>, grid, threads, s, p);
