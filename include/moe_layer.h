@@ -534,9 +534,9 @@ void moe_quant_test_force_wait_timeout(int32_t on);
  * x_scale_dev fp32 [T, scales] the scales go the same way to row_scale_dev
  * [T k, scales] (scales 0 and NULL: none). x and rows, idx and pos do not overlap. T == 0
  * writes offsets of 0. E <= MOE_DISPATCH_MAX_EXPERTS, k <= MOE_ROUTE_MAX_TOP_K,
- * T * k < 2^30. workspace_dev: moe_dispatch_tokens_workspace() bytes (0 for few choices; it goes by the current
- * device's SMs), 256-byte aligned, free for reuse when the call's work on `stream` has finished. Errors:
- * MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ * T * k < 2^30, row_bytes and a row's 4 * scales below 2^30. workspace_dev:
+ * moe_dispatch_tokens_workspace() bytes (0 for few choices; it goes by the current device's SMs), 256-byte aligned,
+ * free for reuse when the call's work on `stream` has finished. Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
  */
 #define MOE_DISPATCH_MAX_EXPERTS 1024
 moe_status_t moe_dispatch_tokens_workspace(int32_t T, int32_t k, int32_t E, int64_t* bytes);

@@ -563,7 +563,7 @@ moe_status_t moe_dispatch_tokens(const void* x_dev, int64_t row_bytes, int64_t r
   if (!in_range(T, k, row_bytes, &st)) return st;
   if (E < 1 || scales < 0 || (T && ((scales > 0) != (x_scale_dev != nullptr) || (scales > 0) != (row_scale_dev != nullptr))))
     return MOE_ERR_INVALID_ARG;
-  if (E > MOE_DISPATCH_MAX_EXPERTS || row_bytes > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  if (E > MOE_DISPATCH_MAX_EXPERTS || row_bytes > INT32_MAX / 2 || scales > INT32_MAX / 8) return MOE_ERR_UNSUPPORTED;
   if (!offsets_dev || (T && (!x_dev || !idx_dev || !rows_dev || !pos_dev || row_stride < row_bytes))) return MOE_ERR_INVALID_ARG;
   if (((uintptr_t)idx_dev | (uintptr_t)offsets_dev | (uintptr_t)pos_dev | (uintptr_t)x_scale_dev | (uintptr_t)row_scale_dev) & 3)
     return MOE_ERR_INVALID_ARG;

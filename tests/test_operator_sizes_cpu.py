@@ -118,3 +118,14 @@ EARLIER = [lambda M: _int8_matmul(M, FAR, 16, 1), lambda M: _int8_matmul(M, 1, 2
 @pytest.mark.parametrize("call", EARLIER)
 def test_sizes_past_32_bits_are_refused_by_the_other_tensor_calls(call, monkeypatch):
     test_sizes_past_32_bits_are_refused(call, monkeypatch)
+
+
+def test_dispatch_refuses_rows_and_scales_past_a_gigabyte():
+    """In the library, before anything reaches a device: a row's bytes, and its scales' likewise."""
+    from sparse_mixture_experts_gemv_gb300 import _native as N
+    far = [0x10000 + (i << 40) for i in range(8)]   # never read
+
+    def dispatch(row, scales):
+        return N.load().moe_dispatch_tokens(far[0], row, row, far[1] if scales else None, scales, far[2], 1, 1, 4, far[3],
+                                            far[4] if scales else None, far[5], far[6], None, 0, None)
+    assert [dispatch(2 ** 30, 0), dispatch(2 ** 31, 0), dispatch(16, 2 ** 28), dispatch(16, 2 ** 31 - 1)] == [N.MOE_ERR_UNSUPPORTED] * 4
