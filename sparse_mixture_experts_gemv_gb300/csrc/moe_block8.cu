@@ -116,7 +116,7 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 }
 int size_of(int dtype) { return dtype == MOE_DTYPE_E4M3 ? 1 : dtype == MOE_DTYPE_F32 ? 4 : 2; }
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
-int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
+int blocks_of(int n) { return tiles_of(n, kBlock); }
 bool is_float(int dtype) { return dtype >= MOE_DTYPE_F32 && dtype <= MOE_DTYPE_F16; }
 
 // Rows that come in another type are quantized to scratch: values, then scales. Few rows are quantized inside the product.
@@ -142,7 +142,7 @@ moe_status_t product(const void* x, int x_dtype, int64_t x_stride, const float* 
   if (x_stride < g.K || g.w_stride < g.K || x_stride * xs % 16 || g.w_stride % 16) return MOE_ERR_INVALID_ARG;
   // a tensor map's strides have 40 bits, its extents 32; tiles are counted in 31
   if (x_stride * xs >= (int64_t)1 << 40 || g.w_stride >= (int64_t)1 << 40 || w_rows >= INT32_MAX ||
-      ((int64_t)(g.rows + 127) / 128 + g.groups) * ((g.channels + 63) / 64) >= INT32_MAX)
+      ((int64_t)tiles_of(g.rows, 128) + g.groups) * tiles_of(g.channels, 64) >= INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (overlap(x, ((g.rows - 1) * x_stride + g.K) * xs, g.out, out_bytes) ||
       overlap(g.w, (w_rows - 1) * g.w_stride + g.K, g.out, out_bytes))

@@ -8,6 +8,7 @@ namespace moe {
 namespace block8 {
 
 constexpr int kBlock = 128;   // values of a scale
+constexpr int tiles_of(int n, int tile) { return (int)(((uint32_t)n + (uint32_t)tile - 1) / (uint32_t)tile); }   // any n >= 0
 
 // Whether the product quantizes rows of other types itself, each CTA for itself: few values, which it keeps as an operand
 // of 16 rows in shared memory. That saves a launch, some 5 us of a call, and takes 4 us for 32,768 values. GB300, us on the

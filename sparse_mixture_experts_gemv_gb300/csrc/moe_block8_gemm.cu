@@ -117,7 +117,7 @@ struct Finder {
       if (past != 0xFFFFFFFFu) break;
     }
     Tile t;
-    const int rows = row[e + 1] - row[e], tm = (rows + kRows - 1) / kRows, in = tile - first[e];
+    const int rows = row[e + 1] - row[e], tm = tiles_of(rows, kRows), in = tile - first[e];
     t.e = e;
     t.n0 = in / tm * NT;
     t.row0 = row[e] + in % tm * kRows;
@@ -144,7 +144,7 @@ MOE_DEV void make_tables(const Params& p, int* first, int* row, int* scratch) {
       row[0] = 0;
       row[1] = p.rows;
       first[0] = 0;
-      first[1] = (p.rows + kRows - 1) / kRows * p.tiles_n;
+      first[1] = tiles_of(p.rows, kRows) * p.tiles_n;
     }
     __syncthreads();
     return;
@@ -177,7 +177,7 @@ MOE_DEV void make_tables(const Params& p, int* first, int* row, int* scratch) {
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     const int e = i * kPer + q;
-    tiles[q] = e < p.groups ? (row[e + 1] - row[e] + kRows - 1) / kRows * p.tiles_n : 0;
+    tiles[q] = e < p.groups ? tiles_of(row[e + 1] - row[e], kRows) * p.tiles_n : 0;
     sum += tiles[q];
   }
   upto = sum;
@@ -802,9 +802,9 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   p.rows = a.rows;
   p.channels = a.channels;
   p.groups = a.groups;
-  p.tiles_n = (a.channels + NT - 1) / NT;
-  p.blocks = (a.K + kBlock - 1) / kBlock;
-  p.row_blocks = (a.channels + kBlock - 1) / kBlock;
+  p.tiles_n = tiles_of(a.channels, NT);
+  p.blocks = tiles_of(a.K, kBlock);
+  p.row_blocks = tiles_of(a.channels, kBlock);
   const int box = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 ? 64 : kRows;
   p.a_bytes = RAW ? 0 : box * kBlock;
   p.x = a.x;
@@ -824,7 +824,7 @@ cudaError_t launch_tile(const GemmArgs& a, int num_sms, cudaStream_t s) {
   p.withhold = t_withhold;
   const size_t smem = p.raw_bytes + (size_t)p.stages * p.stage_bytes + kTurnBytes<NT> + kFixedSmem;
   // at most one tile a group more than the rows fill
-  int64_t tiles = (a.rows + kRows - 1) / kRows;
+  int64_t tiles = tiles_of(a.rows, kRows);
   if (a.offsets) tiles += a.groups < a.rows ? a.groups : a.rows;
   tiles *= p.tiles_n;
   const int grid = (int)(tiles < num_sms ? tiles : num_sms);
@@ -863,8 +863,8 @@ cudaError_t launch_gemm(const GemmArgs& a, int num_sms, cudaStream_t s) {
   // 36 / 49; 32,768 rows of 256 experts, 2,048 x 1,024 113 / 138. (256 channels, before the epilogue's last steps: 16, 33,
   // 76, 41, 118: with 128 sums a lane the registers are full, and loads from tensor memory wait for the sums before.)
   const int64_t groups = a.offsets ? (a.rows < a.groups ? a.rows : a.groups) : 1;
-  const int64_t tm = a.offsets ? (a.rows / kRows > groups ? a.rows / kRows : groups) : (a.rows + kRows - 1) / kRows;
-  const bool narrow = tm * ((a.channels + 63) / 64) <= num_sms;
+  const int64_t tm = a.offsets ? (a.rows / kRows > groups ? a.rows / kRows : groups) : tiles_of(a.rows, kRows);
+  const bool narrow = tm * tiles_of(a.channels, 64) <= num_sms;
   if (a.x_dtype != MOE_DTYPE_E4M3) return narrow ? launch_tile<64, true>(a, num_sms, s) : launch_tile<128, true>(a, num_sms, s);
   return narrow ? launch_tile<64, false>(a, num_sms, s) : launch_tile<128, false>(a, num_sms, s);
 }

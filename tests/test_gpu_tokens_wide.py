@@ -6,6 +6,13 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 
+@pytest.fixture(autouse=True)
+def _memory_goes_back():
+    """Tens of gigabytes, which the allocator would keep from what allocates without it."""
+    yield
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("dtype,H", [(torch.bfloat16, 2 ** 31 - 8), (torch.float32, 2 ** 31 - 4)])
 def test_combine_and_its_gradients(dtype, H):
     """Whole numbers of few bits: results are exact, the dot product too (its terms are 0 but for a thousand of them)."""
