@@ -518,8 +518,9 @@ void moe_quant_test_force_wait_timeout(int32_t on);
 /* ------------------------------------------------------------------------
  * Tokens in the order of their experts and back, and products in 8-bit floating point
  * with a scale for each block of 128. As above: no state, every buffer is the caller's,
- * nothing allocates or synchronises. (The pages name no such interface; it is this
- * library's own.)
+ * nothing allocates or synchronises. What a call writes, its workspace included, overlaps
+ * no other buffer of the call (rows and results are checked, where it says so below). (The
+ * pages name no such interface; it is this library's own.)
  * ------------------------------------------------------------------------ */
 
 /*
@@ -587,9 +588,11 @@ moe_status_t moe_block_quantize(const void* x_dev, int32_t x_dtype, int64_t x_st
  * x_dev [T, K]: E4M3 with x_scale_dev fp32 [T, ceil(K / 128)], or BF16 / F16 / F32 with
  * x_scale_dev NULL, which the call quantizes as moe_block_quantize does. w_dev E4M3 [N, K],
  * w_scale_dev fp32 [ceil(N / 128), ceil(K / 128)]; out_dev [T, N] BF16, F16 or F32 without gaps,
- * rounded once. Blocks are added up on the tensor cores in fp32, and their sums in fp32.
+ * rounded once. Blocks are added up on the tensor cores in fp32, and their sums in fp32, each times the product of
+ * its two scales, which is rounded to fp32 first: below 2^-126 it loses bits, past 2^128 it is infinite.
  * Rows of x and w start x_stride and w_stride elements apart. K, the strides in bytes and
- * the addresses of x and w are multiples of 16 (K else MOE_ERR_UNSUPPORTED); K <= MOE_BLOCK_MAX_K.
+ * the addresses of x and w are multiples of 16 (K else MOE_ERR_UNSUPPORTED); K <= MOE_BLOCK_MAX_K, rows of w (of all
+ * experts) below 2^31 - 1, strides below 2^40 bytes.
  * out overlaps neither x nor w. T or N of 0 is a no-op. workspace_dev: moe_block_matmul_workspace() bytes, 256-byte
  * aligned, free for reuse when the call's work on `stream` has finished (0 bytes for E4M3 rows, and for a few rows of
  * the other types, which the product quantizes itself).

@@ -218,8 +218,13 @@ __global__ void __launch_bounds__(kThreads) dispatch_count_kernel(const Dispatch
 }
 
 // Then every CTA adds up all chunks' numbers and those before its own, eight experts a load, places its chunk and copies
-// its rows. Up to kCountedChoices it counts them all for itself, four a load, which takes it some 3 us, a launch of the
-// counts 5. 4,096 tokens of 2,048 bytes, k = 8: 20 us; 8,191 of 5,120 bytes, k = 8: 69 us with the counts before it, 5.5 TB/s.
+// its rows. Up to kCountedChoices it counts them all for itself, four a load, which takes time with the choices, where a
+// launch of the counts takes it with chunks and experts. 2,048 bytes a row, k = 8, us on the device (in a graph), by itself
+// / by a launch, of 64, 256 and 1,024 experts: 8,192 choices 6.4 / 10.0, 6.6 / 10.4, 6.8 / 13.7; 32,768 14.1 / 16.8,
+// 14.8 / 17.1, 15.1 / 20.4; 40,000 17.7 / 19.7, 18.2 / 20.0, 18.6 / 23.4; 65,536 33.7 / 34.4, 34.7 / 34.6, 35.0 / 37.9;
+// 131,072 65 / 62, 66 / 62, 68 / 65. They cross at 65,536 choices and later with many experts, and from 32,768 up to there
+// counting by itself would gain up to 2 us, 5 with 1,024 experts: the limit, past which callers bring a workspace, is below
+// the crossing for every number of experts. 8,191 tokens of 5,120 bytes, k = 8: 69 us with the counts before it, 5.5 TB/s.
 template <class V>
 __global__ void __launch_bounds__(kThreads, 1) dispatch_chunk_kernel(const DispatchParams p) {
   __shared__ PlanShared<kThreads> s;
@@ -396,7 +401,7 @@ __global__ void __launch_bounds__(kMaxThreads) combine_kernel(const CombineParam
 
 // d_y[pos] = w d_out[t] and d_w = <d_out[t], y[pos]>, eight choices at a time: each thread adds up its columns, then
 // the CTA adds the threads' sums, in a fixed order. 8,191 tokens of 2,048 bf16, k = 8: 87 us, 6.4 TB/s (80 registers a
-// thread instead of 64, three CTAs an SM: 97).
+// thread instead of 64, three CTAs an SM: 97; in 64 registers the 16-byte-wide kernels spill 12 bytes a thread).
 template <int DT, int N>
 __global__ void __launch_bounds__(kMaxThreads, 4) combine_backward_kernel(const CombineParams p) {
   __shared__ Choices s;

@@ -117,7 +117,7 @@ def fp8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale:
     """out[t, n] = sum_b x_scale[t, b] w_scale[n // 128, b] (sum over block b of x[t, k] w[n, k]).
 
     w: float8_e4m3fn [N, K], w_scale: fp32 [ceil(N / 128), ceil(K / 128)], a scale for each 128 x 128
-    of w. x [T, K]: float8_e4m3fn with x_scale fp32 [T, ceil(K / 128)], or bf16, fp16 or fp32 without: it
+    of w; the product of a block's two scales is held in 32 bits. x [T, K]: float8_e4m3fn with x_scale fp32 [T, ceil(K / 128)], or bf16, fp16 or fp32 without: it
     is then quantized by the call as fp8_quantize does. K is a multiple of 16. Rows may be apart (any
     stride(0)); rows off 16-byte boundaries are copied first. out_dtype: bf16, fp16 or fp32; by
     default x's, and bf16 for float8_e4m3fn x. There is no gradient: inputs that require one are refused
